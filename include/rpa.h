@@ -1,7 +1,7 @@
 /*
  * rpa.h -- C ABI of the GB300 (sm_103a) ragged paged attention library.
  *
- * Four operations, each one asynchronous call on a caller-supplied CUDA stream:
+ * The operations, each one asynchronous call on a caller-supplied CUDA stream:
  *
  *   rpa_forward          ragged paged attention over a packed prefill+decode batch
  *                        (tpu-inference "ragged_paged_attention/v2/kernel.py",
@@ -16,6 +16,11 @@
  *   sparse_mla_forward   DSA sparse MLA over selected units of a paged latent cache
  *                        (sglang-jax "dsa/sparse_mla_prefill.py", sparse_mla_attention and
  *                        _sparse_mla_kernel_chunked_hminor).
+ *   rope_apply           rotary positions on packed queries and keys.
+ *   rpa_rope_update_kv_cache
+ *                        rpa_update_kv_cache with the rotation, and the rounding to the
+ *                        cache's type, on the way; rpa_rope_forward_update attends in the
+ *                        same call.
  *
  * Conventions shared by every entry point
  *   - Every tensor argument is a DEVICE pointer owned by the caller; the library
@@ -215,6 +220,119 @@ RPA_API int rpa_forward_update(const rpa_params* p, const void* q, const void* n
                                void* kv_pages, const int32_t* kv_lens, const int32_t* page_indices,
                                const int32_t* cu_q_lens, const int32_t* num_seqs, void* out, void* workspace,
                                size_t workspace_bytes, rpa_stream_t stream);
+
+/* ---------------------------------------------------------------------- */
+/* Rotary positions                                                         */
+/* ---------------------------------------------------------------------- */
+
+/* Pair i of a head's first rotary_dim elements turns by the angle position * f_i:
+ *   (x, y) -> amplitude * (x cos - y sin, y cos + x sin),
+ * where f_i = base^(-2i / rotary_dim), changed by `scaling`; elements past rotary_dim stay as
+ * they are.  pairing names the pair's two elements. */
+#define RPA_ROPE_HALF        0   /* i and i + rotary_dim / 2 */
+#define RPA_ROPE_INTERLEAVED 1   /* 2i and 2i + 1 */
+
+#define RPA_ROPE_SCALE_NONE   0
+#define RPA_ROPE_SCALE_LINEAR 1  /* f_i / factor */
+#define RPA_ROPE_SCALE_NTK    2  /* base * factor^(rotary_dim / (rotary_dim - 2)) for base (rotary_dim > 2) */
+/* With n_i = original_max_position * f_i / (2 pi), the turns of pair i over the original context:
+ * f_i where n_i >= high_freq_factor, f_i / factor where n_i <= low_freq_factor, between them
+ * linear in n_i. */
+#define RPA_ROPE_SCALE_LLAMA3 3
+/* f_i for the pairs below `low`, f_i / factor from `high` on, between them linear in i, with
+ * low = max(floor(c(beta_fast)), 0), high = min(ceil(c(beta_slow)), rotary_dim - 1) and
+ * c(n) = rotary_dim * ln(original_max_position / (2 pi n)) / (2 ln base). */
+#define RPA_ROPE_SCALE_YARN   4
+
+#define RPA_ROPE_MAX_DIM 256
+
+typedef struct {
+    uint32_t struct_size;        /* sizeof(rope_params) */
+    uint32_t version;            /* RPA_ABI_VERSION */
+    int32_t rotary_dim;          /* even, 0 to RPA_ROPE_MAX_DIM; 0 turns nothing */
+    int32_t pairing;             /* RPA_ROPE_HALF or RPA_ROPE_INTERLEAVED */
+    int32_t scaling;             /* RPA_ROPE_SCALE_* */
+    int32_t original_max_position;  /* LLAMA3 and YARN */
+    double base;                 /* > 1 */
+    double factor;               /* >= 1; every scaling but NONE */
+    double low_freq_factor;      /* LLAMA3: 0 < low_freq_factor < high_freq_factor */
+    double high_freq_factor;
+    double beta_fast;            /* YARN: beta_fast > beta_slow > 0 */
+    double beta_slow;
+    double attention_factor;     /* the amplitude; 0 = 1, for YARN 0.1 ln(factor) + 1 */
+} rope_params;
+
+/* What the calls below take: a plain host value that rope_table_init fills once and the caller
+ * keeps.  step[i] is f_i / (2 pi), pair i's turn per position, as a fraction of 2^64: the kernels
+ * multiply it by the position modulo 2^64, which leaves the fraction of a turn exactly, however
+ * far the position, and take the sine and cosine of that in float32.  A caller with frequencies
+ * of its own fills the table itself. */
+typedef struct {
+    uint32_t struct_size;        /* sizeof(rope_table) */
+    uint32_t version;            /* RPA_ABI_VERSION */
+    int32_t rotary_dim;
+    int32_t pairing;
+    float amplitude;             /* finite */
+    uint32_t reserved;           /* 0 */
+    uint64_t step[RPA_ROPE_MAX_DIM / 2];  /* rotary_dim / 2 are used */
+} rope_table;
+
+/* Fills *t from *p on the host (no GPU is needed). */
+RPA_API int rope_table_init(const rope_params* p, rope_table* t);
+
+/* Strides count elements; 0 stands for the dense layout [num_tokens, heads, head_dim]'s.  Each is
+ * a multiple of 8, 0 to 2^30; a row's head_dim elements are adjacent.  Rows of an output
+ * must not overlap: tokens outside heads (token stride >= (heads - 1) * head stride + head_dim) or
+ * heads outside tokens. */
+typedef struct {
+    uint32_t struct_size;        /* sizeof(rope_apply_params) */
+    uint32_t version;            /* RPA_ABI_VERSION */
+    int32_t num_tokens;          /* >= 0 */
+    int32_t num_q_heads;
+    int32_t num_k_heads;         /* 0 with k and k_out NULL */
+    int32_t head_dim;            /* multiple of 16, up to 512, >= the table's rotary_dim */
+    int32_t inverse;             /* 1: the transposed map, by the opposite angle (with amplitude 1 the
+                                    inverse; it takes an output's gradient to the input's) */
+    int32_t reserved;            /* 0 */
+    int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride;
+    int64_t q_out_token_stride, q_out_head_stride, k_out_token_stride, k_out_head_stride;
+} rope_apply_params;
+
+/* q [num_tokens, num_q_heads, head_dim] and k [num_tokens, num_k_heads, head_dim], bf16, turned by
+ * positions int32 [num_tokens] (any value, negative ones too) into q_out and k_out, bf16: computed
+ * in float32, rounded once.  q_out may be q and k_out may be k (with the same strides); otherwise
+ * outputs overlap neither inputs nor each other. */
+RPA_API int rope_apply(const rope_apply_params* p, const rope_table* t, const void* q, const void* k,
+                       const int32_t* positions, void* q_out, void* k_out, rpa_stream_t stream);
+
+/* Token and head strides of q, new_k and new_v, as in rope_apply_params (slices of one projection's
+ * output, say); NULL in place of the struct, or 0 in a field, stands for the dense layout. */
+typedef struct {
+    uint32_t struct_size;        /* sizeof(rope_strides) */
+    uint32_t version;            /* RPA_ABI_VERSION */
+    int64_t q_token, q_head, k_token, k_head, v_token, v_head;
+} rope_strides;
+
+/* rpa_update_kv_cache with what precedes it: new_k turned to its position, both rounded to the
+ * cache's type, and the queries turned beside them.
+ *   q             [max_num_tokens, num_q_heads, head_dim] bf16, or NULL with q_out NULL: no queries
+ *   new_k, new_v  [max_num_tokens, num_combined_kv_heads / 2, head_dim] bf16, whatever kv_dtype is
+ *   positions     int32 [max_num_tokens], or NULL: the position of the token's slot,
+ *                 kv_len - q_len + j (the slot is that one either way)
+ *   q_out         [max_num_tokens, num_q_heads, head_dim] bf16, dense; may be q if q is dense
+ * The cache gets x / k_scale (x / v_scale; no division with scale 0), x in float32 after the turn,
+ * rounded to nearest even: to bf16; to e4m3, +-448 at most, NaN kept; to int8 or int4, within
+ * [-128, 127] or [-8, 7], NaN as 0.  rpa_forward with the same scales reads it back.
+ * head_dim and kv_dtype as rpa_update_kv_cache; int4 takes rotary_dim a multiple of 4.
+ * A scale's reciprocal must be finite.  Only the slots of the batch's tokens are written, and the
+ * q_out rows of those tokens: a token whose metadata is bad is skipped whole, as are the tokens
+ * from cu_q_lens[num_seqs] on.  Two tokens of a batch that name one slot leave it undefined.
+ * `workspace` is optional, as for rpa_update_kv_cache. */
+RPA_API int rpa_rope_update_kv_cache(const rpa_params* p, const rope_table* t, const rope_strides* strides,
+                                     const void* q, const void* new_k, const void* new_v, void* kv_pages,
+                                     const int32_t* kv_lens, const int32_t* page_indices, const int32_t* cu_q_lens,
+                                     const int32_t* num_seqs, const int32_t* positions, void* q_out, void* workspace,
+                                     size_t workspace_bytes, rpa_stream_t stream);
 
 /* ---------------------------------------------------------------------- */
 /* MLA latent ragged paged attention                                       */

@@ -30,7 +30,7 @@ EXPORTS = ("rpa_workspace_size", "rpa_forward", "rpa_update_kv_cache", "mla_work
            "rpa_check_device_status", "rpa_last_error", "rpa_version", "rpa_profile_enable",
            "rpa_profile_reset", "rpa_profile_read", "rpa_forward_noalloc", "rpa_launch_count",
            "rpa_forward_update", "sparse_mla_ragged_workspace_size", "sparse_mla_write_and_attend_ragged",
-           "rpa_selftest_bounded_wait")
+           "rpa_selftest_bounded_wait", "rope_table_init", "rope_apply", "rpa_rope_update_kv_cache")
 
 
 class RpaError(RuntimeError):
@@ -84,6 +84,40 @@ class sparse_ragged_params(ctypes.Structure):
                 ("total_num_pages", ctypes.c_int32), ("sm_scale", ctypes.c_float)]
 
 
+ROPE_HALF, ROPE_INTERLEAVED, ROPE_MAX_DIM = 0, 1, 256
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "llama3": 3, "yarn": 4}
+
+
+class rope_params(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("version", ctypes.c_uint32), ("rotary_dim", ctypes.c_int32),
+                ("pairing", ctypes.c_int32), ("scaling", ctypes.c_int32), ("original_max_position", ctypes.c_int32),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double), ("low_freq_factor", ctypes.c_double),
+                ("high_freq_factor", ctypes.c_double), ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+                ("attention_factor", ctypes.c_double)]
+
+
+class rope_table(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("version", ctypes.c_uint32), ("rotary_dim", ctypes.c_int32),
+                ("pairing", ctypes.c_int32), ("amplitude", ctypes.c_float), ("reserved", ctypes.c_uint32),
+                ("step", ctypes.c_uint64 * (ROPE_MAX_DIM // 2))]
+
+
+class rope_apply_params(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("version", ctypes.c_uint32), ("num_tokens", ctypes.c_int32),
+                ("num_q_heads", ctypes.c_int32), ("num_k_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("inverse", ctypes.c_int32), ("reserved", ctypes.c_int32), ("q_token_stride", ctypes.c_int64),
+                ("q_head_stride", ctypes.c_int64), ("k_token_stride", ctypes.c_int64),
+                ("k_head_stride", ctypes.c_int64), ("q_out_token_stride", ctypes.c_int64),
+                ("q_out_head_stride", ctypes.c_int64), ("k_out_token_stride", ctypes.c_int64),
+                ("k_out_head_stride", ctypes.c_int64)]
+
+
+class rope_strides(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("version", ctypes.c_uint32), ("q_token", ctypes.c_int64),
+                ("q_head", ctypes.c_int64), ("k_token", ctypes.c_int64), ("k_head", ctypes.c_int64),
+                ("v_token", ctypes.c_int64), ("v_head", ctypes.c_int64)]
+
+
 _lib = None
 _lock = threading.Lock()
 
@@ -113,6 +147,10 @@ def load_library(path: str = LIB_PATH):
         lib.sparse_mla_forward.argtypes = [ctypes.POINTER(sparse_params), P, P, P, P, P, P, P, sz, P]
         lib.sparse_mla_ragged_workspace_size.argtypes = [ctypes.POINTER(sparse_ragged_params), szp]
         lib.sparse_mla_write_and_attend_ragged.argtypes = [ctypes.POINTER(sparse_ragged_params)] + [P] * 14 + [sz, P]
+        lib.rope_table_init.argtypes = [ctypes.POINTER(rope_params), ctypes.POINTER(rope_table)]
+        lib.rope_apply.argtypes = [ctypes.POINTER(rope_apply_params), ctypes.POINTER(rope_table)] + [P] * 6
+        lib.rpa_rope_update_kv_cache.argtypes = [ctypes.POINTER(rpa_params), ctypes.POINTER(rope_table),
+                                                 ctypes.POINTER(rope_strides)] + [P] * 11 + [sz, P]
         lib.rpa_check_device_status.argtypes = [P, ctypes.POINTER(ctypes.c_uint32), P]
         lib.rpa_selftest_bounded_wait.argtypes = [P, sz, P]
         lib.rpa_profile_enable.argtypes = [ctypes.c_int]
@@ -344,6 +382,168 @@ def rpa_forward_update(q, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_le
                                   _ptr(kv_lens), _ptr(page_indices), _ptr(cu_q_lens), _ptr(num_seqs), _ptr(out),
                                   _ptr(workspace), workspace.numel(), _stream()))
     return out
+
+
+def make_rope_table(rotary_dim, *, base=10000.0, interleaved=False, scaling=None) -> rope_table:
+    """The table the rotating calls take; made once from the model's configuration.
+
+    ``scaling`` names a change of the frequencies and its numbers, as ``include/rpa.h`` defines them:
+    ``{"type": "linear" | "ntk", "factor": ...}``, ``{"type": "llama3", "factor", "low_freq_factor",
+    "high_freq_factor", "original_max_position"}`` or ``{"type": "yarn", "factor", "beta_fast" (32),
+    "beta_slow" (1), "original_max_position"}``; each may carry ``"attention_factor"``, the factor on
+    every turned element (YaRN's default is 0.1 ln(factor) + 1)."""
+    more = dict(scaling or {"type": "none"})
+    kind = more.pop("type", None)
+    if kind not in ROPE_SCALINGS:
+        raise ValueError(f"scaling type {kind!r} is none of {sorted(ROPE_SCALINGS)}")
+    takes = {"none": (), "linear": ("factor",), "ntk": ("factor",),
+             "llama3": ("factor", "low_freq_factor", "high_freq_factor", "original_max_position"),
+             "yarn": ("factor", "beta_fast", "beta_slow", "original_max_position")}[kind]
+    if kind == "yarn":
+        more = {"beta_fast": 32.0, "beta_slow": 1.0, **more}
+    if set(more) - {"attention_factor"} != set(takes):
+        raise ValueError(f"{kind} scaling takes {', '.join(takes) or 'nothing'} (and attention_factor), got {sorted(more)}")
+    p = rope_params(struct_size=ctypes.sizeof(rope_params), version=ABI_VERSION, rotary_dim=int(rotary_dim),
+                    pairing=ROPE_INTERLEAVED if interleaved else ROPE_HALF, scaling=ROPE_SCALINGS[kind], base=float(base))
+    for name, value in more.items():
+        setattr(p, name, int(value) if name == "original_max_position" else float(value))
+    t = rope_table()
+    _check(load_library().rope_table_init(ctypes.byref(p), ctypes.byref(t)))
+    return t
+
+
+def _rows(t: torch.Tensor, name: str, heads=None, dim=None):
+    """(token stride, head stride) of bf16 rows [tokens, heads, head_dim] on the GPU; any strides with
+    adjacent elements and 16-byte aligned rows."""
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16 or t.dim() != 3:
+        raise ValueError(f"{name} must be bfloat16 [tokens, heads, head_dim], got {t.dtype} {tuple(t.shape)}")
+    n, h, d = t.shape
+    if (heads is not None and h != heads) or (dim is not None and d != dim):
+        raise ValueError(f"{name} must have {heads} heads of {dim}, got {tuple(t.shape)}")
+    token, head, element = t.stride()
+    if h <= 1:  # the stride of a dimension of one entry says nothing
+        head = d
+    if n <= 1:
+        token = h * head
+    if element != 1 or head % 8 or token % 8 or head <= 0 or token <= 0:
+        raise ValueError(f"{name} must have adjacent elements and token and head strides that are positive multiples "
+                         f"of 8, got strides {t.stride()}")
+    return token, head
+
+
+def _same_device(first: torch.Tensor, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors are on {first.device} and {t.device}")
+
+
+def _launch(device: torch.device, call):
+    """call(stream) with ``device`` current, on its current stream."""
+    if device.index == torch.cuda.current_device():
+        _check(call(_stream()))
+    else:
+        with torch.cuda.device(device):
+            _check(call(_stream()))
+
+
+def _is_table(table):
+    if not isinstance(table, rope_table):
+        raise ValueError("table must come from make_rope_table")
+
+
+def rope_apply(q, k, positions, table, *, inverse=False, q_out=None, k_out=None):
+    """Turns q [T, Hq, D] and k [T, Hk, D] (or None) to ``positions`` [T] int32; returns ``(q_out, k_out)``.
+
+    q and k are bf16 with any token and head strides; ``q_out=q`` and ``k_out=k`` work in place.
+    ``inverse`` turns back by the same angles (the map of an output's gradient to the input's)."""
+    lib = load_library()
+    _is_table(table)
+    q_token, q_head = _rows(q, "q")
+    T, hq, d = q.shape
+    _dev(positions, "positions", torch.int32)
+    if positions.shape != (T,):
+        raise ValueError(f"positions must be [{T}], got {tuple(positions.shape)}")
+    q_out = torch.empty((T, hq, d), dtype=q.dtype, device=q.device) if q_out is None else q_out
+    if q_out.shape != q.shape:
+        raise ValueError(f"q_out must have q's shape {tuple(q.shape)}, got {tuple(q_out.shape)}")
+    qo_token, qo_head = _rows(q_out, "q_out")
+    hk = k_token = k_head = ko_token = ko_head = 0
+    if k is not None:
+        k_token, k_head = _rows(k, "k", dim=d)
+        hk = k.shape[1]
+        k_out = torch.empty((T, hk, d), dtype=k.dtype, device=k.device) if k_out is None else k_out
+        if k.shape[0] != T or k_out.shape != k.shape:
+            raise ValueError(f"k and k_out must be [{T}, heads, {d}], got {tuple(k.shape)} and {tuple(k_out.shape)}")
+        ko_token, ko_head = _rows(k_out, "k_out")
+    elif k_out is not None:
+        raise ValueError("k_out goes with k")
+    _same_device(q, k, positions, q_out, k_out)
+    if T == 0:
+        return q_out, k_out
+    prm = rope_apply_params(ctypes.sizeof(rope_apply_params), ABI_VERSION, T, hq, hk, d, 1 if inverse else 0, 0, q_token,
+                            q_head, k_token, k_head, qo_token, qo_head, ko_token, ko_head)
+    _launch(q.device, lambda stream: lib.rope_apply(ctypes.byref(prm), ctypes.byref(table), _ptr(q), _ptr(k),
+                                                    _ptr(positions), _ptr(q_out), _ptr(k_out), stream))
+    return q_out, k_out
+
+
+def _rope_update_args(q, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, table, positions, q_out, **opts):
+    """The checks the appending calls share; (rpa_params, rope_strides, q_out)."""
+    _is_table(table)
+    _dev(kv_pages, "kv_pages")
+    for n, t in (("kv_lens", kv_lens), ("page_indices", page_indices), ("cu_q_lens", cu_q_lens),
+                 ("num_seqs", num_seqs)):
+        _dev(t, n, torch.int32)
+    d, hkv = kv_head_dim(kv_pages), kv_pages.shape[2] // 2
+    k_token, k_head = _rows(new_k, "new_k", hkv, d)
+    v_token, v_head = _rows(new_v, "new_v", hkv, d)
+    T = new_k.shape[0]
+    if new_v.shape[0] != T:
+        raise ValueError("new_k and new_v must have the same number of tokens")
+    q_token = q_head = 0
+    if q is not None:
+        q_token, q_head = _rows(q, "q", dim=d)
+        if q.shape[0] != T:
+            raise ValueError("q must have new_k's number of tokens")
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+        _dev(q_out, "q_out", torch.bfloat16)
+        if q_out.shape != q.shape:
+            raise ValueError(f"q_out must have q's shape {tuple(q.shape)}, got {tuple(q_out.shape)}")
+    elif q_out is not None:
+        raise ValueError("q_out goes with q")
+    if positions is not None:
+        _dev(positions, "positions", torch.int32)
+        if positions.shape != (T,):
+            raise ValueError(f"positions must be [{T}], got {tuple(positions.shape)}")
+    prm = make_rpa_params(new_k if q is None else q, kv_pages, page_indices, **opts)
+    if kv_lens.numel() != prm.max_num_seqs or cu_q_lens.numel() != prm.max_num_seqs + 1 or num_seqs.numel() != 1:
+        raise ValueError("kv_lens must be [max_num_seqs], cu_q_lens [max_num_seqs + 1], num_seqs [1]")
+    _same_device(kv_pages, q, new_k, new_v, kv_lens, page_indices, cu_q_lens, num_seqs, positions, q_out)
+    st = rope_strides(ctypes.sizeof(rope_strides), ABI_VERSION, q_token, q_head, k_token, k_head, v_token, v_head)
+    return prm, st, q_out
+
+
+def rpa_rope_update_kv_cache(q, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, table, *,
+                             positions=None, k_scale=None, v_scale=None, q_out=None, workspace=None):
+    """Turns ``new_k`` [T, Hkv, D] bf16 to its slots' positions and writes it and ``new_v`` into
+    ``kv_pages`` in place, rounded to the cache's type (divided by the scales first); turns ``q``
+    [T, Hq, D] (or None) beside them.  Returns ``(q_out, kv_pages)``.
+
+    q, new_k and new_v take any token and head strides (slices of one projection's output);
+    ``positions`` [T] int32 turns by other positions than the slots' own.  Bad metadata is recorded in
+    ``workspace``'s error word where one is given."""
+    lib = load_library()
+    prm, st, q_out = _rope_update_args(q, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, table,
+                                       positions, q_out, k_scale=k_scale, v_scale=v_scale)
+    if new_k.shape[0] == 0:
+        return q_out, kv_pages
+    _launch(kv_pages.device, lambda stream: lib.rpa_rope_update_kv_cache(
+        ctypes.byref(prm), ctypes.byref(table), ctypes.byref(st), _ptr(q), _ptr(new_k), _ptr(new_v), _ptr(kv_pages),
+        _ptr(kv_lens), _ptr(page_indices), _ptr(cu_q_lens), _ptr(num_seqs), _ptr(positions), _ptr(q_out),
+        _ptr(workspace), 0 if workspace is None else workspace.numel(), stream))
+    return q_out, kv_pages
 
 
 def make_mla_params(ql_nope, q_pe, cache_kv_c, cache_k_pe, kv_lens, page_indices, *, sm_scale=1.0,

@@ -267,6 +267,71 @@ RaggedLayout ragged_layout(const sparse_params& sp, int* splits) {
     return L;
 }
 
+// ---------------------------- rotary positions ----------------------------
+int check_rope_table(const rope_table* t) {
+    if (!t) return fail(RPA_ERR_NULL, "rope table is NULL");
+    if (t->struct_size < sizeof(rope_table)) return fail(RPA_ERR_VALUE, "rope_table.struct_size too small");
+    if (t->version != RPA_ABI_VERSION) return fail(RPA_ERR_VALUE, "rope_table.version %u != %d", t->version, RPA_ABI_VERSION);
+    if (t->rotary_dim < 0 || t->rotary_dim > RPA_ROPE_MAX_DIM || t->rotary_dim % 2)
+        return fail(RPA_ERR_SHAPE, "rotary_dim %d must be even, 0 to %d", t->rotary_dim, RPA_ROPE_MAX_DIM);
+    if (t->pairing != RPA_ROPE_HALF && t->pairing != RPA_ROPE_INTERLEAVED)
+        return fail(RPA_ERR_VALUE, "pairing %d is not an RPA_ROPE_* value", t->pairing);
+    if (!isfinite(t->amplitude)) return fail(RPA_ERR_VALUE, "amplitude must be finite");
+    return RPA_OK;
+}
+
+RopeTab rope_tab(const rope_table* t, bool inverse) {
+    RopeTab r;
+    memcpy(r.step, t->step, sizeof r.step);
+    r.rotary_dim = t->rotary_dim;
+    r.interleaved = t->pairing == RPA_ROPE_INTERLEAVED;
+    r.amplitude = t->amplitude;
+    r.sin_amplitude = inverse ? -t->amplitude : t->amplitude;
+    return r;
+}
+
+// One operand's rows: strides checked (0: dense); an output's rows must not overlap.
+int rope_rows(const char* name, const void* p, int tokens, int heads, int dim, int64_t token, int64_t head, bool output,
+              RopeRows& r) {
+    r.p = static_cast<__nv_bfloat16*>(const_cast<void*>(p));
+    r.head = head ? head : dim;
+    r.token = token ? token : (int64_t)heads * dim;
+    if (!aligned16(p)) return fail(RPA_ERR_VALUE, "%s must be 16-byte aligned", name);
+    // (the bound keeps every byte offset of the rows inside 63 bits)
+    constexpr int64_t kMaxStride = 1ll << 30;
+    if (r.head < 0 || r.token < 0 || r.head % 8 || r.token % 8 || r.head > kMaxStride || r.token > kMaxStride)
+        return fail(RPA_ERR_SHAPE, "%s strides must be multiples of 8 elements, 0 to 2^30", name);
+    if (output) {
+        const bool tokens_out = (heads == 1 || r.head >= dim) && (tokens <= 1 || r.token >= (heads - 1) * r.head + dim);
+        const bool heads_out = (tokens <= 1 || r.token >= dim) && (heads == 1 || r.head >= (tokens - 1) * r.token + dim);
+        if (!tokens_out && !heads_out) return fail(RPA_ERR_SHAPE, "%s strides make rows overlap", name);
+    }
+    return RPA_OK;
+}
+
+// Whether two operands share elements. Rows of one token stride that stay inside it (slices of
+// one projection's output) are compared by their place in it, others by their extent.
+bool rope_overlap(const RopeRows& a, int ha, const RopeRows& b, int hb, int tokens, int dim) {
+    if (tokens <= 0) return false;
+    const int64_t ra = (ha - 1) * a.head + dim, rb = (hb - 1) * b.head + dim;  // a token's elements
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+    const uintptr_t a1 = a0 + 2 * ((tokens - 1) * a.token + ra), b1 = b0 + 2 * ((tokens - 1) * b.token + rb);
+    if (a1 <= b0 || b1 <= a0) return false;
+    if (a.token == b.token && tokens > 1 && ra <= a.token && rb <= b.token) {
+        const int64_t step = 2 * a.token;
+        const int64_t off = b0 >= a0 ? (int64_t)((b0 - a0) % step) : (step - (int64_t)((a0 - b0) % step)) % step;
+        return !(off >= 2 * ra && off + 2 * rb <= step);
+    }
+    return true;
+}
+
+// An output beside an input: the same rows (in place) or none of them.
+bool rope_in_place_or_apart(const RopeRows& in, const RopeRows& out, int heads, int tokens, int dim) {
+    if (in.p == out.p && in.token == out.token && in.head == out.head) return true;
+    if (in.p == out.p && tokens <= 1 && (heads <= 1 || in.head == out.head)) return true;
+    return !rope_overlap(in, heads, out, heads, tokens, dim);
+}
+
 }  // namespace
 
 extern "C" {
@@ -432,6 +497,185 @@ int rpa_forward_update(const rpa_params* p, const void* q, const void* new_k, co
     if (rc) return rc;
     cudaError_t e = launch_rpa_forward_update(a, u, sms, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "rpa_forward_update launch");
+    return RPA_OK;
+}
+
+int rope_table_init(const rope_params* p, rope_table* t) {
+    if (!p || !t) return fail(RPA_ERR_NULL, "params or table is NULL");
+    if (p->struct_size < sizeof(rope_params)) return fail(RPA_ERR_VALUE, "rope_params.struct_size too small");
+    if (p->version != RPA_ABI_VERSION) return fail(RPA_ERR_VALUE, "rope_params.version %u != %d", p->version, RPA_ABI_VERSION);
+    const int r = p->rotary_dim;
+    if (r < 0 || r > RPA_ROPE_MAX_DIM || r % 2)
+        return fail(RPA_ERR_SHAPE, "rotary_dim %d must be even, 0 to %d", r, RPA_ROPE_MAX_DIM);
+    if (p->pairing != RPA_ROPE_HALF && p->pairing != RPA_ROPE_INTERLEAVED)
+        return fail(RPA_ERR_VALUE, "pairing %d is not an RPA_ROPE_* value", p->pairing);
+    const int kind = p->scaling;
+    if (kind < RPA_ROPE_SCALE_NONE || kind > RPA_ROPE_SCALE_YARN)
+        return fail(RPA_ERR_VALUE, "scaling %d is not an RPA_ROPE_SCALE_* value", kind);
+    if (!(p->base > 1.0) || !isfinite(p->base)) return fail(RPA_ERR_VALUE, "base must be finite and > 1");
+    if (kind != RPA_ROPE_SCALE_NONE && (!(p->factor >= 1.0) || !isfinite(p->factor)))
+        return fail(RPA_ERR_VALUE, "factor must be finite and >= 1");
+    if ((kind == RPA_ROPE_SCALE_LLAMA3 || kind == RPA_ROPE_SCALE_YARN) && p->original_max_position <= 0)
+        return fail(RPA_ERR_VALUE, "original_max_position must be positive");
+    if (kind == RPA_ROPE_SCALE_LLAMA3 &&
+        (!(p->low_freq_factor > 0.0) || !(p->high_freq_factor > p->low_freq_factor) || !isfinite(p->high_freq_factor)))
+        return fail(RPA_ERR_VALUE, "0 < low_freq_factor < high_freq_factor is required");
+    if (kind == RPA_ROPE_SCALE_YARN && (!(p->beta_slow > 0.0) || !(p->beta_fast > p->beta_slow) || !isfinite(p->beta_fast)))
+        return fail(RPA_ERR_VALUE, "0 < beta_slow < beta_fast is required");
+    if (kind == RPA_ROPE_SCALE_NTK && r > 0 && r <= 2) return fail(RPA_ERR_SHAPE, "NTK scaling needs rotary_dim > 2");
+    if (!isfinite(p->attention_factor) || p->attention_factor < 0.0)
+        return fail(RPA_ERR_VALUE, "attention_factor must be finite and >= 0 (0 = default)");
+    const double two_pi = 6.283185307179586476925286766559;
+    memset(t, 0, sizeof *t);
+    t->struct_size = sizeof(rope_table);
+    t->version = RPA_ABI_VERSION;
+    t->rotary_dim = r;
+    t->pairing = p->pairing;
+    double amplitude = p->attention_factor;
+    if (amplitude == 0.0) amplitude = kind == RPA_ROPE_SCALE_YARN ? 0.1 * log(p->factor) + 1.0 : 1.0;
+    t->amplitude = (float)amplitude;
+    if (!isfinite(t->amplitude)) return fail(RPA_ERR_VALUE, "attention_factor must be finite in float32");
+    double low = 0.0, high = 0.0;
+    if (kind == RPA_ROPE_SCALE_YARN && r > 0) {
+        const double ctx = p->original_max_position / two_pi, per = r / (2.0 * log(p->base));
+        low = fmax(floor(per * log(ctx / p->beta_fast)), 0.0);
+        high = fmin(ceil(per * log(ctx / p->beta_slow)), r - 1.0);
+    }
+    const double base = kind == RPA_ROPE_SCALE_NTK && r > 2 ? p->base * pow(p->factor, r / (r - 2.0)) : p->base;
+    for (int i = 0; i < r / 2; ++i) {
+        double f = pow(base, -2.0 * i / r);
+        double keep = 1.0;  // the share of f_i itself, the rest f_i / factor
+        if (kind == RPA_ROPE_SCALE_LINEAR) {
+            keep = 0.0;
+        } else if (kind == RPA_ROPE_SCALE_LLAMA3) {
+            const double turns = p->original_max_position * f / two_pi;
+            keep = fmin(fmax((turns - p->low_freq_factor) / (p->high_freq_factor - p->low_freq_factor), 0.0), 1.0);
+        } else if (kind == RPA_ROPE_SCALE_YARN) {
+            keep = 1.0 - fmin(fmax((i - low) / fmax(high - low, 0.001), 0.0), 1.0);
+        }
+        if (keep < 1.0) f = keep * f + (1.0 - keep) * f / p->factor;
+        t->step[i] = (uint64_t)nearbyint(f / two_pi * 18446744073709551616.0);  // f <= 1: below 2^62
+    }
+    return RPA_OK;
+}
+
+int rope_apply(const rope_apply_params* p, const rope_table* t, const void* q, const void* k, const int32_t* positions,
+               void* q_out, void* k_out, rpa_stream_t stream) {
+    if (!p) return fail(RPA_ERR_NULL, "params is NULL");
+    if (p->struct_size < sizeof(rope_apply_params)) return fail(RPA_ERR_VALUE, "rope_apply_params.struct_size too small");
+    if (p->version != RPA_ABI_VERSION) return fail(RPA_ERR_VALUE, "rope_apply_params.version %u != %d", p->version, RPA_ABI_VERSION);
+    int rc = check_rope_table(t);
+    if (rc) return rc;
+    if (p->num_tokens < 0 || p->num_q_heads <= 0 || p->num_k_heads < 0 || p->num_q_heads > 65536 || p->num_k_heads > 65536)
+        return fail(RPA_ERR_SHAPE, "num_tokens >= 0, num_q_heads >= 1 and num_k_heads >= 0 (at most 65536) are required");
+    if (p->head_dim <= 0 || p->head_dim > 512 || p->head_dim % 16)
+        return fail(RPA_ERR_UNSUPPORTED, "head_dim %d (supported: multiples of 16 up to 512)", p->head_dim);
+    if (t->rotary_dim > p->head_dim) return fail(RPA_ERR_SHAPE, "rotary_dim %d exceeds head_dim %d", t->rotary_dim, p->head_dim);
+    if (p->inverse != 0 && p->inverse != 1) return fail(RPA_ERR_VALUE, "inverse must be 0 or 1");
+    if (!q || !q_out || !positions) return fail(RPA_ERR_NULL, "q, q_out or positions is NULL");
+    if ((k != nullptr) != (p->num_k_heads > 0) || (k_out != nullptr) != (p->num_k_heads > 0))
+        return fail(RPA_ERR_NULL, "k and k_out go with num_k_heads > 0");
+    RopeApplyArgs a;
+    memset(&a, 0, sizeof a);
+    const int T = p->num_tokens, hq = p->num_q_heads, hk = p->num_k_heads, d = p->head_dim;
+    rc = rope_rows("q", q, T, hq, d, p->q_token_stride, p->q_head_stride, false, a.q);
+    if (!rc) rc = rope_rows("q_out", q_out, T, hq, d, p->q_out_token_stride, p->q_out_head_stride, true, a.q_out);
+    if (!rc && hk) rc = rope_rows("k", k, T, hk, d, p->k_token_stride, p->k_head_stride, false, a.k);
+    if (!rc && hk) rc = rope_rows("k_out", k_out, T, hk, d, p->k_out_token_stride, p->k_out_head_stride, true, a.k_out);
+    if (rc) return rc;
+    if (!rope_in_place_or_apart(a.q, a.q_out, hq, T, d)) return fail(RPA_ERR_VALUE, "q_out overlaps q without being it");
+    if (hk && !rope_in_place_or_apart(a.k, a.k_out, hk, T, d)) return fail(RPA_ERR_VALUE, "k_out overlaps k without being it");
+    if (hk && (rope_overlap(a.q_out, hq, a.k, hk, T, d) || rope_overlap(a.k_out, hk, a.q, hq, T, d) ||
+               rope_overlap(a.q_out, hq, a.k_out, hk, T, d)))
+        return fail(RPA_ERR_VALUE, "an output overlaps the other operand");
+    if (T == 0) return RPA_OK;
+    const int sms = num_sms_current();
+    if (!sms) return fail(RPA_ERR_CUDA, "no CUDA device");
+    a.tab = rope_tab(t, p->inverse != 0);
+    a.positions = positions;
+    a.num_tokens = T;
+    a.num_q_heads = hq;
+    a.num_k_heads = hk;
+    a.head_dim = d;
+    cudaError_t e = launch_rope_apply(a, sms, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "rope_apply launch");
+    return RPA_OK;
+}
+
+// Validates an rpa_rope_update_kv_cache call (the workspace is checked by the caller) and fills
+// the kernel's argument block.
+static int rope_update_prepare(const rpa_params* p, const rope_table* t, const rope_strides* st, const void* q,
+                               const void* new_k, const void* new_v, void* kv_pages, const int32_t* kv_lens,
+                               const int32_t* page_indices, const int32_t* cu_q_lens, const int32_t* num_seqs,
+                               const int32_t* positions, void* q_out, uint32_t* err, RopeUpdateArgs& a) {
+    int rc = check_rpa_params(p);
+    if (!rc) rc = check_rope_table(t);
+    if (rc) return rc;
+    if (st && st->struct_size < sizeof(rope_strides)) return fail(RPA_ERR_VALUE, "rope_strides.struct_size too small");
+    if (st && st->version != RPA_ABI_VERSION) return fail(RPA_ERR_VALUE, "rope_strides.version %u != %d", st->version, RPA_ABI_VERSION);
+    if (!new_k || !new_v || !kv_pages || !kv_lens || !page_indices || !cu_q_lens || !num_seqs)
+        return fail(RPA_ERR_NULL, "a tensor pointer is NULL");
+    if ((q != nullptr) != (q_out != nullptr)) return fail(RPA_ERR_NULL, "q and q_out go together");
+    if (!aligned16(kv_pages)) return fail(RPA_ERR_VALUE, "kv_pages must be 16-byte aligned");
+    if (t->rotary_dim > p->head_dim) return fail(RPA_ERR_SHAPE, "rotary_dim %d exceeds head_dim %d", t->rotary_dim, p->head_dim);
+    if (p->kv_dtype == RPA_DTYPE_INT4 && t->rotary_dim % 4)
+        return fail(RPA_ERR_UNSUPPORTED, "int4 caches take a rotary_dim that is a multiple of 4 (got %d)", t->rotary_dim);
+    memset(&a, 0, sizeof a);
+    a.k_inv = p->k_scale != 0.f ? 1.f / p->k_scale : 1.f;
+    a.v_inv = p->v_scale != 0.f ? 1.f / p->v_scale : 1.f;
+    if (!isfinite(a.k_inv) || !isfinite(a.v_inv)) return fail(RPA_ERR_VALUE, "the reciprocals of k_scale and v_scale must be finite");
+    const int T = p->max_num_tokens, hq = q ? p->num_q_heads : 0, hkv = p->num_combined_kv_heads / 2, d = p->head_dim;
+    rc = rope_rows("new_k", new_k, T, hkv, d, st ? st->k_token : 0, st ? st->k_head : 0, false, a.k);
+    if (!rc) rc = rope_rows("new_v", new_v, T, hkv, d, st ? st->v_token : 0, st ? st->v_head : 0, false, a.v);
+    if (!rc && q) rc = rope_rows("q", q, T, hq, d, st ? st->q_token : 0, st ? st->q_head : 0, false, a.q);
+    if (rc) return rc;
+    if (q) {
+        RopeRows out;
+        rc = rope_rows("q_out", q_out, T, hq, d, 0, 0, true, out);
+        if (rc) return rc;
+        if (!rope_in_place_or_apart(a.q, out, hq, T, d)) return fail(RPA_ERR_VALUE, "q_out overlaps q without being it");
+        if (rope_overlap(out, hq, a.k, hkv, T, d) || rope_overlap(out, hq, a.v, hkv, T, d))
+            return fail(RPA_ERR_VALUE, "q_out overlaps new_k or new_v");
+        if (q_out == kv_pages) return fail(RPA_ERR_VALUE, "q_out must not alias kv_pages");
+        a.q_out = out.p;
+    }
+    if (kv_pages == new_k || kv_pages == new_v || kv_pages == q) return fail(RPA_ERR_VALUE, "kv_pages must not alias q, new_k or new_v");
+    a.tab = rope_tab(t, false);
+    a.kv_pages = kv_pages;
+    a.kv_lens = kv_lens;
+    a.page_indices = page_indices;
+    a.cu_q_lens = cu_q_lens;
+    a.num_seqs = num_seqs;
+    a.positions = positions;
+    a.err = err;
+    a.kv_dtype = p->kv_dtype;
+    a.row_bytes = p->kv_dtype == RPA_DTYPE_BF16 ? d * 2 : p->kv_dtype == RPA_DTYPE_INT4 ? d / 2 : d;
+    a.max_num_tokens = T;
+    a.num_q_heads = hq;
+    a.num_kv_heads = hkv;
+    a.head_dim = d;
+    a.total_num_pages = p->total_num_pages;
+    a.page_size = p->page_size;
+    a.max_num_seqs = p->max_num_seqs;
+    a.pages_per_seq = p->pages_per_seq;
+    return RPA_OK;
+}
+
+int rpa_rope_update_kv_cache(const rpa_params* p, const rope_table* t, const rope_strides* strides, const void* q,
+                             const void* new_k, const void* new_v, void* kv_pages, const int32_t* kv_lens,
+                             const int32_t* page_indices, const int32_t* cu_q_lens, const int32_t* num_seqs,
+                             const int32_t* positions, void* q_out, void* workspace, size_t workspace_bytes,
+                             rpa_stream_t stream) {
+    if (workspace && workspace_bytes < (size_t)kWsHeaderBytes) return fail(RPA_ERR_WORKSPACE, "workspace smaller than 256 bytes");
+    RopeUpdateArgs a;
+    const int rc = rope_update_prepare(p, t, strides, q, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs,
+                                       positions, q_out,
+                                       workspace ? &reinterpret_cast<WsHeader*>(workspace)->error_bits : nullptr, a);
+    if (rc) return rc;
+    const int sms = num_sms_current();
+    if (!sms) return fail(RPA_ERR_CUDA, "no CUDA device");
+    cudaError_t e = launch_rope_update(a, sms, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "rpa_rope_update_kv_cache launch");
     return RPA_OK;
 }
 

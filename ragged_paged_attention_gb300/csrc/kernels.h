@@ -226,6 +226,45 @@ struct MlaUpdateArgs {
     int total_num_pages, page_size, max_num_seqs, pages_per_seq;
 };
 
+// A rope_table as the kernels take it (by value, in the launch's parameters).
+struct RopeTab {
+    uint64_t step[128];             // pair i's turn per position, as a fraction of 2^64
+    int rotary_dim, interleaved;
+    float amplitude, sin_amplitude; // the sine's factor is negative for the inverse
+};
+
+// bf16 rows: element e of head h of token t at p[t * token + h * head + e].
+struct RopeRows {
+    __nv_bfloat16* p;
+    long long token, head;
+};
+
+struct RopeApplyArgs {
+    RopeTab tab;
+    RopeRows q, k, q_out, k_out;
+    const int32_t* positions;
+    int num_tokens, num_q_heads, num_k_heads, head_dim;
+};
+
+struct RopeUpdateArgs {
+    RopeTab tab;
+    RopeRows q, k, v;               // no q: num_q_heads 0
+    __nv_bfloat16* q_out;           // [max_num_tokens, num_q_heads, head_dim]
+    void* kv_pages;
+    const int32_t* kv_lens;
+    const int32_t* page_indices;
+    const int32_t* cu_q_lens;
+    const int32_t* num_seqs;
+    const int32_t* positions;       // may be null: the slot's position
+    uint32_t* err;                  // may be null
+    float k_inv, v_inv;             // reciprocal scales (1: none)
+    int kv_dtype, row_bytes;        // row_bytes: one head row of K or V in the cache
+    int max_num_tokens, num_q_heads, num_kv_heads, head_dim;
+    int total_num_pages, page_size, max_num_seqs, pages_per_seq;
+};
+
+cudaError_t launch_rope_apply(const RopeApplyArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_rope_update(const RopeUpdateArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_rpa_forward(const RpaArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_wait_selftest(uint32_t* err, cudaStream_t stream);
 cudaError_t launch_rpa_forward_update(const RpaArgs& a, const RpaUpdateArgs& u, int num_sms, cudaStream_t stream);
