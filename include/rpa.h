@@ -16,6 +16,7 @@
  *   sparse_mla_forward   DSA sparse MLA over selected units of a paged latent cache
  *                        (sglang-jax "dsa/sparse_mla_prefill.py", sparse_mla_attention and
  *                        _sparse_mla_kernel_chunked_hminor).
+ *   rpa_cross_forward    attention to all the keys of a sequence, whatever their number.
  *   rope_apply           rotary positions on packed queries and keys.
  *   rpa_rope_update_kv_cache
  *                        rpa_update_kv_cache with the rotation, and the rounding to the
@@ -333,6 +334,34 @@ RPA_API int rpa_rope_update_kv_cache(const rpa_params* p, const rope_table* t, c
                                      const int32_t* kv_lens, const int32_t* page_indices, const int32_t* cu_q_lens,
                                      const int32_t* num_seqs, const int32_t* positions, void* q_out, void* workspace,
                                      size_t workspace_bytes, rpa_stream_t stream);
+
+/* rpa_rope_update_kv_cache, then rpa_forward of the turned queries over the updated cache, in one
+ * call.  `q_rot` is rpa_rope_update_kv_cache's q_out (not NULL; the caller's, holding the turned
+ * queries afterwards), `out` and `workspace` are rpa_forward's; the workspace's error word also
+ * records the cache write's metadata errors.  `out` must not alias q, q_rot, kv_pages, new_k or
+ * new_v. */
+RPA_API int rpa_rope_forward_update(const rpa_params* p, const rope_table* t, const rope_strides* strides, const void* q,
+                                    const void* new_k, const void* new_v, void* kv_pages, const int32_t* kv_lens,
+                                    const int32_t* page_indices, const int32_t* cu_q_lens, const int32_t* num_seqs,
+                                    const int32_t* positions, void* q_rot, void* out, void* workspace,
+                                    size_t workspace_bytes, rpa_stream_t stream);
+
+/* ---------------------------------------------------------------------- */
+/* Cross attention                                                          */
+/* ---------------------------------------------------------------------- */
+
+/* Attention of a packed batch's queries to all the cached keys of their sequence: a decoder's
+ * tokens to its encoder's states, whose number has nothing to do with the queries', or a
+ * sequence's own tokens in both directions.  Arguments and layouts are rpa_forward's, with these
+ * differences: kv_lens[i] is any number of keys from 0 on, fewer than the queries or more; every
+ * query sees keys [0, kv_lens[i]); a sequence without keys gets rows of zeros; sliding_window is 0
+ * and mask_value NaN.  The keys and values are written by rpa_update_kv_cache or
+ * rpa_rope_update_kv_cache (with cu_q_lens and kv_lens of the encoder's side).  `workspace`:
+ * rpa_cross_workspace_size bytes, as rpa_forward's. */
+RPA_API int rpa_cross_workspace_size(const rpa_params* p, size_t* bytes);
+RPA_API int rpa_cross_forward(const rpa_params* p, const void* q, const void* kv_pages, const int32_t* kv_lens,
+                              const int32_t* page_indices, const int32_t* cu_q_lens, const int32_t* num_seqs, void* out,
+                              void* workspace, size_t workspace_bytes, rpa_stream_t stream);
 
 /* ---------------------------------------------------------------------- */
 /* MLA latent ragged paged attention                                       */

@@ -30,7 +30,8 @@ EXPORTS = ("rpa_workspace_size", "rpa_forward", "rpa_update_kv_cache", "mla_work
            "rpa_check_device_status", "rpa_last_error", "rpa_version", "rpa_profile_enable",
            "rpa_profile_reset", "rpa_profile_read", "rpa_forward_noalloc", "rpa_launch_count",
            "rpa_forward_update", "sparse_mla_ragged_workspace_size", "sparse_mla_write_and_attend_ragged",
-           "rpa_selftest_bounded_wait", "rope_table_init", "rope_apply", "rpa_rope_update_kv_cache")
+           "rpa_selftest_bounded_wait", "rope_table_init", "rope_apply", "rpa_rope_update_kv_cache",
+           "rpa_rope_forward_update", "rpa_cross_workspace_size", "rpa_cross_forward")
 
 
 class RpaError(RuntimeError):
@@ -151,6 +152,10 @@ def load_library(path: str = LIB_PATH):
         lib.rope_apply.argtypes = [ctypes.POINTER(rope_apply_params), ctypes.POINTER(rope_table)] + [P] * 6
         lib.rpa_rope_update_kv_cache.argtypes = [ctypes.POINTER(rpa_params), ctypes.POINTER(rope_table),
                                                  ctypes.POINTER(rope_strides)] + [P] * 11 + [sz, P]
+        lib.rpa_rope_forward_update.argtypes = [ctypes.POINTER(rpa_params), ctypes.POINTER(rope_table),
+                                                ctypes.POINTER(rope_strides)] + [P] * 12 + [sz, P]
+        lib.rpa_cross_workspace_size.argtypes = [ctypes.POINTER(rpa_params), szp]
+        lib.rpa_cross_forward.argtypes = [ctypes.POINTER(rpa_params), P, P, P, P, P, P, P, P, sz, P]
         lib.rpa_check_device_status.argtypes = [P, ctypes.POINTER(ctypes.c_uint32), P]
         lib.rpa_selftest_bounded_wait.argtypes = [P, sz, P]
         lib.rpa_profile_enable.argtypes = [ctypes.c_int]
@@ -210,6 +215,17 @@ class Workspace:
             buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
             cls._cache[key] = buf
         return buf
+
+
+def _own_workspace(nbytes: int, device: torch.device, tag: str) -> torch.Tensor:
+    """The workspace of a call that was given none: one per device, stream and purpose, so that calls on
+    two streams share none; while the stream is captured a new one, owned by the graph.  Of that one only
+    the header, with the error word, is zeroed on every replay: the plan writes the rest before it is read."""
+    if torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        ws[:256].zero_()
+        return ws
+    return Workspace.get(nbytes, device, f"{tag} {torch.cuda.current_stream(device).cuda_stream}")
 
 
 def _kv_code(dtype) -> int:
@@ -544,6 +560,77 @@ def rpa_rope_update_kv_cache(q, new_k, new_v, kv_pages, kv_lens, page_indices, c
         _ptr(kv_lens), _ptr(page_indices), _ptr(cu_q_lens), _ptr(num_seqs), _ptr(positions), _ptr(q_out),
         _ptr(workspace), 0 if workspace is None else workspace.numel(), stream))
     return q_out, kv_pages
+
+
+def rpa_rope_forward_update(q, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, table, *,
+                            positions=None, sm_scale=1.0, sliding_window=None, soft_cap=None, mask_value=None,
+                            k_scale=None, v_scale=None, q_rot=None, out=None, workspace=None, batch_kind=BATCH_MIXED):
+    """rpa_rope_update_kv_cache, then rpa_forward of the turned queries (kept in ``q_rot``), in one call;
+    writes ``kv_pages`` in place and returns ``out`` [T, Hq, D]."""
+    lib = load_library()
+    if q is None:
+        raise ValueError("q is required")
+    prm, st, q_rot = _rope_update_args(q, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, table,
+                                       positions, q_rot, sm_scale=sm_scale, sliding_window=sliding_window,
+                                       soft_cap=soft_cap, mask_value=mask_value, k_scale=k_scale, v_scale=v_scale,
+                                       batch_kind=batch_kind)
+    out = torch.empty_like(q_rot) if out is None else out
+    _dev(out, "out", torch.bfloat16)
+    if out.shape != q.shape:
+        raise ValueError(f"out must have q's shape {tuple(q.shape)}, got {tuple(out.shape)}")
+    _same_device(kv_pages, out, workspace)
+    if q.shape[0] == 0:
+        return out
+
+    def call(stream):
+        ws = _own_workspace(rpa_workspace_size(prm), kv_pages.device, "rpa") if workspace is None else workspace
+        return lib.rpa_rope_forward_update(
+            ctypes.byref(prm), ctypes.byref(table), ctypes.byref(st), _ptr(q), _ptr(new_k), _ptr(new_v), _ptr(kv_pages),
+            _ptr(kv_lens), _ptr(page_indices), _ptr(cu_q_lens), _ptr(num_seqs), _ptr(positions), _ptr(q_rot), _ptr(out),
+            _ptr(ws), ws.numel(), stream)
+
+    _launch(kv_pages.device, call)
+    return out
+
+
+def rpa_cross_workspace_size(params: rpa_params) -> int:
+    lib = load_library()
+    n = ctypes.c_size_t(0)
+    _check(lib.rpa_cross_workspace_size(ctypes.byref(params), ctypes.byref(n)))
+    return n.value
+
+
+def rpa_cross_forward(q, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, *, sm_scale=1.0, soft_cap=None,
+                      k_scale=None, v_scale=None, out=None, workspace=None, batch_kind=BATCH_MIXED):
+    """Attention of every query to all ``kv_lens`` keys of its sequence (a decoder's tokens to its
+    encoder's states); returns ``out`` [max_num_tokens, Hq, D] bf16.  A sequence without keys gets zeros."""
+    lib = load_library()
+    _dev(q, "q", torch.bfloat16)
+    _dev(kv_pages, "kv_pages")
+    for n, t in (("kv_lens", kv_lens), ("page_indices", page_indices), ("cu_q_lens", cu_q_lens),
+                 ("num_seqs", num_seqs)):
+        _dev(t, n, torch.int32)
+    if q.dim() != 3 or kv_head_dim(kv_pages) != q.shape[-1]:
+        raise ValueError("q must be [tokens, heads, head_dim] with kv_pages' head_dim")
+    prm = make_rpa_params(q, kv_pages, page_indices, sm_scale=sm_scale, soft_cap=soft_cap, k_scale=k_scale,
+                          v_scale=v_scale, batch_kind=batch_kind)
+    if kv_lens.numel() != prm.max_num_seqs or cu_q_lens.numel() != prm.max_num_seqs + 1 or num_seqs.numel() != 1:
+        raise ValueError("kv_lens must be [max_num_seqs], cu_q_lens [max_num_seqs + 1], num_seqs [1]")
+    out = torch.empty_like(q) if out is None else out
+    _dev(out, "out", torch.bfloat16)
+    if out.shape != q.shape:
+        raise ValueError(f"out must have q's shape {tuple(q.shape)}, got {tuple(out.shape)}")
+    _same_device(q, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, out, workspace)
+    if q.shape[0] == 0:
+        return out
+
+    def call(stream):
+        ws = _own_workspace(rpa_cross_workspace_size(prm), q.device, "rpa") if workspace is None else workspace
+        return lib.rpa_cross_forward(ctypes.byref(prm), _ptr(q), _ptr(kv_pages), _ptr(kv_lens), _ptr(page_indices),
+                                     _ptr(cu_q_lens), _ptr(num_seqs), _ptr(out), _ptr(ws), ws.numel(), stream)
+
+    _launch(q.device, call)
+    return out
 
 
 def make_mla_params(ql_nope, q_pe, cache_kv_c, cache_k_pe, kv_lens, page_indices, *, sm_scale=1.0,

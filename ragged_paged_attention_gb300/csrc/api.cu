@@ -396,6 +396,7 @@ static int rpa_prepare(const rpa_params* p, const void* q, const void* kv_pages,
     a.sm_scale = p->sm_scale;
     a.soft_cap = p->soft_cap;
     a.sliding_window = p->sliding_window;
+    a.causal = 1;
     a.mask_mild = mild_mask(p->mask_value) ? 1 : 0;
     a.mask_value = resolve_mask(p->mask_value);
     a.batch_kind = rpa_batch_kind(p);
@@ -676,6 +677,57 @@ int rpa_rope_update_kv_cache(const rpa_params* p, const rope_table* t, const rop
     if (!sms) return fail(RPA_ERR_CUDA, "no CUDA device");
     cudaError_t e = launch_rope_update(a, sms, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "rpa_rope_update_kv_cache launch");
+    return RPA_OK;
+}
+
+int rpa_rope_forward_update(const rpa_params* p, const rope_table* t, const rope_strides* strides, const void* q,
+                            const void* new_k, const void* new_v, void* kv_pages, const int32_t* kv_lens,
+                            const int32_t* page_indices, const int32_t* cu_q_lens, const int32_t* num_seqs,
+                            const int32_t* positions, void* q_rot, void* out, void* workspace, size_t workspace_bytes,
+                            rpa_stream_t stream) {
+    RpaArgs a;
+    int sms = 0;
+    int rc = rpa_prepare(p, q_rot, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, out, workspace, workspace_bytes,
+                         a, sms);
+    if (rc) return rc;
+    if (!q) return fail(RPA_ERR_NULL, "q is NULL");
+    if (out == q || out == new_k || out == new_v) return fail(RPA_ERR_VALUE, "out must not alias q, new_k or new_v");
+    RopeUpdateArgs u;
+    rc = rope_update_prepare(p, t, strides, q, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs,
+                             positions, q_rot, &a.hdr->error_bits, u);
+    if (rc) return rc;
+    cudaError_t e = launch_rope_update(u, sms, reinterpret_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess) e = launch_rpa_forward(a, sms, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "rpa_rope_forward_update launch");
+    return RPA_OK;
+}
+
+static int check_cross_params(const rpa_params* p) {
+    const int rc = check_rpa_params(p);
+    if (rc) return rc;
+    if (p->sliding_window != 0) return fail(RPA_ERR_VALUE, "cross attention takes no sliding_window");
+    if (!isnan(p->mask_value)) return fail(RPA_ERR_VALUE, "cross attention masks no key: mask_value must be NaN");
+    return RPA_OK;
+}
+
+int rpa_cross_workspace_size(const rpa_params* p, size_t* bytes) {
+    const int rc = check_cross_params(p);
+    if (rc) return rc;
+    return rpa_workspace_size(p, bytes);
+}
+
+int rpa_cross_forward(const rpa_params* p, const void* q, const void* kv_pages, const int32_t* kv_lens,
+                      const int32_t* page_indices, const int32_t* cu_q_lens, const int32_t* num_seqs, void* out,
+                      void* workspace, size_t workspace_bytes, rpa_stream_t stream) {
+    int rc = check_cross_params(p);
+    if (rc) return rc;
+    RpaArgs a;
+    int sms = 0;
+    rc = rpa_prepare(p, q, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, out, workspace, workspace_bytes, a, sms);
+    if (rc) return rc;
+    a.causal = 0;
+    cudaError_t e = launch_rpa_forward(a, sms, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "rpa_cross_forward launch");
     return RPA_OK;
 }
 

@@ -25,6 +25,7 @@ __host__ __device__ inline int update_cache_ints(int max_num_seqs) {
 }
 constexpr int kPrefillRows = 128;       // (token, q-head) rows per prefill item (one TMEM tile)
 constexpr int kMinChunk = 256;          // smallest split-KV chunk (keys)
+constexpr int kCrossZeroBlocks = 8;      // cross attention: blocks beside the plan for rows without a key
 constexpr int kMaxDecodeCtas = 2048;    // most decode shares (static, one per CTA, and pooled)
 // Pool: the part of the line left after the static shares (here only their rounding
 // remainder: measured on the Llama-3 and Gemma-2 batches, pooled shares of 64-256 keys cost
@@ -95,6 +96,7 @@ struct RpaArgs {
     int kv_int4;                // two 4-bit values a byte, element 2i in the low nibble of byte i
     float sm_scale, soft_cap;
     int sliding_window;
+    int causal;                 // 0 (cross attention): every query sees all kv_len keys, of any number
     // a mask_value that leaves masked keys real weight (above -1e30): every key of a sequence
     // takes part, a masked one with mask_value added to its logit (the RPA reference's form);
     // otherwise masked keys are skipped (their weight is exactly zero either way)
@@ -324,15 +326,15 @@ __device__ __forceinline__ bool seq_shape(const RpaArgs& a, int s, int& ql, int&
     uint32_t bad = 0;
     if (c0 < 0 || c1 < c0 || c1 > a.max_num_tokens)
         bad = RPA_DEV_ERR_TOKENS;
-    else if (ql > kl)
+    else if (a.causal && ql > kl)
         bad = RPA_DEV_ERR_Q_LEN;
-    else if (cdiv(kl, a.page_size) > a.pages_per_seq)
+    else if (kl < 0 || (kl > 0 && (kl - 1) / a.page_size >= a.pages_per_seq))
         bad = RPA_DEV_ERR_KV_LEN;
     if (bad) {
         set_error(&a.hdr->error_bits, bad);
         return false;
     }
-    return true;
+    return kl > 0 || a.causal;  // (cross attention without a key: the plan's other blocks write the zeros)
 }
 
 // Sequence of token t: the last s in [0, num) with cu[s] <= t (cu = cu_q_lens, in global or
@@ -350,6 +352,12 @@ __device__ __forceinline__ int seq_of_token(const int32_t* cu, int num, int t) {
 __device__ __forceinline__ bool kind_allows(const RpaArgs& a, bool decode_class) {
     return !(a.batch_kind == RPA_BATCH_DECODE_ONLY && !decode_class) &&
            !(a.batch_kind == RPA_BATCH_PREFILL_ONLY && decode_class);
+}
+
+// Position of the query token `tok` of a sequence: the last key it sees (cross attention: the last
+// key there is).
+__device__ __forceinline__ int query_pos(const RpaArgs& a, int ql, int kl, int tok) {
+    return kl - 1 - (a.causal ? ql - 1 - tok : 0);
 }
 
 // First key any query of a decode-class sequence can see (aligned down to a stage).

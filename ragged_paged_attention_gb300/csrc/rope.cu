@@ -57,6 +57,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_apply_kernel(const __grid_c
 template <int VEC, int KV>
 __global__ void __launch_bounds__(kRopeThreads) rpa_rope_update_kernel(const __grid_constant__ RopeUpdateArgs a) {
     const int warps = gridDim.x * (kRopeThreads / 32);
+    // an rpa_forward plan kernel behind may start now: it reads only metadata this kernel does
+    // not write, and it ends after this grid has
+    pdl_launch_dependents();
     int num = a.num_seqs[0];
     if (num < 0 || num > a.max_num_seqs) {
         if (blockIdx.x == 0 && threadIdx.x == 0) set_error(a.err, RPA_DEV_ERR_NUM_SEQS);

@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(DecTile<D, HG, ESZ, CONV, F16, I4>::kThreads) 
             for (int j = 0; j < 2; ++j) {
                 const int R = rb + 2 * q4 + j;
                 rv[j] = head_ok && R < n_rows;
-                qpos[j] = rv[j] ? kv_len - q_len + R / G : -1;
+                qpos[j] = rv[j] ? query_pos(a, q_len, kv_len, R / G) : -1;
                 wlo[j] = a.sliding_window > 0 ? qpos[j] - a.sliding_window + 1 : 0;
             }
             const int Rb = rb + g8;

@@ -84,7 +84,7 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
                 ngrp += g;
             } else {
                 // causal: query i of the chunk sees kl - ql + i + 1 keys (at most the window)
-                float seen = (float)kl - 0.5f * (float)(ql - 1);
+                float seen = (float)kl - (a.causal ? 0.5f * (float)(ql - 1) : 0.f);
                 if (a.sliding_window > 0) seen = fminf(seen, (float)a.sliding_window);
                 pre_pairs += (float)ql * seen;
             }
@@ -348,6 +348,31 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
 
 __global__ void __launch_bounds__(1024) rpa_plan_kernel(RpaArgs a) { plan_body(a); }
 
+// Cross attention: block 0 plans, the others write the zero rows of sequences without keys (which
+// the plan leaves out). They wait for the stream's earlier work first: it may still use `out`.
+__global__ void __launch_bounds__(1024) rpa_cross_plan_kernel(RpaArgs a) {
+    if (blockIdx.x == 0) {
+        plan_body(a);
+        return;
+    }
+    pdl_launch_dependents();
+    const int num = a.num_seqs[0];
+    if (num < 0 || num > a.max_num_seqs) return;  // (block 0 records it)
+    bool waited = false;
+    for (int s = 0; s < num; ++s) {
+        if (a.kv_lens[s] != 0) continue;
+        const int c0 = a.cu_q_lens[s], c1 = a.cu_q_lens[s + 1];
+        if (c0 < 0 || c1 < c0 || c1 > a.max_num_tokens) continue;
+        if (!waited) pdl_wait();
+        waited = true;
+        const size_t row = (size_t)a.num_q_heads * a.head_dim / 8;  // a token's 16-byte chunks
+        uint4* out = reinterpret_cast<uint4*>(a.out);
+        for (size_t i = c0 * row + (blockIdx.x - 1) * blockDim.x + threadIdx.x; i < c1 * row;
+             i += (size_t)(gridDim.x - 1) * blockDim.x)
+            out[i] = make_uint4(0, 0, 0, 0);
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Cache write: new K/V rows -> their page slots (16-byte copies, bit exact)
 // ---------------------------------------------------------------------------
@@ -501,7 +526,10 @@ cudaError_t launch_rpa_forward(const RpaArgs& a, int num_sms, cudaStream_t strea
     cudaError_t e;
     {
         ProfScope ps("rpa_plan", stream);
-        e = launch_pdl(rpa_plan_kernel, dim3(1), dim3(1024), 0, stream, a.overlap != 0, a);
+        if (a.causal)
+            e = launch_pdl(rpa_plan_kernel, dim3(1), dim3(1024), 0, stream, a.overlap != 0, a);
+        else
+            e = launch_pdl(rpa_cross_plan_kernel, dim3(1 + kCrossZeroBlocks), dim3(1024), 0, stream, a.overlap != 0, a);
     }
     if (e != cudaSuccess) return e;
     return launch_attention(a, num_sms, stream);

@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(prefill_warps<RAW>() * 32, 1)
         const int kvh = w.head;
         const int R0 = w.row_begin;
         const int R1 = min(n_rows, R0 + 128) - 1;
-        const int qmin = kv_len - q_len + R0 / G, qmax = kv_len - q_len + R1 / G;
+        const int qmin = query_pos(a, q_len, kv_len, R0 / G), qmax = query_pos(a, q_len, kv_len, R1 / G);
         // keys the tile's rows see: the causal (windowed) range, or every key with a mild mask
         int kb = a.sliding_window > 0 && !MILD ? max(0, qmin - a.sliding_window + 1) : 0;
         kb = kb / BK * BK;
@@ -884,7 +884,7 @@ __global__ void __launch_bounds__(prefill_warps<RAW>() * 32, 1)
             const int r = quarter * 32 + lane;
             const int R = R0 + r;
             const bool rv = R < n_rows;
-            const int qpos = rv ? kv_len - q_len + R / G : -1;
+            const int qpos = rv ? query_pos(a, q_len, kv_len, R / G) : -1;
             const int wlo = a.sliding_window > 0 ? qpos - a.sliding_window + 1 : INT_MIN;
             const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
             // kv_len is needed again only by a mild mask: this warp's copy waits in shared memory
