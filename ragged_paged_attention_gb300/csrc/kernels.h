@@ -241,8 +241,16 @@ struct RopeRows {
     long long token, head;
 };
 
+// How the head rows of one kind (q, k or v) are cut into block shares: `tokens` whole tokens each, or
+// (parts > 1) `heads` heads of one token; `blocks` shares in all.
+struct RopeShare {
+    int tokens, heads, parts;
+    unsigned blocks;
+};
+
 struct RopeApplyArgs {
     RopeTab tab;
+    RopeShare q_share, k_share;     // set by the launch
     RopeRows q, k, q_out, k_out;
     const int32_t* positions;
     int num_tokens, num_q_heads, num_k_heads, head_dim;
@@ -250,6 +258,7 @@ struct RopeApplyArgs {
 
 struct RopeUpdateArgs {
     RopeTab tab;
+    RopeShare q_share, kv_share;    // set by the launch (k and v are cut alike)
     RopeRows q, k, v;               // no q: num_q_heads 0
     __nv_bfloat16* q_out;           // [max_num_tokens, num_q_heads, head_dim]
     void* kv_pages;
@@ -265,8 +274,8 @@ struct RopeUpdateArgs {
     int total_num_pages, page_size, max_num_seqs, pages_per_seq;
 };
 
-cudaError_t launch_rope_apply(const RopeApplyArgs& a, int num_sms, cudaStream_t stream);
-cudaError_t launch_rope_update(const RopeUpdateArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_rope_apply(RopeApplyArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_rope_update(RopeUpdateArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_rpa_forward(const RpaArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_wait_selftest(uint32_t* err, cudaStream_t stream);
 cudaError_t launch_rpa_forward_update(const RpaArgs& a, const RpaUpdateArgs& u, int num_sms, cudaStream_t stream);

@@ -1,9 +1,7 @@
 // Rotary positions (rope_apply) and the cache write that turns its keys (rpa_rope_update_kv_cache),
 // for sm_103a.
 //
-// Both only move memory: a turned element costs two fused multiply-adds against four bytes.  One
-// warp takes one token: its lanes stand for the units of a head (rope.cuh) and of the heads beside
-// it, keep their sines and cosines, and walk over the token's heads.
+// Both only move memory: a turned element costs two fused multiply-adds against four bytes.
 #include "common.cuh"
 #include "kernels.h"
 #include "profile.h"
@@ -11,10 +9,8 @@
 
 namespace rpa {
 
-constexpr int kRopeThreads = 256;
-
-// Calls body(u, turns, cs, head) for every unit u of `heads` heads of head_dim elements, with the
-// cosines and sines of the unit's pairs at `pos` where it turns.
+// The narrow path (rotary_dim not a multiple of 16): calls body(u, turns, cs, head) for every unit u
+// of heads [h_begin, h_end) of head_dim elements.
 template <int VEC, typename F>
 __device__ __forceinline__ void rope_units(const RopeTab& tab, int head_dim, int heads, int pos, F&& body) {
     const int lane = threadIdx.x & 31, units = head_dim / (2 * VEC);
@@ -30,107 +26,265 @@ __device__ __forceinline__ void rope_units(const RopeTab& tab, int head_dim, int
     }
 }
 
+// The rows of head h of token t: q's heads, then k's.
+__device__ __forceinline__ const __nv_bfloat16* apply_in(const RopeApplyArgs& a, int t, int h) {
+    const int hk = h - a.num_q_heads;
+    return hk < 0 ? a.q.p + t * a.q.token + h * a.q.head : a.k.p + t * a.k.token + hk * a.k.head;
+}
+__device__ __forceinline__ __nv_bfloat16* apply_out(const RopeApplyArgs& a, int t, int h) {
+    const int hk = h - a.num_q_heads;
+    return hk < 0 ? a.q_out.p + t * a.q_out.token + h * a.q_out.head : a.k_out.p + t * a.k_out.token + hk * a.k_out.head;
+}
+
+// A unit's chunks turned in bf16.
+template <bool INTER>
+__device__ __forceinline__ void turn_chunks(uint4& xa, uint4& xb, const float4* cs, int stride) {
+    float x[16];
+    rope_unpack<8>(xa, x);
+    rope_unpack<8>(xb, x + 8);
+    rope_turn8<INTER>(cs, stride, x);
+    xa = rope_pack<8>(x);
+    xb = rope_pack<8>(x + 8);
+}
+
+template <bool INTER>
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rope_apply_kernel(const __grid_constant__ RopeApplyArgs a) {
+    __shared__ RopeShared sh;
+    const bool is_k = blockIdx.x >= a.q_share.blocks;
+    const RopeRows& to = is_k ? a.k_out : a.q_out;
+    rope_block<true, INTER>(
+        a.tab, is_k ? a.k_share : a.q_share, is_k ? blockIdx.x - a.q_share.blocks : blockIdx.x, a.head_dim, a.num_tokens,
+        is_k ? a.k : a.q, is_k ? a.num_k_heads : a.num_q_heads, sh,
+        [&](int t0, int nt) {
+            if (threadIdx.x < nt) sh.pos[threadIdx.x] = a.positions[t0 + threadIdx.x];
+        },
+        [&](int, int t, int h, bool turns, int ca, int cb, uint4 xa, uint4 xb, const float4* cs, int stride) {
+            if (turns) turn_chunks<INTER>(xa, xb, cs, stride);
+            __nv_bfloat16* dst = to.p + t * to.token + h * to.head;
+            *reinterpret_cast<uint4*>(dst + ca) = xa;
+            *reinterpret_cast<uint4*>(dst + cb) = xb;
+        });
+}
+
 template <int VEC>
-__global__ void __launch_bounds__(kRopeThreads) rope_apply_kernel(const __grid_constant__ RopeApplyArgs a) {
-    const int warps = gridDim.x * (kRopeThreads / 32);
-    for (int t = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5); t < a.num_tokens; t += warps) {
-        const int pos = a.positions[t];
-        rope_units<VEC>(a.tab, a.head_dim, a.num_q_heads + a.num_k_heads, pos,
-                        [&](int u, bool turns, const float2 (&cs)[VEC], int h) {
-                            const bool is_k = h >= a.num_q_heads;
-                            const int hh = is_k ? h - a.num_q_heads : h;
-                            const RopeRows &in = is_k ? a.k : a.q, &out = is_k ? a.k_out : a.q_out;
-                            const __nv_bfloat16* src = in.p + t * in.token + hh * in.head;
-                            __nv_bfloat16* dst = out.p + t * out.token + hh * out.head;
-                            int ca, cb;
-                            rope_chunks<VEC>(a.tab, u, turns, ca, cb);
+__global__ void __launch_bounds__(kRopeThreads) rope_apply_narrow_kernel(const __grid_constant__ RopeApplyArgs a) {
+    using Chunk = typename RopeChunk<VEC>::type;
+    const unsigned w = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
+    const int t = (int)w;
+    if (w >= (unsigned)a.num_tokens) return;
+    rope_units<VEC>(a.tab, a.head_dim, a.num_q_heads + a.num_k_heads, a.positions[t],
+                    [&](int u, bool turns, const float2 (&cs)[VEC], int h) {
+                        int ca, cb;
+                        rope_chunks<VEC>(a.tab.rotary_dim, a.tab.interleaved, u, turns, ca, cb);
+                        const __nv_bfloat16* src = apply_in(a, t, h);
+                        Chunk xa = *reinterpret_cast<const Chunk*>(src + ca), xb = *reinterpret_cast<const Chunk*>(src + cb);
+                        if (turns) {
                             float x[2 * VEC];
-                            load_bf16<VEC>(src + ca, x);
-                            load_bf16<VEC>(src + cb, x + VEC);
-                            if (turns) rope_turn<VEC>(a.tab.interleaved, cs, x);
-                            store_bf16<VEC>(dst + ca, x);
-                            store_bf16<VEC>(dst + cb, x + VEC);
-                        });
+                            rope_unpack<VEC>(xa, x);
+                            rope_unpack<VEC>(xb, x + VEC);
+                            rope_turn<VEC>(a.tab.interleaved, cs, x);
+                            xa = rope_pack<VEC>(x);
+                            xb = rope_pack<VEC>(x + VEC);
+                        }
+                        __nv_bfloat16* dst = apply_out(a, t, h);
+                        *reinterpret_cast<Chunk*>(dst + ca) = xa;
+                        *reinterpret_cast<Chunk*>(dst + cb) = xb;
+                    });
+}
+
+// The source row of head h of token t: q's heads, then k's, then v's.
+__device__ __forceinline__ const __nv_bfloat16* update_in(const RopeUpdateArgs& a, int t, int h) {
+    const int hk = h - a.num_q_heads, hv = hk - a.num_kv_heads;
+    return hk < 0 ? a.q.p + t * a.q.token + h * a.q.head
+                  : hv < 0 ? a.k.p + t * a.k.token + hk * a.k.head : a.v.p + t * a.v.token + hv * a.v.head;
+}
+// A unit's values to q_out or to the token's slot of the cache; turn(x) turns them (v turns nothing:
+// its chunks are copied in the same order).
+template <int VEC, int KV, typename Turn>
+__device__ __forceinline__ void update_out(const RopeUpdateArgs& a, int t, int h, uint8_t* slot, bool turns, int ca, int cb,
+                                           typename RopeChunk<VEC>::type xa, typename RopeChunk<VEC>::type xb, Turn&& turn) {
+    using Chunk = typename RopeChunk<VEC>::type;
+    const int hk = h - a.num_q_heads, hv = hk - a.num_kv_heads;
+    const float inv = hv < 0 ? a.k_inv : a.v_inv;
+    const bool convert = hk >= 0 && (KV != RPA_DTYPE_BF16 || inv != 1.f);
+    turns = turns && hv < 0;
+    uint8_t* cache = slot + (hv < 0 ? 2 * hk : 2 * hv + 1) * a.row_bytes;
+    float x[2 * VEC];
+    if (turns || convert) {
+        rope_unpack<VEC>(xa, x);
+        rope_unpack<VEC>(xb, x + VEC);
+        if (turns) turn(x);
+        if (convert) {
+            rope_store_kv<KV, VEC>(cache, ca, x, inv);
+            rope_store_kv<KV, VEC>(cache, cb, x + VEC, inv);
+            return;
+        }
+        xa = rope_pack<VEC>(x);
+        xb = rope_pack<VEC>(x + VEC);
+    }
+    __nv_bfloat16* dst = hk < 0 ? a.q_out + ((size_t)t * a.num_q_heads + h) * a.head_dim : reinterpret_cast<__nv_bfloat16*>(cache);
+    *reinterpret_cast<Chunk*>(dst + ca) = xa;
+    *reinterpret_cast<Chunk*>(dst + cb) = xb;
+}
+
+template <bool INTER, int KV>
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rpa_rope_update_kernel(const __grid_constant__ RopeUpdateArgs a) {
+    __shared__ RopeShared sh;
+    // an rpa_forward plan kernel behind may start now: it reads only metadata this kernel does
+    // not write, and it ends after this grid has
+    pdl_launch_dependents();
+    auto resolve = [&](int t0, int nt) {
+        for (int k = threadIdx.x >> 5; k < nt; k += kRopeWarps) {  // a warp a token
+            int pos = 0;
+            uint8_t* slot = nullptr;
+            if (!rope_slot(a, t0 + k, pos, slot)) slot = nullptr;
+            if (a.positions) pos = a.positions[t0 + k];
+            if ((threadIdx.x & 31) == 0) {
+                sh.pos[k] = pos;
+                sh.slot[k] = slot;
+            }
+        }
+    };
+    unsigned share = blockIdx.x;
+    if (share < a.q_share.blocks) {
+        rope_block<true, INTER>(
+            a.tab, a.q_share, share, a.head_dim, a.max_num_tokens, a.q, a.num_q_heads, sh, resolve,
+            [&](int k, int t, int h, bool turns, int ca, int cb, uint4 xa, uint4 xb, const float4* cs, int stride) {
+                if (!sh.slot[k]) return;
+                if (turns) turn_chunks<INTER>(xa, xb, cs, stride);
+                __nv_bfloat16* dst = a.q_out + ((size_t)t * a.num_q_heads + h) * a.head_dim;
+                *reinterpret_cast<uint4*>(dst + ca) = xa;
+                *reinterpret_cast<uint4*>(dst + cb) = xb;
+            });
+        return;
+    }
+    // a unit of k (part 0) or v (part 1) to the cache
+    auto put = [&](int part, int k, int h, bool turns, int ca, int cb, uint4 xa, uint4 xb, const float4* cs, int stride, float inv) {
+        uint8_t* slot = sh.slot[k];
+        if (!slot) return;
+        uint8_t* row = slot + (2 * h + part) * a.row_bytes;
+        if (KV != RPA_DTYPE_BF16 || inv != 1.f) {
+            float x[16];
+            rope_unpack<8>(xa, x);
+            rope_unpack<8>(xb, x + 8);
+            if (turns) rope_turn8<INTER>(cs, stride, x);
+            rope_store_kv<KV, 8>(row, ca, x, inv);
+            rope_store_kv<KV, 8>(row, cb, x + 8, inv);
+        } else {
+            if (turns) turn_chunks<INTER>(xa, xb, cs, stride);
+            *reinterpret_cast<uint4*>(row + 2 * ca) = xa;
+            *reinterpret_cast<uint4*>(row + 2 * cb) = xb;
+        }
+    };
+    share -= a.q_share.blocks;
+    if (share < a.kv_share.blocks) {
+        rope_block<true, INTER>(a.tab, a.kv_share, share, a.head_dim, a.max_num_tokens, a.k, a.num_kv_heads, sh, resolve,
+                                [&](int k, int, int h, bool turns, int ca, int cb, uint4 xa, uint4 xb, const float4* cs, int stride) {
+                                    put(0, k, h, turns, ca, cb, xa, xb, cs, stride, a.k_inv);
+                                });
+    } else {
+        rope_block<false, INTER>(a.tab, a.kv_share, share - a.kv_share.blocks, a.head_dim, a.max_num_tokens, a.v,
+                                 a.num_kv_heads, sh, resolve,
+                                 [&](int k, int, int h, bool, int ca, int cb, uint4 xa, uint4 xb, const float4* cs, int stride) {
+                                     put(1, k, h, false, ca, cb, xa, xb, cs, stride, a.v_inv);
+                                 });
     }
 }
 
 template <int VEC, int KV>
-__global__ void __launch_bounds__(kRopeThreads) rpa_rope_update_kernel(const __grid_constant__ RopeUpdateArgs a) {
-    const int warps = gridDim.x * (kRopeThreads / 32);
-    // an rpa_forward plan kernel behind may start now: it reads only metadata this kernel does
-    // not write, and it ends after this grid has
-    pdl_launch_dependents();
-    int num = a.num_seqs[0];
-    if (num < 0 || num > a.max_num_seqs) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) set_error(a.err, RPA_DEV_ERR_NUM_SEQS);
-        return;
-    }
-    const int hq = a.num_q_heads, hkv = a.num_kv_heads;
-    for (int t = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5); t < a.max_num_tokens; t += warps) {
-        int pos;
-        size_t slot;
-        if (!rope_slot(a, num, t, pos, slot)) continue;
-        if (a.positions) pos = a.positions[t];
-        rope_units<VEC>(a.tab, a.head_dim, hq + 2 * hkv, pos,
-                        [&](int u, bool turns, const float2 (&cs)[VEC], int h) {
-                            const int kind = h < hq ? 0 : h < hq + hkv ? 1 : 2;  // q, k, v
-                            const int hh = kind == 0 ? h : kind == 1 ? h - hq : h - hq - hkv;
-                            const RopeRows& in = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
-                            const __nv_bfloat16* src = in.p + t * in.token + hh * in.head;
-                            int ca, cb;
-                            rope_chunks<VEC>(a.tab, u, turns && kind < 2, ca, cb);
-                            float x[2 * VEC];
-                            load_bf16<VEC>(src + ca, x);
-                            load_bf16<VEC>(src + cb, x + VEC);
-                            if (turns && kind < 2) rope_turn<VEC>(a.tab.interleaved, cs, x);
-                            if (kind == 0) {
-                                __nv_bfloat16* dst = a.q_out + ((size_t)t * hq + hh) * a.head_dim;
-                                store_bf16<VEC>(dst + ca, x);
-                                store_bf16<VEC>(dst + cb, x + VEC);
-                            } else {
-                                uint8_t* row = static_cast<uint8_t*>(a.kv_pages) +
-                                               (slot * 2 * hkv + 2 * hh + (kind - 1)) * (size_t)a.row_bytes;
-                                const float inv = kind == 1 ? a.k_inv : a.v_inv;
-                                store_kv<KV, VEC>(row, ca, x, inv);
-                                store_kv<KV, VEC>(row, cb, x + VEC, inv);
-                            }
-                        });
-    }
+__global__ void __launch_bounds__(kRopeThreads) rpa_rope_update_narrow_kernel(const __grid_constant__ RopeUpdateArgs a) {
+    using Chunk = typename RopeChunk<VEC>::type;
+    pdl_launch_dependents();  // as above
+    const unsigned w = blockIdx.x * kRopeWarps + (threadIdx.x >> 5);
+    const int t = (int)w;
+    if (w >= (unsigned)a.max_num_tokens) return;
+    int pos;
+    uint8_t* slot;
+    if (!rope_slot(a, t, pos, slot)) return;
+    if (a.positions) pos = a.positions[t];
+    rope_units<VEC>(a.tab, a.head_dim, a.num_q_heads + 2 * a.num_kv_heads, pos,
+                    [&](int u, bool turns, const float2 (&cs)[VEC], int h) {
+                        int ca, cb;
+                        rope_chunks<VEC>(a.tab.rotary_dim, a.tab.interleaved, u, turns, ca, cb);
+                        const __nv_bfloat16* src = update_in(a, t, h);
+                        update_out<VEC, KV>(a, t, h, slot, turns, ca, cb, *reinterpret_cast<const Chunk*>(src + ca),
+                                            *reinterpret_cast<const Chunk*>(src + cb),
+                                            [&](float (&x)[2 * VEC]) { rope_turn<VEC>(a.tab.interleaved, cs, x); });
+                    });
 }
 
-// Pairs per unit: 2 where the turned part's halves start on even elements.
-static int rope_vec(const RopeTab& t) { return t.rotary_dim % 4 == 0 ? 2 : 1; }
+constexpr int kRopePasses = 5, kRopeBlocks = 16;
 
-static int rope_grid(int tokens, int num_sms) {
-    return min(cdiv(tokens, kRopeThreads / 32), num_sms * (2048 / kRopeThreads));
+// Elements per chunk: 16 bytes where the turned part's halves are whole chunks, else two elements
+// or one.
+static int rope_vec(const RopeTab& t) { return t.rotary_dim % 16 == 0 ? 8 : t.rotary_dim % 4 == 0 ? 2 : 1; }
+
+// The shares of one kind, whose rows are some of all `total` head rows of a token.  A block finds its
+// tokens' slots and sines before it can store, some 2 us, so it wants several passes over its threads
+// (kRopePasses); more than kRopeBlocks blocks an SM only repeat that; and a small call is spread over
+// every SM twice, by tokens and then by heads.
+static RopeShare rope_share(const RopeTab& tab, int tokens, int heads, int total, int head_dim, int num_sms) {
+    const int rows = kRopeThreads / (head_dim / 16);  // head rows a block holds at once
+    const int most = min(kRopeTokens, tab.rotary_dim ? kRopePairs / (tab.rotary_dim / 2) : kRopeTokens);
+    RopeShare s = {1, heads, 1, 0};
+    if (heads == 0) return s;
+    const double all = (double)tokens * total;
+    const double share = min(max(kRopePasses * (double)rows, all / (kRopeBlocks * num_sms)), all / (2 * num_sms));
+    s.tokens = max(1, min(most, (int)min(share / heads, 1e6)));
+    s.parts = max(1, min(cdiv(heads, rows), (int)(heads / max(share, 1.0))));
+    s.heads = cdiv(heads, s.parts);
+    s.parts = cdiv(heads, s.heads);
+    s.blocks = (unsigned)(((long long)tokens + s.tokens - 1) / s.tokens * s.parts);
+    return s;
 }
 
-cudaError_t launch_rope_apply(const RopeApplyArgs& a, int num_sms, cudaStream_t stream) {
-    if (a.num_tokens <= 0) return cudaSuccess;
+// Blocks of kRopeWarps warps.
+static unsigned rope_blocks(long long warps) { return (unsigned)((warps + kRopeWarps - 1) / kRopeWarps); }
+
+cudaError_t launch_rope_apply(RopeApplyArgs& a, int num_sms, cudaStream_t stream) {
     ProfScope ps("rope_apply", stream);
-    const int grid = rope_grid(a.num_tokens, num_sms);
-    if (rope_vec(a.tab) == 2)
-        rope_apply_kernel<2><<<grid, kRopeThreads, 0, stream>>>(a);
-    else
-        rope_apply_kernel<1><<<grid, kRopeThreads, 0, stream>>>(a);
+    const int vec = rope_vec(a.tab);
+    if (vec == 8) {
+        const int heads = a.num_q_heads + a.num_k_heads;
+        a.q_share = rope_share(a.tab, a.num_tokens, a.num_q_heads, heads, a.head_dim, num_sms);
+        a.k_share = rope_share(a.tab, a.num_tokens, a.num_k_heads, heads, a.head_dim, num_sms);
+        const unsigned grid = a.q_share.blocks + a.k_share.blocks;
+        if (a.tab.interleaved)
+            rope_apply_kernel<true><<<grid, kRopeThreads, 0, stream>>>(a);
+        else
+            rope_apply_kernel<false><<<grid, kRopeThreads, 0, stream>>>(a);
+    } else if (vec == 2) {
+        rope_apply_narrow_kernel<2><<<rope_blocks(a.num_tokens), kRopeThreads, 0, stream>>>(a);
+    } else {
+        rope_apply_narrow_kernel<1><<<rope_blocks(a.num_tokens), kRopeThreads, 0, stream>>>(a);
+    }
     return cudaGetLastError();
 }
 
 template <int KV>
-static cudaError_t launch_update_kv(const RopeUpdateArgs& a, int num_sms, cudaStream_t stream) {
-    const int grid = rope_grid(a.max_num_tokens, num_sms);
-    if (rope_vec(a.tab) == 2) {
-        rpa_rope_update_kernel<2, KV><<<grid, kRopeThreads, 0, stream>>>(a);
+static cudaError_t launch_update_kv(RopeUpdateArgs& a, int num_sms, cudaStream_t stream) {
+    const int vec = rope_vec(a.tab);
+    if (vec == 8) {
+        const int heads = a.num_q_heads + 2 * a.num_kv_heads;
+        a.q_share = rope_share(a.tab, a.max_num_tokens, a.num_q_heads, heads, a.head_dim, num_sms);
+        a.kv_share = rope_share(a.tab, a.max_num_tokens, a.num_kv_heads, heads, a.head_dim, num_sms);
+        const unsigned grid = a.q_share.blocks + 2 * a.kv_share.blocks;
+        if (a.tab.interleaved)
+            rpa_rope_update_kernel<true, KV><<<grid, kRopeThreads, 0, stream>>>(a);
+        else
+            rpa_rope_update_kernel<false, KV><<<grid, kRopeThreads, 0, stream>>>(a);
+    } else if (vec == 2) {
+        rpa_rope_update_narrow_kernel<2, KV><<<rope_blocks(a.max_num_tokens), kRopeThreads, 0, stream>>>(a);
     } else {
         if constexpr (KV == RPA_DTYPE_INT4)
             return cudaErrorInvalidValue;  // (the host refuses it)
         else
-            rpa_rope_update_kernel<1, KV><<<grid, kRopeThreads, 0, stream>>>(a);
+            rpa_rope_update_narrow_kernel<1, KV><<<rope_blocks(a.max_num_tokens), kRopeThreads, 0, stream>>>(a);
     }
     return cudaGetLastError();
 }
 
-cudaError_t launch_rope_update(const RopeUpdateArgs& a, int num_sms, cudaStream_t stream) {
+cudaError_t launch_rope_update(RopeUpdateArgs& a, int num_sms, cudaStream_t stream) {
     ProfScope ps("rpa_rope_update", stream);
     switch (a.kv_dtype) {
         case RPA_DTYPE_BF16: return launch_update_kv<RPA_DTYPE_BF16>(a, num_sms, stream);
