@@ -217,15 +217,24 @@ class Workspace:
         return buf
 
 
-def _own_workspace(nbytes: int, device: torch.device, tag: str) -> torch.Tensor:
-    """The workspace of a call that was given none: one per device, stream and purpose, so that calls on
-    two streams share none; while the stream is captured a new one, owned by the graph.  Of that one only
-    the header, with the error word, is zeroed on every replay: the plan writes the rest before it is read."""
+_workspaces: dict = {}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
+def _own_workspace(nbytes: int, device: int, stream: int) -> torch.Tensor:
+    """The workspace of an attention call that was given none: one per device, stream and thread, so that
+    calls that overlap share none; while the stream is captured a new one, owned by the graph.  Of that
+    one only the header, with the error word, is zeroed on every replay: the plan writes the rest before
+    it is read."""
     if torch.cuda.is_current_stream_capturing():
         ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
         ws[:256].zero_()
         return ws
-    return Workspace.get(nbytes, device, f"{tag} {torch.cuda.current_stream(device).cuda_stream}")
+    key = (device, stream, threading.get_ident())
+    ws = _workspaces.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = _workspaces[key] = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    return ws
 
 
 def _kv_code(dtype) -> int:
@@ -428,16 +437,16 @@ def make_rope_table(rotary_dim, *, base=10000.0, interleaved=False, scaling=None
     return t
 
 
-def _rows(t: torch.Tensor, name: str, heads=None, dim=None):
-    """(token stride, head stride) of bf16 rows [tokens, heads, head_dim] on the GPU; any strides with
-    adjacent elements and 16-byte aligned rows."""
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16 or t.dim() != 3:
+def _rows(t, name: str, device: int, heads: int = 0, dim: int = 0):
+    """(token stride, head stride) of bf16 rows [tokens, heads, head_dim] on ``device``; any strides with
+    adjacent elements and 16-byte aligned rows.  ``heads`` and ``dim``, where given, must match."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != device or device < 0:
+        raise ValueError(f"{name} must be a CUDA tensor on device {device}")
+    if t.dtype is not torch.bfloat16 or t.dim() != 3:
         raise ValueError(f"{name} must be bfloat16 [tokens, heads, head_dim], got {t.dtype} {tuple(t.shape)}")
     n, h, d = t.shape
-    if (heads is not None and h != heads) or (dim is not None and d != dim):
-        raise ValueError(f"{name} must have {heads} heads of {dim}, got {tuple(t.shape)}")
+    if (heads and h != heads) or (dim and d != dim):
+        raise ValueError(f"{name} must have {heads or h} heads of {dim or d}, got {tuple(t.shape)}")
     token, head, element = t.stride()
     if h <= 1:  # the stride of a dimension of one entry says nothing
         head = d
@@ -449,19 +458,20 @@ def _rows(t: torch.Tensor, name: str, heads=None, dim=None):
     return token, head
 
 
-def _same_device(first: torch.Tensor, *others):
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors are on {first.device} and {t.device}")
+def _on(device: int, t, name: str, dtype, n: int = -1):
+    """Checks a contiguous tensor of ``dtype`` on ``device`` (of ``n`` elements, where given)."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != device or device < 0:
+        raise ValueError(f"{name} must be a CUDA tensor on device {device}")
+    if t.dtype is not dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype}, got {t.dtype}")
+    if n >= 0 and t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements, got shape {tuple(t.shape)}")
 
 
-def _launch(device: torch.device, call):
-    """call(stream) with ``device`` current, on its current stream."""
-    if device.index == torch.cuda.current_device():
-        _check(call(_stream()))
-    else:
-        with torch.cuda.device(device):
-            _check(call(_stream()))
+def _cuda_index(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
 
 
 def _is_table(table):
@@ -474,71 +484,95 @@ def rope_apply(q, k, positions, table, *, inverse=False, q_out=None, k_out=None)
 
     q and k are bf16 with any token and head strides; ``q_out=q`` and ``k_out=k`` work in place.
     ``inverse`` turns back by the same angles (the map of an output's gradient to the input's)."""
-    lib = load_library()
+    lib = _lib or load_library()
     _is_table(table)
-    q_token, q_head = _rows(q, "q")
+    dev = _cuda_index(q, "q")
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return rope_apply(q, k, positions, table, inverse=inverse, q_out=q_out, k_out=k_out)
+    q_token, q_head = _rows(q, "q", dev)
     T, hq, d = q.shape
-    _dev(positions, "positions", torch.int32)
-    if positions.shape != (T,):
-        raise ValueError(f"positions must be [{T}], got {tuple(positions.shape)}")
-    q_out = torch.empty((T, hq, d), dtype=q.dtype, device=q.device) if q_out is None else q_out
+    _on(dev, positions, "positions", torch.int32, T)
+    if q_out is None:
+        q_out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=q.device)
+    qo_token, qo_head = (q_token, q_head) if q_out is q else _rows(q_out, "q_out", dev)
     if q_out.shape != q.shape:
         raise ValueError(f"q_out must have q's shape {tuple(q.shape)}, got {tuple(q_out.shape)}")
-    qo_token, qo_head = _rows(q_out, "q_out")
     hk = k_token = k_head = ko_token = ko_head = 0
     if k is not None:
-        k_token, k_head = _rows(k, "k", dim=d)
+        k_token, k_head = _rows(k, "k", dev, 0, d)
         hk = k.shape[1]
-        k_out = torch.empty((T, hk, d), dtype=k.dtype, device=k.device) if k_out is None else k_out
+        if k_out is None:
+            k_out = torch.empty((T, hk, d), dtype=torch.bfloat16, device=q.device)
+        ko_token, ko_head = (k_token, k_head) if k_out is k else _rows(k_out, "k_out", dev)
         if k.shape[0] != T or k_out.shape != k.shape:
             raise ValueError(f"k and k_out must be [{T}, heads, {d}], got {tuple(k.shape)} and {tuple(k_out.shape)}")
-        ko_token, ko_head = _rows(k_out, "k_out")
     elif k_out is not None:
         raise ValueError("k_out goes with k")
-    _same_device(q, k, positions, q_out, k_out)
     if T == 0:
         return q_out, k_out
-    prm = rope_apply_params(ctypes.sizeof(rope_apply_params), ABI_VERSION, T, hq, hk, d, 1 if inverse else 0, 0, q_token,
-                            q_head, k_token, k_head, qo_token, qo_head, ko_token, ko_head)
-    _launch(q.device, lambda stream: lib.rope_apply(ctypes.byref(prm), ctypes.byref(table), _ptr(q), _ptr(k),
-                                                    _ptr(positions), _ptr(q_out), _ptr(k_out), stream))
+    prm = rope_apply_params(_APPLY_SIZE, ABI_VERSION, T, hq, hk, d, 1 if inverse else 0, 0, q_token, q_head, k_token, k_head,
+                            qo_token, qo_head, ko_token, ko_head)
+    rc = lib.rope_apply(ctypes.byref(prm), ctypes.byref(table), q.data_ptr(), k.data_ptr() if hk else None,
+                        positions.data_ptr(), q_out.data_ptr(), k_out.data_ptr() if hk else None, _raw_stream(dev))
+    if rc:
+        _check(rc)
     return q_out, k_out
 
 
-def _rope_update_args(q, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, table, positions, q_out, **opts):
+def _batch_params(dev, tokens, hq, d, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, sm_scale=1.0, sliding_window=None,
+                  soft_cap=None, mask_value=None, k_scale=None, v_scale=None, batch_kind=BATCH_MIXED) -> rpa_params:
+    """rpa_params of a batch of ``tokens`` queries of ``hq`` heads, its cache and metadata checked."""
+    if not isinstance(kv_pages, torch.Tensor) or kv_pages.get_device() != dev or kv_pages.dim() != 4:
+        raise ValueError(f"kv_pages must be [pages, page_size, heads, head_dim] on device {dev}")
+    if not kv_pages.is_contiguous():
+        raise ValueError("kv_pages must be contiguous")
+    code = _kv_code(kv_pages.dtype)
+    pages, ps, combined, width = kv_pages.shape
+    if (width * 2 if code == INT4 else width) != d:
+        raise ValueError(f"kv_pages hold heads of {kv_head_dim(kv_pages)}, the rows {d}")
+    _on(dev, page_indices, "page_indices", torch.int32)
+    if page_indices.dim() != 2:
+        raise ValueError("page_indices must be [max_num_seqs, pages_per_seq]")
+    seqs, pps = page_indices.shape
+    _on(dev, kv_lens, "kv_lens", torch.int32, seqs)
+    _on(dev, cu_q_lens, "cu_q_lens", torch.int32, seqs + 1)
+    _on(dev, num_seqs, "num_seqs", torch.int32, 1)
+    return rpa_params(_PARAMS_SIZE, ABI_VERSION, tokens, hq, combined, d, pages, ps, seqs, pps, BF16, code, sm_scale,
+                      sliding_window or 0, soft_cap or 0.0, math.nan if mask_value is None else mask_value, k_scale or 0.0,
+                      v_scale or 0.0, batch_kind)
+
+
+_PARAMS_SIZE, _APPLY_SIZE, _STRIDES_SIZE = (ctypes.sizeof(x) for x in (rpa_params, rope_apply_params, rope_strides))
+
+
+def _rope_update_args(dev, q, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, table, positions, q_out,
+                      **opts):
     """The checks the appending calls share; (rpa_params, rope_strides, q_out)."""
     _is_table(table)
-    _dev(kv_pages, "kv_pages")
-    for n, t in (("kv_lens", kv_lens), ("page_indices", page_indices), ("cu_q_lens", cu_q_lens),
-                 ("num_seqs", num_seqs)):
-        _dev(t, n, torch.int32)
-    d, hkv = kv_head_dim(kv_pages), kv_pages.shape[2] // 2
-    k_token, k_head = _rows(new_k, "new_k", hkv, d)
-    v_token, v_head = _rows(new_v, "new_v", hkv, d)
-    T = new_k.shape[0]
+    k_token, k_head = _rows(new_k, "new_k", dev)
+    T, hkv, d = new_k.shape
+    v_token, v_head = _rows(new_v, "new_v", dev, hkv, d)
     if new_v.shape[0] != T:
         raise ValueError("new_k and new_v must have the same number of tokens")
     q_token = q_head = 0
     if q is not None:
-        q_token, q_head = _rows(q, "q", dim=d)
+        q_token, q_head = _rows(q, "q", dev, 0, d)
         if q.shape[0] != T:
             raise ValueError("q must have new_k's number of tokens")
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-        _dev(q_out, "q_out", torch.bfloat16)
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        _on(dev, q_out, "q_out", torch.bfloat16)
         if q_out.shape != q.shape:
             raise ValueError(f"q_out must have q's shape {tuple(q.shape)}, got {tuple(q_out.shape)}")
     elif q_out is not None:
         raise ValueError("q_out goes with q")
     if positions is not None:
-        _dev(positions, "positions", torch.int32)
-        if positions.shape != (T,):
-            raise ValueError(f"positions must be [{T}], got {tuple(positions.shape)}")
-    prm = make_rpa_params(new_k if q is None else q, kv_pages, page_indices, **opts)
-    if kv_lens.numel() != prm.max_num_seqs or cu_q_lens.numel() != prm.max_num_seqs + 1 or num_seqs.numel() != 1:
-        raise ValueError("kv_lens must be [max_num_seqs], cu_q_lens [max_num_seqs + 1], num_seqs [1]")
-    _same_device(kv_pages, q, new_k, new_v, kv_lens, page_indices, cu_q_lens, num_seqs, positions, q_out)
-    st = rope_strides(ctypes.sizeof(rope_strides), ABI_VERSION, q_token, q_head, k_token, k_head, v_token, v_head)
-    return prm, st, q_out
+        _on(dev, positions, "positions", torch.int32, T)
+    prm = _batch_params(dev, T, hkv if q is None else q.shape[1], d, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, **opts)
+    if prm.num_combined_kv_heads != 2 * hkv:
+        raise ValueError(f"kv_pages have {prm.num_combined_kv_heads} combined heads, new_k and new_v {hkv} each")
+    return prm, rope_strides(_STRIDES_SIZE, ABI_VERSION, q_token, q_head, k_token, k_head, v_token, v_head), q_out
 
 
 def rpa_rope_update_kv_cache(q, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, table, *,
@@ -550,16 +584,44 @@ def rpa_rope_update_kv_cache(q, new_k, new_v, kv_pages, kv_lens, page_indices, c
     q, new_k and new_v take any token and head strides (slices of one projection's output);
     ``positions`` [T] int32 turns by other positions than the slots' own.  Bad metadata is recorded in
     ``workspace``'s error word where one is given."""
-    lib = load_library()
-    prm, st, q_out = _rope_update_args(q, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, table,
+    lib = _lib or load_library()
+    dev = _cuda_index(new_k, "new_k")
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return rpa_rope_update_kv_cache(q, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, table,
+                                            positions=positions, k_scale=k_scale, v_scale=v_scale, q_out=q_out,
+                                            workspace=workspace)
+    prm, st, q_out = _rope_update_args(dev, q, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, table,
                                        positions, q_out, k_scale=k_scale, v_scale=v_scale)
-    if new_k.shape[0] == 0:
+    if workspace is not None:
+        _on(dev, workspace, "workspace", torch.uint8)
+    if prm.max_num_tokens == 0:
         return q_out, kv_pages
-    _launch(kv_pages.device, lambda stream: lib.rpa_rope_update_kv_cache(
-        ctypes.byref(prm), ctypes.byref(table), ctypes.byref(st), _ptr(q), _ptr(new_k), _ptr(new_v), _ptr(kv_pages),
-        _ptr(kv_lens), _ptr(page_indices), _ptr(cu_q_lens), _ptr(num_seqs), _ptr(positions), _ptr(q_out),
-        _ptr(workspace), 0 if workspace is None else workspace.numel(), stream))
+    rc = lib.rpa_rope_update_kv_cache(
+        ctypes.byref(prm), ctypes.byref(table), ctypes.byref(st), None if q is None else q.data_ptr(), new_k.data_ptr(),
+        new_v.data_ptr(), kv_pages.data_ptr(), kv_lens.data_ptr(), page_indices.data_ptr(), cu_q_lens.data_ptr(),
+        num_seqs.data_ptr(), None if positions is None else positions.data_ptr(), None if q is None else q_out.data_ptr(),
+        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(), _raw_stream(dev))
+    if rc:
+        _check(rc)
     return q_out, kv_pages
+
+
+def _attention_buffers(dev, size, prm, q, out, workspace):
+    """(out, workspace, stream) of an attention call, made where none are given; size: its workspace query."""
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    _on(dev, out, "out", torch.bfloat16)
+    if out.shape != q.shape:
+        raise ValueError(f"out must have q's shape {tuple(q.shape)}, got {tuple(out.shape)}")
+    stream = _raw_stream(dev)
+    if workspace is not None:
+        _on(dev, workspace, "workspace", torch.uint8)
+    elif prm.max_num_tokens:
+        n = ctypes.c_size_t(0)
+        _check(size(ctypes.byref(prm), ctypes.byref(n)))
+        workspace = _own_workspace(n.value, dev, stream)
+    return out, workspace, stream
 
 
 def rpa_rope_forward_update(q, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, table, *,
@@ -567,29 +629,28 @@ def rpa_rope_forward_update(q, new_k, new_v, kv_pages, kv_lens, page_indices, cu
                             k_scale=None, v_scale=None, q_rot=None, out=None, workspace=None, batch_kind=BATCH_MIXED):
     """rpa_rope_update_kv_cache, then rpa_forward of the turned queries (kept in ``q_rot``), in one call;
     writes ``kv_pages`` in place and returns ``out`` [T, Hq, D]."""
-    lib = load_library()
-    if q is None:
-        raise ValueError("q is required")
-    prm, st, q_rot = _rope_update_args(q, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, table,
+    lib = _lib or load_library()
+    dev = _cuda_index(q, "q")
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return rpa_rope_forward_update(q, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, table,
+                                           positions=positions, sm_scale=sm_scale, sliding_window=sliding_window,
+                                           soft_cap=soft_cap, mask_value=mask_value, k_scale=k_scale, v_scale=v_scale,
+                                           q_rot=q_rot, out=out, workspace=workspace, batch_kind=batch_kind)
+    prm, st, q_rot = _rope_update_args(dev, q, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, table,
                                        positions, q_rot, sm_scale=sm_scale, sliding_window=sliding_window,
                                        soft_cap=soft_cap, mask_value=mask_value, k_scale=k_scale, v_scale=v_scale,
                                        batch_kind=batch_kind)
-    out = torch.empty_like(q_rot) if out is None else out
-    _dev(out, "out", torch.bfloat16)
-    if out.shape != q.shape:
-        raise ValueError(f"out must have q's shape {tuple(q.shape)}, got {tuple(out.shape)}")
-    _same_device(kv_pages, out, workspace)
-    if q.shape[0] == 0:
+    out, workspace, stream = _attention_buffers(dev, lib.rpa_workspace_size, prm, q, out, workspace)
+    if prm.max_num_tokens == 0:
         return out
-
-    def call(stream):
-        ws = _own_workspace(rpa_workspace_size(prm), kv_pages.device, "rpa") if workspace is None else workspace
-        return lib.rpa_rope_forward_update(
-            ctypes.byref(prm), ctypes.byref(table), ctypes.byref(st), _ptr(q), _ptr(new_k), _ptr(new_v), _ptr(kv_pages),
-            _ptr(kv_lens), _ptr(page_indices), _ptr(cu_q_lens), _ptr(num_seqs), _ptr(positions), _ptr(q_rot), _ptr(out),
-            _ptr(ws), ws.numel(), stream)
-
-    _launch(kv_pages.device, call)
+    rc = lib.rpa_rope_forward_update(
+        ctypes.byref(prm), ctypes.byref(table), ctypes.byref(st), q.data_ptr(), new_k.data_ptr(), new_v.data_ptr(),
+        kv_pages.data_ptr(), kv_lens.data_ptr(), page_indices.data_ptr(), cu_q_lens.data_ptr(), num_seqs.data_ptr(),
+        None if positions is None else positions.data_ptr(), q_rot.data_ptr(), out.data_ptr(), workspace.data_ptr(),
+        workspace.numel(), stream)
+    if rc:
+        _check(rc)
     return out
 
 
@@ -604,32 +665,27 @@ def rpa_cross_forward(q, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, *
                       k_scale=None, v_scale=None, out=None, workspace=None, batch_kind=BATCH_MIXED):
     """Attention of every query to all ``kv_lens`` keys of its sequence (a decoder's tokens to its
     encoder's states); returns ``out`` [max_num_tokens, Hq, D] bf16.  A sequence without keys gets zeros."""
-    lib = load_library()
-    _dev(q, "q", torch.bfloat16)
-    _dev(kv_pages, "kv_pages")
-    for n, t in (("kv_lens", kv_lens), ("page_indices", page_indices), ("cu_q_lens", cu_q_lens),
-                 ("num_seqs", num_seqs)):
-        _dev(t, n, torch.int32)
-    if q.dim() != 3 or kv_head_dim(kv_pages) != q.shape[-1]:
-        raise ValueError("q must be [tokens, heads, head_dim] with kv_pages' head_dim")
-    prm = make_rpa_params(q, kv_pages, page_indices, sm_scale=sm_scale, soft_cap=soft_cap, k_scale=k_scale,
-                          v_scale=v_scale, batch_kind=batch_kind)
-    if kv_lens.numel() != prm.max_num_seqs or cu_q_lens.numel() != prm.max_num_seqs + 1 or num_seqs.numel() != 1:
-        raise ValueError("kv_lens must be [max_num_seqs], cu_q_lens [max_num_seqs + 1], num_seqs [1]")
-    out = torch.empty_like(q) if out is None else out
-    _dev(out, "out", torch.bfloat16)
-    if out.shape != q.shape:
-        raise ValueError(f"out must have q's shape {tuple(q.shape)}, got {tuple(out.shape)}")
-    _same_device(q, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, out, workspace)
-    if q.shape[0] == 0:
+    lib = _lib or load_library()
+    dev = _cuda_index(q, "q")
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return rpa_cross_forward(q, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, sm_scale=sm_scale,
+                                     soft_cap=soft_cap, k_scale=k_scale, v_scale=v_scale, out=out, workspace=workspace,
+                                     batch_kind=batch_kind)
+    _on(dev, q, "q", torch.bfloat16)
+    if q.dim() != 3:
+        raise ValueError(f"q must be [tokens, heads, head_dim], got {tuple(q.shape)}")
+    T, hq, d = q.shape
+    prm = _batch_params(dev, T, hq, d, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, sm_scale, None, soft_cap, None,
+                        k_scale, v_scale, batch_kind)
+    out, workspace, stream = _attention_buffers(dev, lib.rpa_cross_workspace_size, prm, q, out, workspace)
+    if T == 0:
         return out
-
-    def call(stream):
-        ws = _own_workspace(rpa_cross_workspace_size(prm), q.device, "rpa") if workspace is None else workspace
-        return lib.rpa_cross_forward(ctypes.byref(prm), _ptr(q), _ptr(kv_pages), _ptr(kv_lens), _ptr(page_indices),
-                                     _ptr(cu_q_lens), _ptr(num_seqs), _ptr(out), _ptr(ws), ws.numel(), stream)
-
-    _launch(q.device, call)
+    rc = lib.rpa_cross_forward(ctypes.byref(prm), q.data_ptr(), kv_pages.data_ptr(), kv_lens.data_ptr(), page_indices.data_ptr(),
+                               cu_q_lens.data_ptr(), num_seqs.data_ptr(), out.data_ptr(), workspace.data_ptr(),
+                               workspace.numel(), stream)
+    if rc:
+        _check(rc)
     return out
 
 
