@@ -406,6 +406,8 @@ static int rpa_prepare(const rpa_params* p, const void* q, const void* kv_pages,
     a.decode_heads = decode_heads_for(p->head_dim, p->kv_dtype != RPA_DTYPE_BF16);
     a.num_sms = sms;
     a.overlap = prof_enabled() ? 0 : 1;
+    a.split_sms = a.overlap;
+    a.prefill_rows = kPrefillRows;
     rpa_rates(p->head_dim, a.kv_byte != 0, a.has_scale != 0,
               rpa_pow2_scale(a.k_scale_or_one) && rpa_pow2_scale(a.v_scale_or_one), &a.pre_flops_per_ns_sm,
               &a.dec_bytes_per_ns_sm);
@@ -726,7 +728,7 @@ int rpa_cross_forward(const rpa_params* p, const void* q, const void* kv_pages, 
     rc = rpa_prepare(p, q, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, out, workspace, workspace_bytes, a, sms);
     if (rc) return rc;
     a.causal = 0;
-    cudaError_t e = launch_rpa_forward(a, sms, reinterpret_cast<cudaStream_t>(stream));
+    cudaError_t e = launch_rpa_cross(a, sms, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "rpa_cross_forward launch");
     return RPA_OK;
 }

@@ -108,6 +108,8 @@ struct RpaArgs {
     int decode_per_sm;          // decode CTAs resident per SM (occupancy of the chosen kernel)
     int decode_heads;           // KV heads per decode item (decode_heads_for)
     int num_sms;
+    int prefill_rows;           // rows of a prefill item: 128, or 256 for the cross kernel with two tiles a CTA
+    int split_sms;              // the plan may give prefill and decode a share of the SMs each
     int overlap;                // run prefill beside decode (off while kernels are timed one by one)
     float pre_flops_per_ns_sm;  // prefill kernel rate per SM (this head size and cache type)
     float dec_bytes_per_ns_sm;  // decode kernel rate per SM while SMs, not HBM, limit it
@@ -277,6 +279,7 @@ struct RopeUpdateArgs {
 cudaError_t launch_rope_apply(RopeApplyArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_rope_update(RopeUpdateArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_rpa_forward(const RpaArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_rpa_cross(RpaArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_wait_selftest(uint32_t* err, cudaStream_t stream);
 cudaError_t launch_rpa_forward_update(const RpaArgs& a, const RpaUpdateArgs& u, int num_sms, cudaStream_t stream);
 cudaError_t launch_mla_forward_update(const LatentArgs& a, const MlaUpdateArgs& u, int num_sms, cudaStream_t stream);
@@ -298,6 +301,13 @@ cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, c
     return cudaLaunchKernelEx(&cfg, kern, std::forward<A>(args)...);
 }
 
+// 3-D bf16 tensor [d2][d1][d0] (d0 contiguous) with a box of {64, b1, b2}, 128-byte swizzle.
+bool make_tmap_bf16(struct CUtensorMap_st* tm, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b1,
+                    uint32_t b2);
+// Cross attention's prefill-class work with two tiles in flight an SM, for the batches it takes.
+bool rpa_cross_tc_takes(const RpaArgs& a);
+int rpa_cross_tile_rows(const RpaArgs& a);  // 256 or 128: the rows of an item
+cudaError_t launch_rpa_cross_tc(const RpaArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_rpa_decode(const RpaArgs& a, int num_sms, cudaStream_t stream);
 int rpa_decode_ctas_per_sm(const RpaArgs& a);  // resident CTAs per SM of the kernel launch_rpa_decode picks
 cudaError_t launch_rpa_prefill(const RpaArgs& a, int num_sms, cudaStream_t stream, int tail);

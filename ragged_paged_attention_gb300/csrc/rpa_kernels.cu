@@ -128,7 +128,7 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
         const float pre_flops = s_pf, dec_bytes = s_db;
         float tt = INFINITY;
         int nn = S;
-        if (a.overlap && pre_flops > 0.f && dec_bytes > 0.f && tid + 1 < S) {
+        if (a.split_sms && pre_flops > 0.f && dec_bytes > 0.f && tid + 1 < S) {
             nn = tid + 1;
             const float tp = pre_flops / (a.pre_flops_per_ns_sm * (float)nn);
             const float td = dec_bytes / fminf(kDecHbmBytesPerNs, a.dec_bytes_per_ns_sm * (float)(S - nn));
@@ -171,7 +171,7 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
         int n_pre = S;
         if (pre_flops <= 0.f) {
             n_pre = 0;
-        } else if (a.overlap && dec_bytes > 0.f && S > 1) {
+        } else if (a.split_sms && dec_bytes > 0.f && S > 1) {
             const float serial = pre_flops / (a.pre_flops_per_ns_sm * (float)S) +
                                  dec_bytes / fminf(kDecHbmBytesPerNs, a.dec_bytes_per_ns_sm * (float)S);
             if (bt < 0.9f * serial) n_pre = bn;
@@ -231,7 +231,7 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
                 nrh = cdiv(ql * G, kDecodeRows);
                 wk = (round_bk(kl - klo) + a.item_cost_keys) * n_groups * nrh;
             } else {
-                np = cdiv(ql * G, kPrefillRows) * a.num_kv_heads;
+                np = cdiv(ql * G, a.prefill_rows) * a.num_kv_heads;
             }
         }
         long long tot_w;
@@ -320,7 +320,7 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
             WorkItem w;
             w.seq = s0 + k;
             w.head = h;
-            w.row_begin = r * kPrefillRows;
+            w.row_begin = r * a.prefill_rows;
             w.key_begin = 0;
             w.key_end = e_kl[k];
             w.first_item = it;
@@ -526,13 +526,31 @@ cudaError_t launch_rpa_forward(const RpaArgs& a, int num_sms, cudaStream_t strea
     cudaError_t e;
     {
         ProfScope ps("rpa_plan", stream);
-        if (a.causal)
-            e = launch_pdl(rpa_plan_kernel, dim3(1), dim3(1024), 0, stream, a.overlap != 0, a);
-        else
-            e = launch_pdl(rpa_cross_plan_kernel, dim3(1 + kCrossZeroBlocks), dim3(1024), 0, stream, a.overlap != 0, a);
+        e = launch_pdl(rpa_plan_kernel, dim3(1), dim3(1024), 0, stream, a.overlap != 0, a);
     }
     if (e != cudaSuccess) return e;
     return launch_attention(a, num_sms, stream);
+}
+
+// Cross attention: the plan with the zero rows beside it, then the batch's prefill-class sequences on
+// the kernel with two tiles in flight, where it takes them, and decode behind it (started early, it
+// waits for that grid unless there was nothing for it); else the launches of rpa_forward.
+cudaError_t launch_rpa_cross(RpaArgs& a, int num_sms, cudaStream_t stream) {
+    const bool tc = rpa_cross_tc_takes(a);
+    if (tc) {
+        a.split_sms = 0;
+        a.prefill_rows = rpa_cross_tile_rows(a);
+    }
+    cudaError_t e;
+    {
+        ProfScope ps("rpa_plan", stream);
+        e = launch_pdl(rpa_cross_plan_kernel, dim3(1 + kCrossZeroBlocks), dim3(1024), 0, stream, a.overlap != 0, a);
+    }
+    if (e != cudaSuccess) return e;
+    if (!tc || a.batch_kind == RPA_BATCH_DECODE_ONLY) return launch_attention(a, num_sms, stream);
+    e = launch_rpa_cross_tc(a, num_sms, stream);
+    if (e != cudaSuccess || a.batch_kind == RPA_BATCH_PREFILL_ONLY) return e;
+    return launch_rpa_decode(a, num_sms, stream);
 }
 
 cudaError_t launch_rpa_forward_update(const RpaArgs& a, const RpaUpdateArgs& u, int num_sms, cudaStream_t stream) {
