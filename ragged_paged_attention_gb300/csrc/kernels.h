@@ -25,6 +25,12 @@ __host__ __device__ inline int update_cache_ints(int max_num_seqs) {
 }
 constexpr int kPrefillRows = 128;       // (token, q-head) rows per prefill item (one TMEM tile)
 constexpr int kMinChunk = 256;          // smallest split-KV chunk (keys)
+// Cross attention's kernel with two tiles in flight, measured: ns a 128-key block takes per tile with
+// every SM full (head_dim 64 and 128 alike), of one tile alone in a two-tile CTA, and in one tile's chain;
+// the rate at which it reads keys; and what decode costs beside it at least (its launch, the full plan,
+// a few stages' latency)
+constexpr float kCrossTileNs = 700.f, kCrossOneTileNs = 1300.f, kCrossChainNs = 1300.f;
+constexpr float kCrossHbmBytesPerNs = 6000.f, kCrossDecodeNs = 25000.f;
 constexpr int kCrossZeroBlocks = 8;      // cross attention: blocks beside the plan for rows without a key
 constexpr int kMaxDecodeCtas = 2048;    // most decode shares (static, one per CTA, and pooled)
 // Pool: the part of the line left after the static shares (here only their rounding

@@ -40,6 +40,11 @@
 
 namespace rpa {
 
+// An item as the warps get it: a tile's (or two tiles') rows of one KV head, with its sequence's numbers.
+struct __align__(16) CrossItem {
+    int seq, head, row, q_start, n_rows, kv_len, blocks, pad;
+};
+
 template <int D, int TILES>
 struct CrossTc {
     static constexpr int BK = 128;
@@ -56,7 +61,7 @@ struct CrossTc {
     static constexpr int kOffV = kOffK + NK * kTile;
     static constexpr int kOffBar = kOffV + NV * kTile;
     static constexpr int kBars = 2 * (NK + NV) + 8 + 5 * TILES;
-    static constexpr int kOffItem = (kOffBar + kBars * 8 + 15) / 16 * 16;  // [2] WorkItem, abort, TMEM base
+    static constexpr int kOffItem = (kOffBar + kBars * 8 + 15) / 16 * 16;  // [2] CrossItem, abort, TMEM base
     static constexpr int kSmem = kOffItem + 2 * 32 + 16;
     static constexpr int kSoft = 4 * TILES;                // softmax warps
     static constexpr int kThreads = (kSoft + 4) * 32;
@@ -75,11 +80,6 @@ template <int R>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
-
-// The block of one item: its sequence, rows and key blocks.
-struct CrossItem {
-    int seq, head, row, q_start, n_rows, kv_len, blocks;
-};
 
 template <int D, int TILES>
 __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>::kCtas)
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>
     uint64_t* o_empty = s_full + 2 * TILES;
     uint64_t* p_full = s_full + 3 * TILES;
     uint64_t* pv_done = s_full + 4 * TILES;
-    WorkItem* s_items = reinterpret_cast<WorkItem*>(smem + T::kOffItem);
+    CrossItem* s_items = reinterpret_cast<CrossItem*>(smem + T::kOffItem);
     volatile int& s_abort = *reinterpret_cast<volatile int*>(smem + T::kOffItem + 64);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + T::kOffItem + 68);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -153,19 +153,11 @@ __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>
     // Reads the next item (every warp); false when there is none.
     auto next_item = [&](CrossItem& it) -> bool {
         const uint32_t slot = items & 1, ph = (items >> 1) & 1;
-        WorkItem w;
-        w.seq = -1;
-        if (mbar_wait(&item_full[slot], ph, err)) w = s_items[slot];
+        it.seq = -1;
+        if (mbar_wait(&item_full[slot], ph, err)) it = s_items[slot];
         __syncwarp();
         if (lane == 0) mbar_arrive(&item_empty[slot]);
-        if (w.seq < 0 || s_abort) return false;
-        it.seq = w.seq;
-        it.head = w.head;
-        it.row = w.row_begin;
-        it.q_start = a.cu_q_lens[w.seq];
-        it.n_rows = (a.cu_q_lens[w.seq + 1] - it.q_start) * G;
-        it.kv_len = a.kv_lens[w.seq];
-        it.blocks = cdiv(it.kv_len, BK);
+        if (it.seq < 0 || s_abort) return false;
         ++items;
         return true;
     };
@@ -394,14 +386,23 @@ __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>
             bool ok = true;
             auto fetch = [&]() {  // the first lane of the K warp hands the next item to every warp
                 const uint32_t slot = fetched & 1, ph = (fetched >> 1) & 1;
-                WorkItem w;
-                w.seq = -1;
+                CrossItem n;
+                n.seq = -1;
                 if (!mbar_wait(&item_empty[slot], ph ^ 1, err)) s_abort = 1;
                 if (!s_abort) {
                     const int i = atomicAdd(&hdr->next_item[1], 1);
-                    if (i < hdr->num_items[1]) w = a.pre_items[i];
+                    if (i < hdr->num_items[1]) {
+                        const WorkItem w = a.pre_items[i];
+                        n.seq = w.seq;
+                        n.head = w.head;
+                        n.row = w.row_begin;
+                        n.q_start = a.cu_q_lens[w.seq];
+                        n.n_rows = (a.cu_q_lens[w.seq + 1] - n.q_start) * G;
+                        n.kv_len = a.kv_lens[w.seq];
+                        n.blocks = cdiv(n.kv_len, BK);
+                    }
                 }
-                s_items[slot] = w;
+                s_items[slot] = n;
                 mbar_arrive(&item_full[slot]);
                 ++fetched;
             };
@@ -415,20 +416,6 @@ __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>
                     return (lane * box_rows < BK && j < it.blocks && key < it.kv_len) ? __ldg(tbl + (key >> lps)) : 0;
                 };
                 int page_next = page_of(0);
-                if (!part && lane == 0) {
-                    const uint32_t iph = (items - 1) & 1;
-                    ok = mbar_wait(q_empty, iph ^ 1, err);  // the previous item's QKs have read Q
-                    if (ok) {
-                        const int tiles = min(TILES, cdiv(it.n_rows - it.row, 128));
-                        mbar_arrive_expect_tx(q_full, tiles * T::kTile);
-                        for (int t = 0; t < tiles; ++t)
-#pragma unroll
-                            for (int p = 0; p < T::DP; ++p)
-                                tma_load_3d(smem_u32(smem + t * T::kTile + p * T::kPanel), &tm_q, 64 * p, it.head * G,
-                                            it.q_start + (it.row + t * 128) / G, q_full);
-                    }
-                }
-                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
                 for (int j = 0; ok && j < it.blocks; ++j, ++jr) {
                     int page = page_next;
                     page_next = page_of(j + 1);
@@ -459,7 +446,7 @@ __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>
                         // the rows past the sequence: zeros, whatever the page or an earlier block left there
                         ok = mbar_wait(v_land, nland & 1, err);
                         ++nland;
-                        if (!ok) break;
+                        if (!ok) break;  // (every lane has waited)
                         for (int i = valid * 8 + lane; i < BK * 8; i += 32)
 #pragma unroll
                             for (int p = 0; p < T::DP; ++p)
@@ -467,6 +454,22 @@ __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&full[slot]);
+                    }
+                    if (!part && j == 0) {
+                        // the item's Q behind its first keys: it waits for the previous item's last QK
+                        if (lane == 0) {
+                            ok = mbar_wait(q_empty, (items & 1), err);
+                            if (ok) {
+                                const int tiles = min(TILES, cdiv(it.n_rows - it.row, 128));
+                                mbar_arrive_expect_tx(q_full, tiles * T::kTile);
+                                for (int t = 0; t < tiles; ++t)
+#pragma unroll
+                                    for (int p = 0; p < T::DP; ++p)
+                                        tma_load_3d(smem_u32(smem + t * T::kTile + p * T::kPanel), &tm_q, 64 * p, it.head * G,
+                                                    it.q_start + (it.row + t * 128) / G, q_full);
+                            }
+                        }
+                        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
                     }
                 }
                 if (!ok) s_abort = 1;

@@ -348,11 +348,123 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
 
 __global__ void __launch_bounds__(1024) rpa_plan_kernel(RpaArgs a) { plan_body(a); }
 
+// Cross attention on the kernel with two tiles in flight: that kernel also takes short sequences (a
+// tile with few rows costs it as many cycles as a full one, but one row of decode reads its keys about
+// as fast as HBM gives them), so decode's split of the keys pays only for batches too narrow to fill the
+// SMs. Estimates both, in ns, from measured rates; when the one kernel is no slower it writes the
+// items of every sequence and returns true: no decode, and none of plan_body's code (which, run once
+// per call, takes 10 us, most of it instruction fetches).
+__device__ __forceinline__ bool cross_plan_body(const RpaArgs& a) {
+    __shared__ float red[32][6];
+    __shared__ int scan[40], ends[1024], s_num, s_one;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_launch_dependents();
+    if (tid == 0) {
+        const int n = a.num_seqs[0];
+        s_num = n < 0 || n > a.max_num_seqs ? 0 : n;
+        if (n < 0 || n > a.max_num_seqs) set_error(&a.hdr->error_bits, RPA_DEV_ERR_NUM_SEQS);
+    }
+    __syncthreads();
+    const int num = s_num, G = a.num_q_heads / a.num_kv_heads;
+    // [0] blocks' time on all SMs together, [1] longest sequence, [2] keys: of every sequence, then of
+    // the prefill class alone
+    float v[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    int tiles = 0;  // of this thread's first sequence
+    for (int s = tid; s < num; s += blockDim.x) {
+        int ql, kl;
+        if (!seq_shape(a, s, ql, kl) || ql < 1) continue;
+        const bool dec = ql * G <= 16;
+        if (!kind_allows(a, dec)) {
+            set_error(&a.hdr->error_bits, RPA_DEV_ERR_BATCH_KIND);
+            continue;
+        }
+        const int n = cdiv(ql * G, a.prefill_rows) * a.num_kv_heads, blocks = cdiv(kl, 128);
+        if (s == tid) tiles = n;
+        // a full 256-row item's block takes two tiles' time, one of up to 128 rows the latency of one
+        const float t = a.prefill_rows == 128 ? kCrossTileNs : ql * G > 128 ? 2.f * kCrossTileNs : kCrossOneTileNs;
+        const float c[3] = {t * n * blocks, (float)blocks, (float)kl};
+        for (int k = 0; k < 6; k += 3) {
+            if (k && dec) break;
+            v[k] += c[0];
+            v[k + 1] = fmaxf(v[k + 1], c[1]);
+            v[k + 2] += c[2];
+        }
+    }
+    // over the warp, then over the warps' results (blockDim.x is 1024)
+    for (int round = 0; round < 2; ++round) {
+        if (round) {
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < 6; ++k) v[k] = red[lane][k];
+        }
+#pragma unroll 1
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int k = 0; k < 6; ++k) {
+                const float w = __shfl_xor_sync(0xffffffffu, v[k], o);
+                v[k] = k % 3 == 1 ? fmaxf(v[k], w) : v[k] + w;
+            }
+        if (!round && lane == 0)
+#pragma unroll
+            for (int k = 0; k < 6; ++k) red[warp][k] = v[k];
+    }
+    if (tid == 0) {
+        const float key_bytes = 4.f * a.num_kv_heads * a.head_dim;
+        const auto one = [&](const float* c) {
+            return fmaxf(fmaxf(c[0] / a.num_sms, c[1] * kCrossChainNs), c[2] * key_bytes / kCrossHbmBytesPerNs);
+        };
+        const float dec_keys = v[2] - v[5];
+        const float split = one(v + 3) + fmaxf(dec_keys * key_bytes / kDecHbmBytesPerNs, kCrossDecodeNs);
+        s_one = dec_keys == 0.f || one(v) <= split;
+    }
+    __syncthreads();
+    if (!s_one) return false;
+    int base = 0;
+    for (int s0 = 0; s0 < num; s0 += blockDim.x) {
+        if (s0) {
+            int ql, kl;
+            tiles = 0;
+            if (s0 + tid < num && seq_shape(a, s0 + tid, ql, kl) && ql >= 1 && kind_allows(a, ql * G <= 16))
+                tiles = cdiv(ql * G, a.prefill_rows) * a.num_kv_heads;
+        }
+        int total;
+        ends[tid] = block_exclusive_scan(tiles, scan, &total) + tiles;
+        __syncthreads();
+        for (int i = tid; i < total && base + i < a.max_pre_items; i += blockDim.x) {
+            int lo = 0, hi = min((int)blockDim.x, num - s0) - 1;  // the first sequence whose end exceeds i
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (ends[mid] > i) hi = mid; else lo = mid + 1;
+            }
+            const int rel = i - (lo ? ends[lo - 1] : 0);
+            WorkItem w = {};
+            w.seq = s0 + lo;
+            w.head = rel % a.num_kv_heads;
+            w.row_begin = rel / a.num_kv_heads * a.prefill_rows;
+            w.num_splits = 1;
+            a.pre_items[base + i] = w;
+        }
+        base += total;
+        __syncthreads();
+    }
+    if (tid == 0) {
+        WsHeader* hdr = a.hdr;
+        hdr->num_items[0] = 0;
+        hdr->num_items[1] = min(base, a.max_pre_items);
+        hdr->next_item[0] = hdr->next_item[1] = hdr->next_item[2] = 0;
+        hdr->prefill_ctas = base > 0 ? a.num_sms : 0;
+        hdr->dec_ctas = hdr->dec_shares = 0;
+        a.cta_first[0] = 0;
+        pdl_wait();  // (as the end of plan_body)
+    }
+    return true;
+}
+
 // Cross attention: block 0 plans, the others write the zero rows of sequences without keys (which
 // the plan leaves out). They wait for the stream's earlier work first: it may still use `out`.
-__global__ void __launch_bounds__(1024) rpa_cross_plan_kernel(RpaArgs a) {
+__global__ void __launch_bounds__(1024) rpa_cross_plan_kernel(RpaArgs a, int one_kernel) {
     if (blockIdx.x == 0) {
-        plan_body(a);
+        if (!one_kernel || !cross_plan_body(a)) plan_body(a);
         return;
     }
     pdl_launch_dependents();
@@ -532,11 +644,12 @@ cudaError_t launch_rpa_forward(const RpaArgs& a, int num_sms, cudaStream_t strea
     return launch_attention(a, num_sms, stream);
 }
 
-// Cross attention: the plan with the zero rows beside it, then the batch's prefill-class sequences on
-// the kernel with two tiles in flight, where it takes them, and decode behind it (started early, it
-// waits for that grid unless there was nothing for it); else the launches of rpa_forward.
+// Cross attention: the plan with the zero rows beside it, then the kernel with two tiles in flight,
+// where it takes the batch, and decode behind it (started early, it waits for that grid unless there
+// was nothing for it; it finds no item when the plan gave every sequence to the one kernel); else the
+// launches of rpa_forward.
 cudaError_t launch_rpa_cross(RpaArgs& a, int num_sms, cudaStream_t stream) {
-    const bool tc = rpa_cross_tc_takes(a);
+    const bool tc = rpa_cross_tc_takes(a) && a.batch_kind != RPA_BATCH_DECODE_ONLY;
     if (tc) {
         a.split_sms = 0;
         a.prefill_rows = rpa_cross_tile_rows(a);
@@ -544,10 +657,10 @@ cudaError_t launch_rpa_cross(RpaArgs& a, int num_sms, cudaStream_t stream) {
     cudaError_t e;
     {
         ProfScope ps("rpa_plan", stream);
-        e = launch_pdl(rpa_cross_plan_kernel, dim3(1 + kCrossZeroBlocks), dim3(1024), 0, stream, a.overlap != 0, a);
+        e = launch_pdl(rpa_cross_plan_kernel, dim3(1 + kCrossZeroBlocks), dim3(1024), 0, stream, a.overlap != 0, a, tc ? 1 : 0);
     }
     if (e != cudaSuccess) return e;
-    if (!tc || a.batch_kind == RPA_BATCH_DECODE_ONLY) return launch_attention(a, num_sms, stream);
+    if (!tc) return launch_attention(a, num_sms, stream);
     e = launch_rpa_cross_tc(a, num_sms, stream);
     if (e != cudaSuccess || a.batch_kind == RPA_BATCH_PREFILL_ONLY) return e;
     return launch_rpa_decode(a, num_sms, stream);
