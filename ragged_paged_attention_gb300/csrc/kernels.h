@@ -75,7 +75,8 @@ inline bool rpa_pow2_scale(float s) {
     return s > 0.f && m == 0.5f && e >= -40 && e <= 40;
 }
 
-// One unit of work for a persistent attention CTA (32 bytes).
+// One unit of work for a persistent attention CTA (32 bytes). An RPA prefill item takes every key its
+// rows see: key_begin is its sequence's first query token, key_end its kv_len and first_item its rows.
 struct __align__(16) WorkItem {
     int seq;         // sequence (RPA/MLA) or flat query b*S+s (sparse)
     int head;        // first KV head (RPA) or first q head (latent) of the tile

@@ -384,24 +384,27 @@ __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>
             uint32_t nland = 0;  // V blocks zeroed behind their rows
             uint32_t fetched = 0;
             bool ok = true;
-            auto fetch = [&]() {  // the first lane of the K warp hands the next item to every warp
+            const int n_items = hdr->num_items[1];
+            // The first lane of the K warp hands the next item to every warp. (It takes the item once the
+            // last one's copies are issued, not earlier: a CTA that held an item in reserve would keep it
+            // from an idle one.)
+            auto fetch = [&]() {
+                const int place = atomicAdd(&hdr->next_item[1], 1);
                 const uint32_t slot = fetched & 1, ph = (fetched >> 1) & 1;
                 CrossItem n;
                 n.seq = -1;
-                if (!mbar_wait(&item_empty[slot], ph ^ 1, err)) s_abort = 1;
-                if (!s_abort) {
-                    const int i = atomicAdd(&hdr->next_item[1], 1);
-                    if (i < hdr->num_items[1]) {
-                        const WorkItem w = a.pre_items[i];
-                        n.seq = w.seq;
-                        n.head = w.head;
-                        n.row = w.row_begin;
-                        n.q_start = a.cu_q_lens[w.seq];
-                        n.n_rows = (a.cu_q_lens[w.seq + 1] - n.q_start) * G;
-                        n.kv_len = a.kv_lens[w.seq];
-                        n.blocks = cdiv(n.kv_len, BK);
-                    }
+                if (place < n_items) {
+                    const WorkItem w = a.pre_items[place];
+                    n.seq = w.seq;
+                    n.head = w.head;
+                    n.row = w.row_begin;
+                    n.q_start = w.key_begin;
+                    n.n_rows = w.first_item;
+                    n.kv_len = w.key_end;
+                    n.blocks = cdiv(n.kv_len, BK);
                 }
+                if (!mbar_wait(&item_empty[slot], ph ^ 1, err)) s_abort = 1;
+                if (s_abort) n.seq = -1;
                 s_items[slot] = n;
                 mbar_arrive(&item_full[slot]);
                 ++fetched;

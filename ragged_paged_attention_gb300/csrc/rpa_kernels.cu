@@ -321,9 +321,9 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
             w.seq = s0 + k;
             w.head = h;
             w.row_begin = r * a.prefill_rows;
-            w.key_begin = 0;
+            w.key_begin = a.cu_q_lens[w.seq];
             w.key_end = e_kl[k];
-            w.first_item = it;
+            w.first_item = (a.cu_q_lens[w.seq + 1] - w.key_begin) * G;
             w.num_splits = 1;
             w.split = 0;
             a.pre_items[it] = w;
@@ -441,6 +441,9 @@ __device__ __forceinline__ bool cross_plan_body(const RpaArgs& a) {
             w.seq = s0 + lo;
             w.head = rel % a.num_kv_heads;
             w.row_begin = rel / a.num_kv_heads * a.prefill_rows;
+            w.key_begin = a.cu_q_lens[w.seq];
+            w.key_end = a.kv_lens[w.seq];
+            w.first_item = (a.cu_q_lens[w.seq + 1] - w.key_begin) * G;
             w.num_splits = 1;
             a.pre_items[base + i] = w;
         }
