@@ -406,8 +406,6 @@ static int rpa_prepare(const rpa_params* p, const void* q, const void* kv_pages,
     a.decode_heads = decode_heads_for(p->head_dim, p->kv_dtype != RPA_DTYPE_BF16);
     a.num_sms = sms;
     a.overlap = prof_enabled() ? 0 : 1;
-    a.split_sms = a.overlap;
-    a.prefill_rows = kPrefillRows;
     rpa_rates(p->head_dim, a.kv_byte != 0, a.has_scale != 0,
               rpa_pow2_scale(a.k_scale_or_one) && rpa_pow2_scale(a.v_scale_or_one), &a.pre_flops_per_ns_sm,
               &a.dec_bytes_per_ns_sm);
@@ -698,6 +696,9 @@ int rpa_rope_forward_update(const rpa_params* p, const rope_table* t, const rope
     rc = rope_update_prepare(p, t, strides, q, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs,
                              positions, q_rot, &a.hdr->error_bits, u);
     if (rc) return rc;
+    // so few query rows that every sequence is decode-class: the prefill launches are left out
+    if (a.batch_kind == RPA_BATCH_MIXED && (long long)p->max_num_tokens * (a.num_q_heads / a.num_kv_heads) <= 16)
+        a.batch_kind = RPA_BATCH_DECODE_ONLY;
     cudaError_t e = launch_rope_update(u, sms, reinterpret_cast<cudaStream_t>(stream));
     if (e == cudaSuccess) e = launch_rpa_forward(a, sms, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "rpa_rope_forward_update launch");
@@ -712,10 +713,30 @@ static int check_cross_params(const rpa_params* p) {
     return RPA_OK;
 }
 
+// rpa_forward's workspace with a list behind it that has room for the items of split sequences: as
+// many as the partial results' space has slots of kCrossSlotRows rows.
+struct CrossLayout {
+    size_t items, total;
+    int max_items, max_slots;
+};
+
+static CrossLayout cross_layout(const rpa_params* p) {
+    const RpaLayout L = rpa_layout(p);
+    CrossLayout c;
+    c.max_slots = L.max_dec * (kMaxDecodeHeads * kDecodeRows / kCrossSlotRows);
+    if (p->head_dim >= 256) c.max_slots /= 2;  // (two KV heads an item there)
+    c.max_items = L.max_pre + c.max_slots;
+    c.items = L.total;
+    c.total = align_up(c.items + sizeof(WorkItem) * (size_t)c.max_items);
+    return c;
+}
+
 int rpa_cross_workspace_size(const rpa_params* p, size_t* bytes) {
     const int rc = check_cross_params(p);
     if (rc) return rc;
-    return rpa_workspace_size(p, bytes);
+    if (!bytes) return fail(RPA_ERR_NULL, "bytes is NULL");
+    *bytes = cross_layout(p).total;
+    return RPA_OK;
 }
 
 int rpa_cross_forward(const rpa_params* p, const void* q, const void* kv_pages, const int32_t* kv_lens,
@@ -727,8 +748,15 @@ int rpa_cross_forward(const rpa_params* p, const void* q, const void* kv_pages, 
     int sms = 0;
     rc = rpa_prepare(p, q, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, out, workspace, workspace_bytes, a, sms);
     if (rc) return rc;
+    const CrossLayout c = cross_layout(p);
+    rc = check_workspace(workspace, workspace_bytes, c.total);
+    if (rc) return rc;
     a.causal = 0;
-    cudaError_t e = launch_rpa_cross(a, sms, reinterpret_cast<cudaStream_t>(stream));
+    if (rpa_cross_tc_takes(a)) {
+        a.pre_items = reinterpret_cast<WorkItem*>(static_cast<uint8_t*>(workspace) + c.items);
+        a.max_pre_items = c.max_items;
+    }
+    cudaError_t e = launch_rpa_cross(a, c.max_slots, sms, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "rpa_cross_forward launch");
     return RPA_OK;
 }

@@ -25,12 +25,10 @@ __host__ __device__ inline int update_cache_ints(int max_num_seqs) {
 }
 constexpr int kPrefillRows = 128;       // (token, q-head) rows per prefill item (one TMEM tile)
 constexpr int kMinChunk = 256;          // smallest split-KV chunk (keys)
-// Cross attention's kernel with two tiles in flight, measured: ns a 128-key block takes per tile with
-// every SM full (head_dim 64 and 128 alike), of one tile alone in a two-tile CTA, and in one tile's chain;
-// the rate at which it reads keys; and what decode costs beside it at least (its launch, the full plan,
-// a few stages' latency)
-constexpr float kCrossTileNs = 700.f, kCrossOneTileNs = 1300.f, kCrossChainNs = 1300.f;
-constexpr float kCrossHbmBytesPerNs = 6000.f, kCrossDecodeNs = 25000.f;
+// Cross attention's two-tile kernel: a sequence of up to kCrossSplitRows rows may be cut along its keys
+// into up to kCrossMaxSplits pieces of kCrossMinBlocks 128-key blocks or more, whose results wait in
+// slots of kCrossSlotRows rows
+constexpr int kCrossSplitRows = 32, kCrossMaxSplits = 64, kCrossMinBlocks = 4, kCrossSlotRows = 16;
 constexpr int kCrossZeroBlocks = 8;      // cross attention: blocks beside the plan for rows without a key
 constexpr int kMaxDecodeCtas = 2048;    // most decode shares (static, one per CTA, and pooled)
 // Pool: the part of the line left after the static shares (here only their rounding
@@ -75,8 +73,10 @@ inline bool rpa_pow2_scale(float s) {
     return s > 0.f && m == 0.5f && e >= -40 && e <= 40;
 }
 
-// One unit of work for a persistent attention CTA (32 bytes). An RPA prefill item takes every key its
-// rows see: key_begin is its sequence's first query token, key_end its kv_len and first_item its rows.
+// One unit of work for a persistent attention CTA (32 bytes). Cross attention's two-tile kernel has its
+// sequence's first query token in key_begin, its kv_len in key_end and its rows in first_item; an item
+// of a sequence cut along its keys (one tile: its rows begin at 0) has its head's first partial-result
+// slot in row_begin.
 struct __align__(16) WorkItem {
     int seq;         // sequence (RPA/MLA) or flat query b*S+s (sparse)
     int head;        // first KV head (RPA) or first q head (latent) of the tile
@@ -115,8 +115,7 @@ struct RpaArgs {
     int decode_per_sm;          // decode CTAs resident per SM (occupancy of the chosen kernel)
     int decode_heads;           // KV heads per decode item (decode_heads_for)
     int num_sms;
-    int prefill_rows;           // rows of a prefill item: 128, or 256 for the cross kernel with two tiles a CTA
-    int split_sms;              // the plan may give prefill and decode a share of the SMs each
+    int prefill_rows;           // cross attention's two-tile kernel: rows of an item (128 or 256)
     int overlap;                // run prefill beside decode (off while kernels are timed one by one)
     float pre_flops_per_ns_sm;  // prefill kernel rate per SM (this head size and cache type)
     float dec_bytes_per_ns_sm;  // decode kernel rate per SM while SMs, not HBM, limit it
@@ -286,7 +285,7 @@ struct RopeUpdateArgs {
 cudaError_t launch_rope_apply(RopeApplyArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_rope_update(RopeUpdateArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_rpa_forward(const RpaArgs& a, int num_sms, cudaStream_t stream);
-cudaError_t launch_rpa_cross(RpaArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_rpa_cross(RpaArgs& a, int max_slots, int num_sms, cudaStream_t stream);
 cudaError_t launch_wait_selftest(uint32_t* err, cudaStream_t stream);
 cudaError_t launch_rpa_forward_update(const RpaArgs& a, const RpaUpdateArgs& u, int num_sms, cudaStream_t stream);
 cudaError_t launch_mla_forward_update(const LatentArgs& a, const MlaUpdateArgs& u, int num_sms, cudaStream_t stream);

@@ -40,9 +40,11 @@
 
 namespace rpa {
 
-// An item as the warps get it: a tile's (or two tiles') rows of one KV head, with its sequence's numbers.
+// An item as the warps get it: a tile's (or two tiles') rows of one KV head against `blocks` key blocks
+// from block0 on, with its sequence's numbers. One of `splits` pieces leaves its result in slots of
+// kCrossSlotRows rows, the pieces' one behind another from `slot` on.
 struct __align__(16) CrossItem {
-    int seq, head, row, q_start, n_rows, kv_len, blocks, pad;
+    int seq, head, row, q_start, n_rows, kv_len, blocks, block0, splits, split, slot, pad;
 };
 
 template <int D, int TILES>
@@ -60,9 +62,9 @@ struct CrossTc {
     static constexpr int kOffK = TILES * kTile;
     static constexpr int kOffV = kOffK + NK * kTile;
     static constexpr int kOffBar = kOffV + NV * kTile;
-    static constexpr int kBars = 2 * (NK + NV) + 8 + 5 * TILES;
+    static constexpr int kBars = 2 * (NK + NV) + 9 + 5 * TILES;
     static constexpr int kOffItem = (kOffBar + kBars * 8 + 15) / 16 * 16;  // [2] CrossItem, abort, TMEM base
-    static constexpr int kSmem = kOffItem + 2 * 32 + 16;
+    static constexpr int kSmem = kOffItem + 2 * (int)sizeof(CrossItem) + 16;
     static constexpr int kSoft = 4 * TILES;                // softmax warps
     static constexpr int kThreads = (kSoft + 4) * 32;
     static constexpr int kColS = 0, kColSStep = ONE_S ? 0 : 128;
@@ -98,14 +100,16 @@ __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>
     uint64_t* item_empty = q_full + 4;  // [2]
     uint64_t* v_land = q_full + 6;      // the last block's V, before its rows past the sequence are zeroed
     uint64_t* fin = q_full + 7;         // every product has completed
-    uint64_t* s_full = q_full + 8;      // [TILES] each
+    uint64_t* join = q_full + 8;        // tile 0's softmax warps, around a piece's ticket
+    uint64_t* s_full = q_full + 9;      // [TILES] each
     uint64_t* s_free = s_full + TILES;
     uint64_t* o_empty = s_full + 2 * TILES;
     uint64_t* p_full = s_full + 3 * TILES;
     uint64_t* pv_done = s_full + 4 * TILES;
     CrossItem* s_items = reinterpret_cast<CrossItem*>(smem + T::kOffItem);
-    volatile int& s_abort = *reinterpret_cast<volatile int*>(smem + T::kOffItem + 64);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + T::kOffItem + 68);
+    volatile int& s_abort = *reinterpret_cast<volatile int*>(smem + T::kOffItem + 2 * sizeof(CrossItem));
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + T::kOffItem + 2 * sizeof(CrossItem) + 4);
+    volatile int& s_last = *reinterpret_cast<volatile int*>(smem + T::kOffItem + 2 * sizeof(CrossItem) + 8);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     WsHeader* hdr = a.hdr;
     uint32_t* err = &hdr->error_bits;
@@ -125,6 +129,7 @@ __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>
         mbar_init(q_empty, TILES);
         mbar_init(v_land, 1);
         mbar_init(fin, TILES);
+        mbar_init(join, 4);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&item_full[i], 1);
             mbar_init(&item_empty[i], T::kThreads / 32);
@@ -172,6 +177,12 @@ __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>
                        col_o = tmem + lane_off + T::kColO + t * D;
         const float cs = a.sm_scale * kLog2e;
         uint32_t nblk = 0;  // blocks this tile has processed
+        uint32_t njoin = 0;
+        auto join_warps = [&]() -> bool {  // a bounded barrier of the tile's four warps
+            __syncwarp();
+            if (lane == 0) mbar_arrive(join);
+            return mbar_wait(join, njoin++ & 1, err);
+        };
         bool ok = true;
         while (ok && next_item(it)) {
             if (it.row + t * 128 >= it.n_rows) continue;  // this item has no such tile
@@ -192,7 +203,7 @@ __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s_free[t]);
-                const int valid = it.kv_len - j * BK;
+                const int valid = it.kv_len - (it.block0 + j) * BK;
                 if (valid < BK) {
 #pragma unroll
                     for (int i = 0; i < BK; ++i) x[i] = i < valid ? x[i] : -INFINITY;
@@ -254,6 +265,62 @@ __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>
             if (ok && mbar_wait(&pv_done[t], (nblk - 1) & 1, err)) {
                 tc_fence_after();
                 const bool rv = R < it.n_rows;
+                if (it.splits > 1) {
+                    // a piece: its rows' maximum (log2 units), sum and O as they are; the last piece of the
+                    // head to arrive joins them all
+                    const int rows16 = cdiv(it.n_rows, kCrossSlotRows) * kCrossSlotRows;
+                    const size_t row = (size_t)it.slot * kCrossSlotRows + (size_t)it.split * rows16 + R;
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        float o[32];
+                        tmem_ld32(col_o + c * 32, o);
+                        if (rv) {
+                            float4* d4 = reinterpret_cast<float4*>(a.partial_o + row * D + c * 32);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) d4[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        }
+                    }
+                    if (rv) *reinterpret_cast<float2*>(a.partial_ml + row * 2) = make_float2(m_use, l);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&o_empty[t]);
+                    __threadfence();
+                    ok = join_warps();
+                    if (ok && tid == 0) s_last = atomicAdd(&a.tickets[it.slot / 2], 1) == it.splits - 1;
+                    ok = ok && join_warps();
+                    const bool last = ok && s_last;
+                    ok = ok && join_warps();  // (s_last is read before the next piece's is written)
+                    if (last) {
+                        __threadfence();
+                        const float* ml = a.partial_ml + (size_t)it.slot * kCrossSlotRows * 2;
+                        const float* po = a.partial_o + (size_t)it.slot * kCrossSlotRows * D;
+                        for (int i = tid; i < it.n_rows * (D / 4); i += 128) {
+                            const int r = i / (D / 4), c = i % (D / 4) * 4;
+                            float M = -INFINITY, L = 0.f;
+                            for (int sp = 0; sp < it.splits; ++sp) M = fmaxf(M, __ldcg(ml + 2 * (sp * rows16 + r)));
+                            const float Mu = M == -INFINITY ? 0.f : M;
+                            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                            for (int sp = 0; sp < it.splits; ++sp) {
+                                const float2 m = __ldcg(reinterpret_cast<const float2*>(ml) + sp * rows16 + r);
+                                const float4 o = __ldcg(reinterpret_cast<const float4*>(po + (size_t)(sp * rows16 + r) * D + c));
+                                const float f = fast_exp2(m.x - Mu);
+                                L += f * m.y;
+                                acc.x += f * o.x;
+                                acc.y += f * o.y;
+                                acc.z += f * o.z;
+                                acc.w += f * o.w;
+                            }
+                            const float inv = L > 0.f ? 1.f / L : 0.f;
+                            __nv_bfloat16* dst =
+                                a.out + ((size_t)(it.q_start + r / G) * a.num_q_heads + it.head * G + r % G) * D + c;
+                            *reinterpret_cast<uint2*>(dst) =
+                                make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+                        }
+                    }
+                    if (!ok) s_abort = 1;
+                    continue;
+                }
                 const float inv = l > 0.f ? 1.f / l : 0.f;
                 __nv_bfloat16* dst = a.out + ((size_t)(it.q_start + (rv ? R / G : 0)) * a.num_q_heads + it.head * G +
                                               (rv ? R % G : 0)) * D;
@@ -397,11 +464,16 @@ __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>
                     const WorkItem w = a.pre_items[place];
                     n.seq = w.seq;
                     n.head = w.head;
-                    n.row = w.row_begin;
                     n.q_start = w.key_begin;
                     n.n_rows = w.first_item;
                     n.kv_len = w.key_end;
-                    n.blocks = cdiv(n.kv_len, BK);
+                    n.splits = w.num_splits;
+                    n.split = w.split;
+                    n.row = w.num_splits > 1 ? 0 : w.row_begin;
+                    n.slot = w.row_begin;
+                    const int blocks = cdiv(n.kv_len, BK);  // (pieces are at least a block: the plan's bound)
+                    n.block0 = (int)((long long)blocks * w.split / w.num_splits);
+                    n.blocks = (int)((long long)blocks * (w.split + 1) / w.num_splits) - n.block0;
                 }
                 if (!mbar_wait(&item_empty[slot], ph ^ 1, err)) s_abort = 1;
                 if (s_abort) n.seq = -1;
@@ -415,14 +487,14 @@ __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>
                 if (!next_item(it)) break;
                 const int* tbl = a.page_indices + (size_t)it.seq * a.pages_per_seq;
                 auto page_of = [&](int j) -> int {
-                    const int key = j * BK + lane * box_rows;
+                    const int key = (it.block0 + j) * BK + lane * box_rows;
                     return (lane * box_rows < BK && j < it.blocks && key < it.kv_len) ? __ldg(tbl + (key >> lps)) : 0;
                 };
                 int page_next = page_of(0);
                 for (int j = 0; ok && j < it.blocks; ++j, ++jr) {
                     int page = page_next;
                     page_next = page_of(j + 1);
-                    const int valid = it.kv_len - j * BK;  // >= 1
+                    const int key0 = (it.block0 + j) * BK, valid = it.kv_len - key0;  // valid >= 1
                     const int boxes = valid >= BK ? BK >> lbr : (valid + box_rows - 1) >> lbr;
                     if (lane < boxes && (unsigned)page >= (unsigned)a.total_num_pages) {
                         if (!part) set_error(err, RPA_DEV_ERR_PAGE);
@@ -440,7 +512,7 @@ __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>
                     if (!ok) break;
                     uint8_t* stage = smem + (part ? T::kOffV : T::kOffK) + slot * T::kTile;
                     if (lane < boxes) {
-                        const int z = (page << lps) + ((j * BK + lane * box_rows) & in_page);
+                        const int z = (page << lps) + ((key0 + lane * box_rows) & in_page);
 #pragma unroll
                         for (int p = 0; p < T::DP; ++p)
                             tma_load_3d(smem_u32(stage + p * T::kPanel + lane * box_rows * 128), &tm_kv, 64 * p, 2 * it.head + part, z, bar);

@@ -128,7 +128,7 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
         const float pre_flops = s_pf, dec_bytes = s_db;
         float tt = INFINITY;
         int nn = S;
-        if (a.split_sms && pre_flops > 0.f && dec_bytes > 0.f && tid + 1 < S) {
+        if (a.overlap && pre_flops > 0.f && dec_bytes > 0.f && tid + 1 < S) {
             nn = tid + 1;
             const float tp = pre_flops / (a.pre_flops_per_ns_sm * (float)nn);
             const float td = dec_bytes / fminf(kDecHbmBytesPerNs, a.dec_bytes_per_ns_sm * (float)(S - nn));
@@ -171,7 +171,7 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
         int n_pre = S;
         if (pre_flops <= 0.f) {
             n_pre = 0;
-        } else if (a.split_sms && dec_bytes > 0.f && S > 1) {
+        } else if (a.overlap && dec_bytes > 0.f && S > 1) {
             const float serial = pre_flops / (a.pre_flops_per_ns_sm * (float)S) +
                                  dec_bytes / fminf(kDecHbmBytesPerNs, a.dec_bytes_per_ns_sm * (float)S);
             if (bt < 0.9f * serial) n_pre = bn;
@@ -231,7 +231,7 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
                 nrh = cdiv(ql * G, kDecodeRows);
                 wk = (round_bk(kl - klo) + a.item_cost_keys) * n_groups * nrh;
             } else {
-                np = cdiv(ql * G, a.prefill_rows) * a.num_kv_heads;
+                np = cdiv(ql * G, kPrefillRows) * a.num_kv_heads;
             }
         }
         long long tot_w;
@@ -320,10 +320,10 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
             WorkItem w;
             w.seq = s0 + k;
             w.head = h;
-            w.row_begin = r * a.prefill_rows;
-            w.key_begin = a.cu_q_lens[w.seq];
+            w.row_begin = r * kPrefillRows;
+            w.key_begin = 0;
             w.key_end = e_kl[k];
-            w.first_item = (a.cu_q_lens[w.seq + 1] - w.key_begin) * G;
+            w.first_item = it;
             w.num_splits = 1;
             w.split = 0;
             a.pre_items[it] = w;
@@ -348,131 +348,12 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
 
 __global__ void __launch_bounds__(1024) rpa_plan_kernel(RpaArgs a) { plan_body(a); }
 
-// Cross attention on the kernel with two tiles in flight: that kernel also takes short sequences (a
-// tile with few rows costs it as many cycles as a full one, but one row of decode reads its keys about
-// as fast as HBM gives them), so decode's split of the keys pays only for batches too narrow to fill the
-// SMs. Estimates both, in ns, from measured rates; when the one kernel is no slower it writes the
-// items of every sequence and returns true: no decode, and none of plan_body's code (which, run once
-// per call, takes 10 us, most of it instruction fetches).
-__device__ __forceinline__ bool cross_plan_body(const RpaArgs& a) {
-    __shared__ float red[32][6];
-    __shared__ int scan[40], ends[1024], s_num, s_one;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    pdl_launch_dependents();
-    if (tid == 0) {
-        const int n = a.num_seqs[0];
-        s_num = n < 0 || n > a.max_num_seqs ? 0 : n;
-        if (n < 0 || n > a.max_num_seqs) set_error(&a.hdr->error_bits, RPA_DEV_ERR_NUM_SEQS);
-    }
-    __syncthreads();
-    const int num = s_num, G = a.num_q_heads / a.num_kv_heads;
-    // [0] blocks' time on all SMs together, [1] longest sequence, [2] keys: of every sequence, then of
-    // the prefill class alone
-    float v[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    int tiles = 0;  // of this thread's first sequence
-    for (int s = tid; s < num; s += blockDim.x) {
-        int ql, kl;
-        if (!seq_shape(a, s, ql, kl) || ql < 1) continue;
-        const bool dec = ql * G <= 16;
-        if (!kind_allows(a, dec)) {
-            set_error(&a.hdr->error_bits, RPA_DEV_ERR_BATCH_KIND);
-            continue;
-        }
-        const int n = cdiv(ql * G, a.prefill_rows) * a.num_kv_heads, blocks = cdiv(kl, 128);
-        if (s == tid) tiles = n;
-        // a full 256-row item's block takes two tiles' time, one of up to 128 rows the latency of one
-        const float t = a.prefill_rows == 128 ? kCrossTileNs : ql * G > 128 ? 2.f * kCrossTileNs : kCrossOneTileNs;
-        const float c[3] = {t * n * blocks, (float)blocks, (float)kl};
-        for (int k = 0; k < 6; k += 3) {
-            if (k && dec) break;
-            v[k] += c[0];
-            v[k + 1] = fmaxf(v[k + 1], c[1]);
-            v[k + 2] += c[2];
-        }
-    }
-    // over the warp, then over the warps' results (blockDim.x is 1024)
-    for (int round = 0; round < 2; ++round) {
-        if (round) {
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < 6; ++k) v[k] = red[lane][k];
-        }
-#pragma unroll 1
-        for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-            for (int k = 0; k < 6; ++k) {
-                const float w = __shfl_xor_sync(0xffffffffu, v[k], o);
-                v[k] = k % 3 == 1 ? fmaxf(v[k], w) : v[k] + w;
-            }
-        if (!round && lane == 0)
-#pragma unroll
-            for (int k = 0; k < 6; ++k) red[warp][k] = v[k];
-    }
-    if (tid == 0) {
-        const float key_bytes = 4.f * a.num_kv_heads * a.head_dim;
-        const auto one = [&](const float* c) {
-            return fmaxf(fmaxf(c[0] / a.num_sms, c[1] * kCrossChainNs), c[2] * key_bytes / kCrossHbmBytesPerNs);
-        };
-        const float dec_keys = v[2] - v[5];
-        const float split = one(v + 3) + fmaxf(dec_keys * key_bytes / kDecHbmBytesPerNs, kCrossDecodeNs);
-        s_one = dec_keys == 0.f || one(v) <= split;
-    }
-    __syncthreads();
-    if (!s_one) return false;
-    int base = 0;
-    for (int s0 = 0; s0 < num; s0 += blockDim.x) {
-        if (s0) {
-            int ql, kl;
-            tiles = 0;
-            if (s0 + tid < num && seq_shape(a, s0 + tid, ql, kl) && ql >= 1 && kind_allows(a, ql * G <= 16))
-                tiles = cdiv(ql * G, a.prefill_rows) * a.num_kv_heads;
-        }
-        int total;
-        ends[tid] = block_exclusive_scan(tiles, scan, &total) + tiles;
-        __syncthreads();
-        for (int i = tid; i < total && base + i < a.max_pre_items; i += blockDim.x) {
-            int lo = 0, hi = min((int)blockDim.x, num - s0) - 1;  // the first sequence whose end exceeds i
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if (ends[mid] > i) hi = mid; else lo = mid + 1;
-            }
-            const int rel = i - (lo ? ends[lo - 1] : 0);
-            WorkItem w = {};
-            w.seq = s0 + lo;
-            w.head = rel % a.num_kv_heads;
-            w.row_begin = rel / a.num_kv_heads * a.prefill_rows;
-            w.key_begin = a.cu_q_lens[w.seq];
-            w.key_end = a.kv_lens[w.seq];
-            w.first_item = (a.cu_q_lens[w.seq + 1] - w.key_begin) * G;
-            w.num_splits = 1;
-            a.pre_items[base + i] = w;
-        }
-        base += total;
-        __syncthreads();
-    }
-    if (tid == 0) {
-        WsHeader* hdr = a.hdr;
-        hdr->num_items[0] = 0;
-        hdr->num_items[1] = min(base, a.max_pre_items);
-        hdr->next_item[0] = hdr->next_item[1] = hdr->next_item[2] = 0;
-        hdr->prefill_ctas = base > 0 ? a.num_sms : 0;
-        hdr->dec_ctas = hdr->dec_shares = 0;
-        a.cta_first[0] = 0;
-        pdl_wait();  // (as the end of plan_body)
-    }
-    return true;
-}
-
-// Cross attention: block 0 plans, the others write the zero rows of sequences without keys (which
-// the plan leaves out). They wait for the stream's earlier work first: it may still use `out`.
-__global__ void __launch_bounds__(1024) rpa_cross_plan_kernel(RpaArgs a, int one_kernel) {
-    if (blockIdx.x == 0) {
-        if (!one_kernel || !cross_plan_body(a)) plan_body(a);
-        return;
-    }
+// Zero rows of cross attention's sequences without keys (which the plans leave out), by the blocks
+// beside the plan's. They wait for the stream's earlier work first: it may still use `out`.
+__device__ __forceinline__ void cross_zero_body(const RpaArgs& a, int block, int nblocks) {
     pdl_launch_dependents();
     const int num = a.num_seqs[0];
-    if (num < 0 || num > a.max_num_seqs) return;  // (block 0 records it)
+    if (num < 0 || num > a.max_num_seqs) return;  // (the plan records it)
     bool waited = false;
     for (int s = 0; s < num; ++s) {
         if (a.kv_lens[s] != 0) continue;
@@ -482,9 +363,137 @@ __global__ void __launch_bounds__(1024) rpa_cross_plan_kernel(RpaArgs a, int one
         waited = true;
         const size_t row = (size_t)a.num_q_heads * a.head_dim / 8;  // a token's 16-byte chunks
         uint4* out = reinterpret_cast<uint4*>(a.out);
-        for (size_t i = c0 * row + (blockIdx.x - 1) * blockDim.x + threadIdx.x; i < c1 * row;
-             i += (size_t)(gridDim.x - 1) * blockDim.x)
+        for (size_t i = c0 * row + block * blockDim.x + threadIdx.x; i < c1 * row; i += (size_t)nblocks * blockDim.x)
             out[i] = make_uint4(0, 0, 0, 0);
+    }
+}
+
+// Cross attention on the launches of rpa_forward.
+__global__ void __launch_bounds__(1024) rpa_cross_plan_kernel(RpaArgs a) {
+    if (blockIdx.x == 0)
+        plan_body(a);
+    else
+        cross_zero_body(a, blockIdx.x - 1, gridDim.x - 1);
+}
+
+// Cross attention on the kernel with two tiles in flight, which takes every sequence, decode's too: a
+// tile with few rows costs it as many cycles as a full one, but that is still about as fast as HBM gives
+// the keys. When the batch has fewer items than CTAs run at once, its sequences of few rows are cut
+// along their keys, into as many pieces as fill the CTAs, of kCrossMinBlocks blocks at least, as far as
+// the workspace has room for the partial results (slots of 16 rows). Pieces cost: leaving a result and
+// joining takes the softmax warps some 3 us (64 decodes over 1450 keys, 20 heads, which fill the CTAs
+// four times over: 94 us whole, 116 in two pieces each; one decode over 20000 keys, 8 heads of 128: 25 us
+// in pieces, 74 through rpa_forward's launches).
+// (rpa_forward's plan, with decode's equal shares, runs 10 us, most of it instruction fetches: this one
+// is kept small.)
+__global__ void __launch_bounds__(1024) rpa_cross_tc_plan_kernel(RpaArgs a, int ctas, int max_slots) {
+    if (blockIdx.x > 0) {
+        cross_zero_body(a, blockIdx.x - 1, gridDim.x - 1);
+        return;
+    }
+    __shared__ float red[32][2];
+    __shared__ long long scan[40];
+    __shared__ int items_end[1024], slots_end[1024], s_num;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_launch_dependents();
+    if (tid == 0) {
+        const int n = a.num_seqs[0];
+        s_num = n < 0 || n > a.max_num_seqs ? 0 : n;
+        if (n < 0 || n > a.max_num_seqs) set_error(&a.hdr->error_bits, RPA_DEV_ERR_NUM_SEQS);
+    }
+    __syncthreads();
+    const int num = s_num, G = a.num_q_heads / a.num_kv_heads;
+    // a sequence's rows and key blocks (rows 0: nothing to do)
+    auto shape = [&](int s, int& rows, int& blocks) {
+        int ql, kl;
+        rows = blocks = 0;
+        if (s >= num || !seq_shape(a, s, ql, kl) || ql < 1) return;
+        if (!kind_allows(a, ql * G <= 16)) {
+            set_error(&a.hdr->error_bits, RPA_DEV_ERR_BATCH_KIND);
+            return;
+        }
+        rows = ql * G;
+        blocks = cdiv(kl, 128);
+    };
+    int rows0 = 0, blocks0 = 0;       // of this thread's first sequence
+    float v[2] = {0.f, 0.f};          // items, and slots a split would multiply
+    for (int s = tid; s < num; s += blockDim.x) {
+        int rows, blocks;
+        shape(s, rows, blocks);
+        if (s == tid) {
+            rows0 = rows;
+            blocks0 = blocks;
+        }
+        v[0] += (float)cdiv(rows, a.prefill_rows) * a.num_kv_heads;
+        if (rows <= kCrossSplitRows) v[1] += (float)cdiv(rows, kCrossSlotRows) * a.num_kv_heads;
+    }
+    for (int round = 0; round < 2; ++round) {  // over the warp, then over the 32 warps' results
+        if (round) {
+            __syncthreads();
+            v[0] = red[lane][0];
+            v[1] = red[lane][1];
+        }
+#pragma unroll 1
+        for (int o = 16; o > 0; o >>= 1) {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+            v[1] += __shfl_xor_sync(0xffffffffu, v[1], o);
+        }
+        if (!round && lane == 0) {
+            red[warp][0] = v[0];
+            red[warp][1] = v[1];
+        }
+    }
+    // pieces of a sequence: as many as fill the CTAs, and as every sequence of few rows finds slots for
+    // (a little fewer: the sums are floats)
+    if (warp == 0) red[lane][0] = fminf((float)ctas / fmaxf(v[0], 1.f), (float)max_slots / (v[1] * 1.001f + 1.f));
+    __syncthreads();
+    const int most = min(kCrossMaxSplits, (int)red[0][0]);
+    int base = 0, slot_base = 0;
+    for (int s0 = 0; s0 < num; s0 += blockDim.x) {
+        if (s0) shape(s0 + tid, rows0, blocks0);
+        const int pieces = rows0 <= kCrossSplitRows ? max(1, min(most, blocks0 / kCrossMinBlocks)) : 1;
+        const int n = cdiv(rows0, a.prefill_rows) * a.num_kv_heads * pieces;
+        const int slots = pieces > 1 ? cdiv(rows0, kCrossSlotRows) * a.num_kv_heads * pieces : 0;
+        long long total;
+        const long long before = block_exclusive_scan(((long long)slots << 32) | n, scan, &total);
+        items_end[tid] = (int)(before & 0xffffffffll) + n;
+        slots_end[tid] = (int)(before >> 32) + slots;
+        __syncthreads();
+        const int total_n = (int)(total & 0xffffffffll);
+        for (int i = tid; i < total_n && base + i < a.max_pre_items; i += blockDim.x) {
+            int lo = 0, hi = min((int)blockDim.x, num - s0) - 1;  // the first sequence whose end exceeds i
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (items_end[mid] > i) hi = mid; else lo = mid + 1;
+            }
+            const int rel = i - (lo ? items_end[lo - 1] : 0);
+            const int slot0 = lo ? slots_end[lo - 1] : 0;
+            WorkItem w;
+            w.seq = s0 + lo;
+            w.key_begin = a.cu_q_lens[w.seq];
+            w.key_end = a.kv_lens[w.seq];
+            w.first_item = (a.cu_q_lens[w.seq + 1] - w.key_begin) * G;
+            const int tiles = cdiv(w.first_item, a.prefill_rows);
+            w.num_splits = (items_end[lo] - (lo ? items_end[lo - 1] : 0)) / (tiles * a.num_kv_heads);
+            // pieces of one head together, heads of one tile together
+            w.split = rel % w.num_splits;
+            w.head = rel / w.num_splits % a.num_kv_heads;
+            w.row_begin = rel / (w.num_splits * a.num_kv_heads) * a.prefill_rows;
+            if (w.num_splits > 1) {  // (one tile) row_begin: the first slot of this head's pieces
+                w.row_begin = slot_base + slot0 + w.head * w.num_splits * cdiv(w.first_item, kCrossSlotRows);
+                if (w.split == 0) a.tickets[w.row_begin / 2] = 0;
+            }
+            a.pre_items[base + i] = w;
+        }
+        base += total_n;
+        slot_base += (int)(total >> 32);
+        __syncthreads();
+    }
+    if (tid == 0) {
+        WsHeader* hdr = a.hdr;
+        hdr->num_items[1] = min(base, a.max_pre_items);
+        hdr->next_item[1] = 0;
+        pdl_wait();  // (as the end of plan_body)
     }
 }
 
@@ -647,26 +656,22 @@ cudaError_t launch_rpa_forward(const RpaArgs& a, int num_sms, cudaStream_t strea
     return launch_attention(a, num_sms, stream);
 }
 
-// Cross attention: the plan with the zero rows beside it, then the kernel with two tiles in flight,
-// where it takes the batch, and decode behind it (started early, it waits for that grid unless there
-// was nothing for it; it finds no item when the plan gave every sequence to the one kernel); else the
-// launches of rpa_forward.
-cudaError_t launch_rpa_cross(RpaArgs& a, int num_sms, cudaStream_t stream) {
-    const bool tc = rpa_cross_tc_takes(a) && a.batch_kind != RPA_BATCH_DECODE_ONLY;
-    if (tc) {
-        a.split_sms = 0;
-        a.prefill_rows = rpa_cross_tile_rows(a);
-    }
+// Cross attention: the plan with the zero rows beside it, then the kernel with two tiles in flight
+// alone, where it takes the batch, else the launches of rpa_forward.
+cudaError_t launch_rpa_cross(RpaArgs& a, int max_slots, int num_sms, cudaStream_t stream) {
+    const bool tc = rpa_cross_tc_takes(a);
+    if (tc) a.prefill_rows = rpa_cross_tile_rows(a);
     cudaError_t e;
     {
         ProfScope ps("rpa_plan", stream);
-        e = launch_pdl(rpa_cross_plan_kernel, dim3(1 + kCrossZeroBlocks), dim3(1024), 0, stream, a.overlap != 0, a, tc ? 1 : 0);
+        if (tc)
+            e = launch_pdl(rpa_cross_tc_plan_kernel, dim3(1 + kCrossZeroBlocks), dim3(1024), 0, stream, a.overlap != 0, a,
+                           num_sms * (a.prefill_rows == 128 ? 2 : 1), max_slots);
+        else
+            e = launch_pdl(rpa_cross_plan_kernel, dim3(1 + kCrossZeroBlocks), dim3(1024), 0, stream, a.overlap != 0, a);
     }
     if (e != cudaSuccess) return e;
-    if (!tc) return launch_attention(a, num_sms, stream);
-    e = launch_rpa_cross_tc(a, num_sms, stream);
-    if (e != cudaSuccess || a.batch_kind == RPA_BATCH_PREFILL_ONLY) return e;
-    return launch_rpa_decode(a, num_sms, stream);
+    return tc ? launch_rpa_cross_tc(a, num_sms, stream) : launch_attention(a, num_sms, stream);
 }
 
 cudaError_t launch_rpa_forward_update(const RpaArgs& a, const RpaUpdateArgs& u, int num_sms, cudaStream_t stream) {
