@@ -336,7 +336,7 @@ RPA_API int rpa_rope_update_kv_cache(const rpa_params* p, const rope_table* t, c
                                      size_t workspace_bytes, rpa_stream_t stream);
 
 /* rpa_rope_update_kv_cache, then rpa_forward of the turned queries over the updated cache, in one
- * call.  `q_rot` is rpa_rope_update_kv_cache's q_out (not NULL; the caller's, holding the turned
+ * call (`out` equals the two calls' up to rounding: the keys of a decode may be split elsewhere).  `q_rot` is rpa_rope_update_kv_cache's q_out (not NULL; the caller's, holding the turned
  * queries afterwards), `out` and `workspace` are rpa_forward's; the workspace's error word also
  * records the cache write's metadata errors.  `out` must not alias q, q_rot, kv_pages, new_k or
  * new_v. */

@@ -410,6 +410,7 @@ static int rpa_prepare(const rpa_params* p, const void* q, const void* kv_pages,
               rpa_pow2_scale(a.k_scale_or_one) && rpa_pow2_scale(a.v_scale_or_one), &a.pre_flops_per_ns_sm,
               &a.dec_bytes_per_ns_sm);
     a.item_cost_keys = rpa_item_cost_keys(a.kv_byte || a.has_scale);
+    a.min_chunk = kMinChunk;
     a.decode_per_sm = rpa_decode_ctas_per_sm(a);
     if (a.decode_per_sm <= 0) return fail(RPA_ERR_CUDA, "decode kernel occupancy query failed");
     a.hdr = reinterpret_cast<WsHeader*>(ws);
@@ -699,6 +700,7 @@ int rpa_rope_forward_update(const rpa_params* p, const rope_table* t, const rope
     // so few query rows that every sequence is decode-class: the prefill launches are left out
     if (a.batch_kind == RPA_BATCH_MIXED && (long long)p->max_num_tokens * (a.num_q_heads / a.num_kv_heads) <= 16)
         a.batch_kind = RPA_BATCH_DECODE_ONLY;
+    a.min_chunk = kStepMinChunk;
     cudaError_t e = launch_rope_update(u, sms, reinterpret_cast<cudaStream_t>(stream));
     if (e == cudaSuccess) e = launch_rpa_forward(a, sms, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "rpa_rope_forward_update launch");

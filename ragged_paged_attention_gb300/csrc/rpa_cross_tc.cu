@@ -149,10 +149,9 @@ __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // started early behind the plan: its lists are complete from here on; the decode grid behind may
-    // start too (it waits for this grid's end before it works)
+    // started early behind the plan, whose lists are complete from here on. (Nothing may start early
+    // behind this grid: the next call's plan would overwrite the lists under it.)
     pdl_wait();
-    pdl_launch_dependents();
 
     uint32_t items = 0;  // items this CTA has taken (ring slots, q phases)
     // Reads the next item (every warp); false when there is none.

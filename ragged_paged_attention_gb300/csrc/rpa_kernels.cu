@@ -180,13 +180,13 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
         // decode CTAs resident at once: beside the prefill share, or every slot
         int ctas = (n_pre > 0 && n_pre < S ? S - n_pre : S) * a.decode_per_sm;
         ctas = max(1, min(ctas, kMaxDecodeCtas / 2));
-        // static shares: all but the pool's part of the line, none under kMinChunk keys
+        // static shares: all but the pool's part of the line, none under min_chunk keys
         const long long w_static = W * (100 - kPoolPercent) / 100;
         long long q1 = div_nn(w_static, ctas) / kDecodeBK * kDecodeBK;
         int r = ctas;
-        if (q1 < kMinChunk) {
-            q1 = kMinChunk;
-            r = (int)min((long long)ctas, div_nn(w_static, kMinChunk));
+        if (q1 < a.min_chunk) {
+            q1 = a.min_chunk;
+            r = (int)min((long long)ctas, div_nn(w_static, a.min_chunk));
         }
         const long long ls = (long long)r * q1;
         // pooled shares: about kPoolPerCta per CTA, at least kMinPoolChunk keys, within the bound

@@ -180,6 +180,27 @@ def test_calls_on_two_streams_at_once():
         assert torch.equal(out.cpu().view(torch.int16), ref.view(torch.int16))
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_calls_back_to_back_share_a_workspace(d):
+    # calls on one stream, one workspace, nothing waits between them: different batches take turns
+    bs = [batch([1] * 20 + [90], [1500] * 21, 8, 2, d, 16, seed=1), batch([60] * 8, [900] * 8, 8, 2, d, 16, seed=2),
+          batch([2], [9000], 8, 2, d, 16, seed=3), batch([0, 5], [7, 0], 8, 2, d, 16, seed=4)]
+    want = [check(b, TOL_BF16) for b in bs]
+    g = [b.to("cuda") for b in bs]
+    size = max(api.rpa_cross_workspace_size(api.make_rpa_params(b.q, b.kv_pages, b.page_indices)) for b in g)
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    outs = [[torch.full_like(b.q, 7.0) for b in g] for _ in range(10)]
+    torch.cuda.synchronize()
+    for turn in outs:
+        for b, out in zip(g, turn):
+            api.rpa_cross_forward(b.q, b.kv_pages, b.kv_lens, b.page_indices, b.cu_q_lens, b.num_seqs, sm_scale=b.sm_scale,
+                                  out=out, workspace=ws)
+    assert api.check_device_status(ws) == 0
+    for turn in outs:
+        for out, ref in zip(turn, want):
+            assert torch.equal(out.cpu().view(torch.int16), ref.view(torch.int16))
+
+
 # ------------------------------------------------------------------ the fused step
 def step_inputs(b, seed):
     """bf16 new rows for a batch whose cache may be narrower."""
@@ -209,11 +230,13 @@ def test_step_is_the_write_then_attention(dtype, ks, vs, kw):
     n = b.num_tokens
     assert torch.equal(g.kv_pages.view(torch.uint8), pages.view(torch.uint8))
     assert torch.equal(q_rot[:n].view(torch.int16), q_out[:n].view(torch.int16)) and (q_rot[n:].float() == 5.0).all()
-    assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+    # (the step may cut decode's keys elsewhere than rpa_forward does: equal up to rounding)
+    tol = (TOL_BF16 if dtype == BF16 else TOL_FP8) * (3 if dtype in (INT8, INT4) else 1)
+    assert (out[:n].double() - want[:n].double()).abs().max().item() <= tol and (out[n:].float() == 7.0).all()
     # and against the oracle, which attends over the cache as written
     ref = oracle.rpa(q_rot.cpu(), g.kv_pages.cpu(), b.kv_lens, b.page_indices, b.cu_q_lens, len(b.q_lens), **b.options())
     err = (out[:n].cpu().double() - ref[:n]).abs().max().item()
-    assert err <= (TOL_BF16 if dtype == BF16 else TOL_FP8) * (3 if dtype in (INT8, INT4) else 1)
+    assert err <= tol
 
 
 def test_step_reports_bad_metadata_and_refuses():
