@@ -573,16 +573,20 @@ static cudaError_t launch_cross(const RpaArgs& a, int num_sms, cudaStream_t stre
                                 const CUtensorMap& tq, int box_rows) {
     using T = CrossTc<D, TILES>;
     auto kern = rpa_cross_tc_kernel<D, TILES>;
-    static bool configured = false;
-    if (!configured) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
+    static bool configured[64] = {};  // (by device: the attribute is the device's)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!configured[dev]) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
         if (e != cudaSuccess) return e;
         // the warpgroups' register shares are dealt out of what the launch holds
         cudaFuncAttributes fa;
         e = cudaFuncGetAttributes(&fa, kern);
         if (e != cudaSuccess) return e;
         if (fa.numRegs != T::kRegsLaunch) return cudaErrorLaunchOutOfResources;
-        configured = true;
+        configured[dev] = true;
     }
     ProfScope ps("rpa_cross_tc", stream);
     return launch_pdl(kern, dim3(num_sms * T::kCtas), dim3(T::kThreads), T::kSmem, stream, a.overlap != 0, a, tkv, tq, box_rows);

@@ -354,17 +354,28 @@ __device__ __forceinline__ void cross_zero_body(const RpaArgs& a, int block, int
     pdl_launch_dependents();
     const int num = a.num_seqs[0];
     if (num < 0 || num > a.max_num_seqs) return;  // (the plan records it)
+    __shared__ int found[1024], n_found;
     bool waited = false;
-    for (int s = 0; s < num; ++s) {
-        if (a.kv_lens[s] != 0) continue;
-        const int c0 = a.cu_q_lens[s], c1 = a.cu_q_lens[s + 1];
-        if (c0 < 0 || c1 < c0 || c1 > a.max_num_tokens) continue;
-        if (!waited) pdl_wait();
-        waited = true;
-        const size_t row = (size_t)a.num_q_heads * a.head_dim / 8;  // a token's 16-byte chunks
-        uint4* out = reinterpret_cast<uint4*>(a.out);
-        for (size_t i = c0 * row + block * blockDim.x + threadIdx.x; i < c1 * row; i += (size_t)nblocks * blockDim.x)
-            out[i] = make_uint4(0, 0, 0, 0);
+    for (int s0 = 0; s0 < num; s0 += blockDim.x) {
+        if (threadIdx.x == 0) n_found = 0;
+        __syncthreads();
+        const int s = s0 + threadIdx.x;
+        if (s < num && a.kv_lens[s] == 0) {
+            const int c0 = a.cu_q_lens[s], c1 = a.cu_q_lens[s + 1];
+            if (c0 >= 0 && c1 > c0 && c1 <= a.max_num_tokens) found[atomicAdd(&n_found, 1)] = s;
+        }
+        __syncthreads();
+        const int n = n_found;
+        if (n > 0 && !waited) pdl_wait();
+        waited = waited || n > 0;
+        for (int i = 0; i < n; ++i) {
+            const int c0 = a.cu_q_lens[found[i]], c1 = a.cu_q_lens[found[i] + 1];
+            const size_t row = (size_t)a.num_q_heads * a.head_dim / 8;  // a token's 16-byte chunks
+            uint4* out = reinterpret_cast<uint4*>(a.out);
+            for (size_t j = c0 * row + block * blockDim.x + threadIdx.x; j < c1 * row; j += (size_t)nblocks * blockDim.x)
+                out[j] = make_uint4(0, 0, 0, 0);
+        }
+        __syncthreads();  // the next sequences reuse the list
     }
 }
 

@@ -91,6 +91,29 @@ def test_batch_shapes(q_lens, kv_lens):
     check(batch(q_lens, kv_lens, 8, 2, 128, 16, seed=len(q_lens)), TOL_BF16)
 
 
+@pytest.mark.parametrize("d,dtype", [(64, BF16), (128, BF16), (128, FP8)])
+def test_many_sequences(d, dtype):
+    # more sequences than the plan's block has threads; a third without keys, some without queries
+    rng = np.random.default_rng(5)
+    q_lens = rng.integers(0, 3, 2500).tolist()
+    kv_lens = (rng.integers(0, 40, 2500) * (rng.random(2500) < 0.7)).tolist()
+    check(batch(q_lens, kv_lens, 4, 2, d, 16, dtype=dtype, seed=6), TOL_BF16 if dtype == BF16 else TOL_FP8)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 64), (8, 2, 128), (32, 1, 128), (3, 3, 64)])
+@pytest.mark.parametrize("q_lens,kv_lens", [([1], [513]), ([1, 2], [5000, 511]), ([8, 1, 0], [3000, 1, 9]), ([2, 9], [4097, 2048])])
+def test_sequences_cut_along_their_keys(hq, hkv, d, q_lens, kv_lens):
+    # few items: the keys of sequences of up to 32 rows are shared out, others stay whole
+    check(batch(q_lens, kv_lens, hq, hkv, d, 32, seed=hq + d), TOL_BF16)
+
+
+def test_no_sequences_and_one_stream_of_nothing():
+    b = batch([2, 40], [30, 50], 8, 2, 128, 16, seed=1)
+    b.num_seqs[0] = 0
+    out, bits = run(b)
+    assert bits == 0 and (out.float() == 7.0).all()
+
+
 def test_extreme_logits_and_offsets():
     # logits of +-thousands, one key far above the rest at either end, equal keys
     b = batch([3, 50, 2], [900, 260, 900], 4, 2, 128, 16, seed=11)

@@ -227,7 +227,8 @@ def check_write(b, q_out, kv, f, amp, inter, positions=None, k_scale=None, v_sca
                                          (INT8, 0.02, 0.03), (INT4, 0.3, 0.4)], ids=str)
 @pytest.mark.parametrize("hq,hkv,d,rot,inter,ps,strided", [
     (8, 2, 128, 128, False, 16, True), (6, 2, 64, 64, True, 8, False), (4, 4, 256, 64, False, 32, True),
-    (3, 1, 96, 24, False, 4, False), (5, 5, 192, 192, True, 12, False), (2, 1, 128, 20, True, 16, True)])
+    (3, 1, 96, 24, False, 4, False), (5, 5, 192, 192, True, 12, False), (2, 1, 128, 20, True, 16, True),
+    (3, 3, 96, 96, False, 16, True), (4, 1, 128, 16, False, 1, False)])
 def test_update(dtype, ks, vs, hq, hkv, d, rot, inter, ps, strided):
     b = make_batch([1, 0, 37, 1, 5], [40000, 70, 37, 1, 300], hq, hkv, d, ps, dtype, seed=d + rot, pad=3, strided=strided)
     t = api.make_rope_table(rot, base=500000.0, interleaved=inter, scaling=LLAMA3)
@@ -252,6 +253,33 @@ def test_update_batch_shapes(n, T):
     b = make_batch([T] * n, [T + (13 * s) % 90 for s in range(n)], 4, 2, 64, 16, BF16, seed=n, pad=1)
     t, (f, amp) = api.make_rope_table(64, scaling=YARN), plain.frequencies(64, 10000.0, YARN)
     check_write(b, *write(b, t), f, amp, False)
+
+
+def test_update_of_no_sequences():
+    b = make_batch([2, 3], [20, 9], 4, 2, 128, 16, BF16, seed=1)
+    b["num"][0] = 0
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    q_out, kv = write(b, api.make_rope_table(64), workspace=ws)
+    assert (q_out.float() == 7.0).all() and torch.equal(bits(kv), bits(b["kv"])) and api.check_device_status(ws) == 0
+
+
+def test_update_behind_four_gigabytes():
+    # the last pages of a cache of 9.8 GB, with rows of another cache's size in front
+    hq, hkv, d, ps, pages = 4, 4, 128, 16, 300000
+    kv = torch.empty(pages, ps, 2 * hkv, d, dtype=BF16, device="cuda")
+    kv[-3:].zero_()
+    q, k, v = randn(1, 20, hq, d), randn(2, 20, hkv, d), randn(3, 20, hkv, d)
+    table = torch.tensor([[pages - 1, pages - 2]], dtype=torch.int32, device="cuda")
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    t, (f, amp) = api.make_rope_table(128), plain.frequencies(128)
+    api.rpa_rope_update_kv_cache(q.cuda(), k.cuda(), v.cuda(), kv, i32(20), table, i32(0, 20), i32(1), t)
+    got = kv[[pages - 1, pages - 2]].flatten(0, 1)[:20].cpu()
+    near(got[:, 0::2], plain.rope(k, torch.arange(20), f, amp, False), plain.rope_slack(k, f, amp, False))
+    assert torch.equal(bits(got[:, 1::2]), bits(v))
+    # and read from there: every query over the 20 keys
+    out = api.rpa_cross_forward(q.cuda(), kv, i32(20), table, i32(0, 20), i32(1), sm_scale=0.1)
+    ref = plain.attend_all(q, kv[-3:].cpu(), torch.tensor([20]), torch.tensor([[2, 1]]), torch.tensor([0, 20]), 1, sm_scale=0.1)
+    assert (out.cpu().double() - ref).abs().max() <= 2e-2
 
 
 def test_update_without_queries_other_positions_and_no_turn():
