@@ -219,6 +219,8 @@ class Workspace:
 
 _workspaces: dict = {}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+_current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_BF16, _I32 = torch.bfloat16, torch.int32
 
 
 def _own_workspace(nbytes: int, device: int, stream: int) -> torch.Tensor:
@@ -440,14 +442,16 @@ def make_rope_table(rotary_dim, *, base=10000.0, interleaved=False, scaling=None
 def _rows(t, name: str, device: int, heads: int = 0, dim: int = 0):
     """(token stride, head stride) of bf16 rows [tokens, heads, head_dim] on ``device``; any strides with
     adjacent elements and 16-byte aligned rows.  ``heads`` and ``dim``, where given, must match."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != device or device < 0:
-        raise ValueError(f"{name} must be a CUDA tensor on device {device}")
-    if t.dtype is not torch.bfloat16 or t.dim() != 3:
-        raise ValueError(f"{name} must be bfloat16 [tokens, heads, head_dim], got {t.dtype} {tuple(t.shape)}")
-    n, h, d = t.shape
+    try:
+        n, h, d = t.shape
+        token, head, element = t.stride()
+        good = t.dtype is _BF16 and t.get_device() == device
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if not good:
+        raise ValueError(f"{name} must be a bfloat16 CUDA tensor [tokens, heads, head_dim] on device {device}")
     if (heads and h != heads) or (dim and d != dim):
         raise ValueError(f"{name} must have {heads or h} heads of {dim or d}, got {tuple(t.shape)}")
-    token, head, element = t.stride()
     if h <= 1:  # the stride of a dimension of one entry says nothing
         head = d
     if n <= 1:
@@ -460,10 +464,12 @@ def _rows(t, name: str, device: int, heads: int = 0, dim: int = 0):
 
 def _on(device: int, t, name: str, dtype, n: int = -1):
     """Checks a contiguous tensor of ``dtype`` on ``device`` (of ``n`` elements, where given)."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != device or device < 0:
-        raise ValueError(f"{name} must be a CUDA tensor on device {device}")
-    if t.dtype is not dtype or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous {dtype}, got {t.dtype}")
+    try:
+        good = t.dtype is dtype and t.get_device() == device and t.is_contiguous()
+    except AttributeError:
+        good = False
+    if not good:
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor on device {device}")
     if n >= 0 and t.numel() != n:
         raise ValueError(f"{name} must have {n} elements, got shape {tuple(t.shape)}")
 
@@ -487,12 +493,12 @@ def rope_apply(q, k, positions, table, *, inverse=False, q_out=None, k_out=None)
     lib = _lib or load_library()
     _is_table(table)
     dev = _cuda_index(q, "q")
-    if dev != torch.cuda.current_device():
+    if dev != _current():
         with torch.cuda.device(dev):
             return rope_apply(q, k, positions, table, inverse=inverse, q_out=q_out, k_out=k_out)
     q_token, q_head = _rows(q, "q", dev)
     T, hq, d = q.shape
-    _on(dev, positions, "positions", torch.int32, T)
+    _on(dev, positions, "positions", _I32, T)
     if q_out is None:
         q_out = torch.empty((T, hq, d), dtype=torch.bfloat16, device=q.device)
     qo_token, qo_head = (q_token, q_head) if q_out is q else _rows(q_out, "q_out", dev)
@@ -531,13 +537,13 @@ def _batch_params(dev, tokens, hq, d, kv_pages, kv_lens, page_indices, cu_q_lens
     pages, ps, combined, width = kv_pages.shape
     if (width * 2 if code == INT4 else width) != d:
         raise ValueError(f"kv_pages hold heads of {kv_head_dim(kv_pages)}, the rows {d}")
-    _on(dev, page_indices, "page_indices", torch.int32)
+    _on(dev, page_indices, "page_indices", _I32)
     if page_indices.dim() != 2:
         raise ValueError("page_indices must be [max_num_seqs, pages_per_seq]")
     seqs, pps = page_indices.shape
-    _on(dev, kv_lens, "kv_lens", torch.int32, seqs)
-    _on(dev, cu_q_lens, "cu_q_lens", torch.int32, seqs + 1)
-    _on(dev, num_seqs, "num_seqs", torch.int32, 1)
+    _on(dev, kv_lens, "kv_lens", _I32, seqs)
+    _on(dev, cu_q_lens, "cu_q_lens", _I32, seqs + 1)
+    _on(dev, num_seqs, "num_seqs", _I32, 1)
     return rpa_params(_PARAMS_SIZE, ABI_VERSION, tokens, hq, combined, d, pages, ps, seqs, pps, BF16, code, sm_scale,
                       sliding_window or 0, soft_cap or 0.0, math.nan if mask_value is None else mask_value, k_scale or 0.0,
                       v_scale or 0.0, batch_kind)
@@ -568,7 +574,7 @@ def _rope_update_args(dev, q, new_k, new_v, kv_pages, kv_lens, page_indices, cu_
     elif q_out is not None:
         raise ValueError("q_out goes with q")
     if positions is not None:
-        _on(dev, positions, "positions", torch.int32, T)
+        _on(dev, positions, "positions", _I32, T)
     prm = _batch_params(dev, T, hkv if q is None else q.shape[1], d, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, **opts)
     if prm.num_combined_kv_heads != 2 * hkv:
         raise ValueError(f"kv_pages have {prm.num_combined_kv_heads} combined heads, new_k and new_v {hkv} each")
@@ -586,7 +592,7 @@ def rpa_rope_update_kv_cache(q, new_k, new_v, kv_pages, kv_lens, page_indices, c
     ``workspace``'s error word where one is given."""
     lib = _lib or load_library()
     dev = _cuda_index(new_k, "new_k")
-    if dev != torch.cuda.current_device():
+    if dev != _current():
         with torch.cuda.device(dev):
             return rpa_rope_update_kv_cache(q, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, table,
                                             positions=positions, k_scale=k_scale, v_scale=v_scale, q_out=q_out,
@@ -631,7 +637,7 @@ def rpa_rope_forward_update(q, new_k, new_v, kv_pages, kv_lens, page_indices, cu
     writes ``kv_pages`` in place and returns ``out`` [T, Hq, D]."""
     lib = _lib or load_library()
     dev = _cuda_index(q, "q")
-    if dev != torch.cuda.current_device():
+    if dev != _current():
         with torch.cuda.device(dev):
             return rpa_rope_forward_update(q, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, table,
                                            positions=positions, sm_scale=sm_scale, sliding_window=sliding_window,
@@ -667,7 +673,7 @@ def rpa_cross_forward(q, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, *
     encoder's states); returns ``out`` [max_num_tokens, Hq, D] bf16.  A sequence without keys gets zeros."""
     lib = _lib or load_library()
     dev = _cuda_index(q, "q")
-    if dev != torch.cuda.current_device():
+    if dev != _current():
         with torch.cuda.device(dev):
             return rpa_cross_forward(q, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, sm_scale=sm_scale,
                                      soft_cap=soft_cap, k_scale=k_scale, v_scale=v_scale, out=out, workspace=workspace,
