@@ -700,7 +700,7 @@ int rpa_rope_forward_update(const rpa_params* p, const rope_table* t, const rope
     // so few query rows that every sequence is decode-class: the prefill launches are left out
     if (a.batch_kind == RPA_BATCH_MIXED && (long long)p->max_num_tokens * (a.num_q_heads / a.num_kv_heads) <= 16)
         a.batch_kind = RPA_BATCH_DECODE_ONLY;
-    a.min_chunk = kStepMinChunk;
+    a.min_chunk = kStepMinChunk + a.item_cost_keys;
     cudaError_t e = launch_rope_update(u, sms, reinterpret_cast<cudaStream_t>(stream));
     if (e == cudaSuccess) e = launch_rpa_forward(a, sms, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "rpa_rope_forward_update launch");

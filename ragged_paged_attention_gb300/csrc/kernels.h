@@ -25,9 +25,10 @@ __host__ __device__ inline int update_cache_ints(int max_num_seqs) {
 }
 constexpr int kPrefillRows = 128;       // (token, q-head) rows per prefill item (one TMEM tile)
 constexpr int kMinChunk = 256;          // smallest split-KV chunk (keys)
-// rpa_rope_forward_update's, which its small decode batches meet: 7 decodes over some 1500 fp8 keys of
-// 8 heads take 37.9 us with chunks of 256 keys at least, 33.3 with 128, 36.1 with 64 (more to join);
-// batches that fill the SMs are cut longer than either
+// rpa_rope_forward_update's, beside a group's cost on the line (so that every share holds keys), which its
+// small decode batches meet: 7 decodes over some 1500 fp8 keys of 8 heads take 37.9 us with chunks of 256
+// keys at least, 33.3 with 128, 36.1 with 64 (more to join); batches that fill the SMs are cut longer than
+// either
 constexpr int kStepMinChunk = 128;
 // Cross attention's two-tile kernel: a sequence of up to kCrossSplitRows rows may be cut along its keys
 // into up to kCrossMaxSplits pieces of kCrossMinBlocks 128-key blocks or more, whose results wait in
@@ -124,7 +125,7 @@ struct RpaArgs {
     float pre_flops_per_ns_sm;  // prefill kernel rate per SM (this head size and cache type)
     float dec_bytes_per_ns_sm;  // decode kernel rate per SM while SMs, not HBM, limit it
     int item_cost_keys;         // per-group cost on the decode line (a multiple of 16 keys)
-    int min_chunk;              // smallest static decode share (keys, a multiple of 16)
+    int min_chunk;              // smallest static decode share (a multiple of 16 above item_cost_keys)
     // workspace
     WsHeader* hdr;
     WorkItem* dec_items;

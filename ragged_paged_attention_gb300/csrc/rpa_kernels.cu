@@ -180,7 +180,8 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
         // decode CTAs resident at once: beside the prefill share, or every slot
         int ctas = (n_pre > 0 && n_pre < S ? S - n_pre : S) * a.decode_per_sm;
         ctas = max(1, min(ctas, kMaxDecodeCtas / 2));
-        // static shares: all but the pool's part of the line, none under min_chunk keys
+        // static shares: all but the pool's part of the line, none under min_chunk (which is longer than
+        // a group's cost: a share without a key would have no item that opens it)
         const long long w_static = W * (100 - kPoolPercent) / 100;
         long long q1 = div_nn(w_static, ctas) / kDecodeBK * kDecodeBK;
         int r = ctas;

@@ -262,6 +262,32 @@ def test_step_is_the_write_then_attention(dtype, ks, vs, kw):
     assert err <= tol
 
 
+@pytest.mark.parametrize("dtype,ks,vs", [(BF16, None, None), (FP8, None, None), (FP8, 0.5, 0.25)], ids=str)
+@pytest.mark.parametrize("hq,hkv,d,ps", [(12, 2, 64, 16), (64, 8, 256, 8), (8, 4, 128, 16), (16, 16, 128, 64)])
+def test_step_of_small_decode_batches(dtype, ks, vs, hq, hkv, d, ps):
+    """Decode shares shorter than rpa_forward's: batches whose shares are as short as they get, on one
+    workspace that each leaves its lists in for the next."""
+    t = api.make_rope_table(d)
+    lens = [([1] * 24, list(range(20, 2000, 83))), ([1] * 4 + [23], [2788, 300, 16, 1100, 523]), ([1], [129]), ([1] * 9, [1] * 9),
+            ([2, 1, 1], [640, 128, 127]), ([1] * 40, [150] * 40), ([1], [5000])]
+    ws = torch.zeros(1 << 27, dtype=torch.uint8, device="cuda")
+    for i, (q_lens, kv_lens) in enumerate(lens):
+        b = batch(q_lens, kv_lens, hq, hkv, d, ps, dtype=dtype, seed=40 + i, k_scale=ks, v_scale=vs)
+        k, v = step_inputs(b, i)
+        g, k, v = b.to("cuda"), k.cuda(), v.cuda()
+        meta = (g.kv_lens, g.page_indices, g.cu_q_lens, g.num_seqs)
+        q_rot, out = torch.empty_like(g.q), torch.full_like(g.q, 7.0)
+        for _ in range(2):  # (the same rows again: the same cache)
+            out.fill_(7.0)
+            api.rpa_rope_forward_update(g.q, k, v, g.kv_pages, *meta, t, q_rot=q_rot, out=out, workspace=ws, **b.options())
+        assert api.check_device_status(ws) == 0
+        n = b.num_tokens
+        ref = oracle.rpa(q_rot.cpu(), g.kv_pages.cpu(), b.kv_lens, b.page_indices, b.cu_q_lens, len(b.q_lens), **b.options())
+        err = (out[:n].cpu().double() - ref[:n]).abs().max().item()
+        assert err <= (TOL_BF16 if dtype == BF16 else TOL_FP8), (i, err)
+        assert (out[n:].float() == 7.0).all()
+
+
 def test_step_reports_bad_metadata_and_refuses():
     b = batch([1, 4], [30, 20], 8, 2, 128, 16, seed=2)
     k, v = (x.cuda() for x in step_inputs(b, 1))
