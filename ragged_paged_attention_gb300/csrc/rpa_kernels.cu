@@ -396,8 +396,8 @@ __global__ void __launch_bounds__(1024) rpa_cross_plan_kernel(RpaArgs a) {
 // joining takes the softmax warps some 3 us (64 decodes over 1450 keys, 20 heads, which fill the CTAs
 // four times over: 94 us whole, 116 in two pieces each; one decode over 20000 keys, 8 heads of 128: 25 us
 // in pieces, 74 through rpa_forward's launches).
-// (rpa_forward's plan, with decode's equal shares, runs 10 us, most of it instruction fetches: this one
-// is kept small.)
+// (rpa_forward's plan, with decode's equal shares, takes 8 to 10 us, a chain of latencies: this one is kept
+// short, 3 to 4 us.)
 __global__ void __launch_bounds__(1024) rpa_cross_tc_plan_kernel(RpaArgs a, int ctas, int max_slots) {
     if (blockIdx.x > 0) {
         cross_zero_body(a, blockIdx.x - 1, gridDim.x - 1);
@@ -405,10 +405,11 @@ __global__ void __launch_bounds__(1024) rpa_cross_tc_plan_kernel(RpaArgs a, int 
     }
     __shared__ float red[32][2];
     __shared__ long long scan[40];
-    __shared__ int items_end[1024], slots_end[1024], s_num;
+    __shared__ int items_end[1024], slots_end[1024], order[1024], s_num, s_most, in_class[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_launch_dependents();
     if (tid == 0) {
+        s_most = 0;
         const int n = a.num_seqs[0];
         s_num = n < 0 || n > a.max_num_seqs ? 0 : n;
         if (n < 0 || n > a.max_num_seqs) set_error(&a.hdr->error_bits, RPA_DEV_ERR_NUM_SEQS);
@@ -429,6 +430,7 @@ __global__ void __launch_bounds__(1024) rpa_cross_tc_plan_kernel(RpaArgs a, int 
     };
     int rows0 = 0, blocks0 = 0;       // of this thread's first sequence
     float v[2] = {0.f, 0.f};          // items, and slots a split would multiply
+    int top = 0;                      // most key blocks
     for (int s = tid; s < num; s += blockDim.x) {
         int rows, blocks;
         shape(s, rows, blocks);
@@ -436,9 +438,12 @@ __global__ void __launch_bounds__(1024) rpa_cross_tc_plan_kernel(RpaArgs a, int 
             rows0 = rows;
             blocks0 = blocks;
         }
+        top = max(top, blocks);
         v[0] += (float)cdiv(rows, a.prefill_rows) * a.num_kv_heads;
         if (rows <= kCrossSplitRows) v[1] += (float)cdiv(rows, kCrossSlotRows) * a.num_kv_heads;
     }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0 && top > 0) atomicMax(&s_most, top);
     for (int round = 0; round < 2; ++round) {  // over the warp, then over the 32 warps' results
         if (round) {
             __syncthreads();
@@ -457,23 +462,61 @@ __global__ void __launch_bounds__(1024) rpa_cross_tc_plan_kernel(RpaArgs a, int 
     }
     // pieces of a sequence: as many as fill the CTAs, and as every sequence of few rows finds slots for
     // (a little fewer: the sums are floats)
-    if (warp == 0) red[lane][0] = fminf((float)ctas / fmaxf(v[0], 1.f), (float)max_slots / (v[1] * 1.001f + 1.f));
+    if (warp == 0) {
+        red[lane][0] = fminf((float)ctas / fmaxf(v[0], 1.f), (float)max_slots / (v[1] * 1.001f + 1.f));
+        red[lane][1] = v[0];
+    }
     __syncthreads();
     const int most = min(kCrossMaxSplits, (int)red[0][0]);
+    const bool many = s_most > 1 && red[0][1] > (float)ctas;
     int base = 0, slot_base = 0;
     for (int s0 = 0; s0 < num; s0 += blockDim.x) {
         if (s0) shape(s0 + tid, rows0, blocks0);
+        // More items than CTAs, and more than a block each: sequences with more key blocks first, in 32
+        // classes of their share of the most. CTAs take the items in turn, and short ones at the end leave
+        // them less to wait for one another (16 prompts of 4 to 448 queries over 700 to 1500 keys, 20 heads
+        // of 64: 47.4 us, in the order of the sequences 51.3). It costs the plan 1 us, which fewer items
+        // would not win back.
+        order[tid] = tid;
+        if (many) {
+            if (tid < 32) in_class[tid] = 0;
+            __syncthreads();
+            const int cls = rows0 > 0 ? 31 - (int)(31.f * (float)blocks0 / (float)s_most) : 31;
+            const uint32_t peers = __match_any_sync(0xffffffffu, cls);
+            int at = 0;
+            if (lane == __ffs(peers) - 1) at = atomicAdd(&in_class[cls], __popc(peers));
+            at = __shfl_sync(0xffffffffu, at, __ffs(peers) - 1) + __popc(peers & ((1u << lane) - 1));
+            __syncthreads();
+            if (warp == 0) {
+                int c = in_class[lane], sum = c;
+#pragma unroll 1
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int below = __shfl_up_sync(0xffffffffu, sum, o);
+                    if (lane >= o) sum += below;
+                }
+                in_class[lane] = sum - c;
+            }
+            __syncthreads();
+            at += in_class[cls];
+            order[at] = tid;
+            items_end[at] = rows0;
+            slots_end[at] = blocks0;
+            __syncthreads();
+            rows0 = items_end[tid];
+            blocks0 = slots_end[tid];
+        }
         const int pieces = rows0 <= kCrossSplitRows ? max(1, min(most, blocks0 / kCrossMinBlocks)) : 1;
         const int n = cdiv(rows0, a.prefill_rows) * a.num_kv_heads * pieces;
         const int slots = pieces > 1 ? cdiv(rows0, kCrossSlotRows) * a.num_kv_heads * pieces : 0;
         long long total;
         const long long before = block_exclusive_scan(((long long)slots << 32) | n, scan, &total);
+        // (the scan's barriers lie between the reads above and these writes)
         items_end[tid] = (int)(before & 0xffffffffll) + n;
         slots_end[tid] = (int)(before >> 32) + slots;
         __syncthreads();
         const int total_n = (int)(total & 0xffffffffll);
         for (int i = tid; i < total_n && base + i < a.max_pre_items; i += blockDim.x) {
-            int lo = 0, hi = min((int)blockDim.x, num - s0) - 1;  // the first sequence whose end exceeds i
+            int lo = 0, hi = (many ? (int)blockDim.x : min((int)blockDim.x, num - s0)) - 1;  // the first end beyond i
             while (lo < hi) {
                 const int mid = (lo + hi) >> 1;
                 if (items_end[mid] > i) hi = mid; else lo = mid + 1;
@@ -481,7 +524,7 @@ __global__ void __launch_bounds__(1024) rpa_cross_tc_plan_kernel(RpaArgs a, int 
             const int rel = i - (lo ? items_end[lo - 1] : 0);
             const int slot0 = lo ? slots_end[lo - 1] : 0;
             WorkItem w;
-            w.seq = s0 + lo;
+            w.seq = s0 + order[lo];
             w.key_begin = a.cu_q_lens[w.seq];
             w.key_end = a.kv_lens[w.seq];
             w.first_item = (a.cu_q_lens[w.seq + 1] - w.key_begin) * G;

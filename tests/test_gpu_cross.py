@@ -100,6 +100,16 @@ def test_many_sequences(d, dtype):
     check(batch(q_lens, kv_lens, 4, 2, d, 16, dtype=dtype, seed=6), TOL_BF16 if dtype == BF16 else TOL_FP8)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_sequences_of_many_lengths_in_any_order(d):
+    # more items than CTAs, in an order by length across more sequences than the plan's block has threads
+    rng = np.random.default_rng(8)
+    kv_lens = (rng.integers(0, 10, 1300) ** 3 * (rng.random(1300) < 0.9)).astype(int).tolist()
+    q_lens = rng.integers(0, 4, 1300)
+    q_lens[[7, 700, 1299]] = 300, 41, 33
+    check(batch(q_lens.tolist(), kv_lens, 4, 2, d, 16, seed=9), TOL_BF16)
+
+
 @pytest.mark.parametrize("hq,hkv,d", [(8, 2, 64), (8, 2, 128), (32, 1, 128), (3, 3, 64)])
 @pytest.mark.parametrize("q_lens,kv_lens", [([1], [513]), ([1, 2], [5000, 511]), ([8, 1, 0], [3000, 1, 9]), ([2, 9], [4097, 2048])])
 def test_sequences_cut_along_their_keys(hq, hkv, d, q_lens, kv_lens):
