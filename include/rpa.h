@@ -336,10 +336,10 @@ RPA_API int rpa_rope_update_kv_cache(const rpa_params* p, const rope_table* t, c
                                      size_t workspace_bytes, rpa_stream_t stream);
 
 /* rpa_rope_update_kv_cache, then rpa_forward of the turned queries over the updated cache, in one
- * call (`out` equals the two calls' up to rounding: the keys of a decode may be split elsewhere).  `q_rot` is rpa_rope_update_kv_cache's q_out (not NULL; the caller's, holding the turned
- * queries afterwards), `out` and `workspace` are rpa_forward's; the workspace's error word also
- * records the cache write's metadata errors.  `out` must not alias q, q_rot, kv_pages, new_k or
- * new_v. */
+ * call (`out` equals the two calls' up to rounding: the keys of a decode may be split elsewhere).
+ * `q_rot` is rpa_rope_update_kv_cache's q_out (not NULL; the caller's, holding the turned queries
+ * afterwards), `out` and `workspace` are rpa_forward's; the workspace's error word also records the
+ * cache write's metadata errors.  `out` must not alias q, q_rot, kv_pages, new_k or new_v. */
 RPA_API int rpa_rope_forward_update(const rpa_params* p, const rope_table* t, const rope_strides* strides, const void* q,
                                     const void* new_k, const void* new_v, void* kv_pages, const int32_t* kv_lens,
                                     const int32_t* page_indices, const int32_t* cu_q_lens, const int32_t* num_seqs,

@@ -1,5 +1,5 @@
-// Prefill-class work of cross attention (sequences with more than one 16-row tile of query rows, every
-// key visible) on the 5th-generation tensor cores of sm_103a, for bf16 caches.
+// Cross attention (every key visible) on the 5th-generation tensor cores of sm_103a, for bf16 caches: every
+// sequence of the batch, from one row of queries on.
 //
 //   S = Q K^T, P = 2^(c S - m), O += P V, l += sum P, out = O / l, with m a row's running maximum of
 //   c S, c = sm_scale log2(e).
@@ -11,8 +11,8 @@
 // So two tiles of 128 rows are in flight on every SM, each with warps of its own: while one tile's
 // softmax runs, the tensor pipe works for the other. With a row's 128 scores in one thread no maximum
 // is exchanged between warps (two warps a row quarter, half a row a thread: 745 us against 676 for 4 x
-// 4096 queries over 4096 keys, 32/8 heads of 128). The causal kernel keeps one tile in flight, its rows
-// split over two warps: 839 us. The two tiles are
+// 4096 queries over 4096 keys, 32/8 heads of 128, which is 1626 TFLOP/s). The causal kernel keeps one tile
+// in flight, its rows split over two warps: 839 us. The two tiles are
 //   TILES = 2 (D = 128): 256 rows of one KV head in one CTA, which share the K/V stream;
 //   TILES = 1 (D = 64): two CTAs an SM with a tile each, whose softmaxes drift apart by themselves
 //              (8 x 4864 queries over 1536 keys, 20 heads: 323 us; with TILES = 2: 351 us).
@@ -26,9 +26,14 @@
 // is still at work, as soon as its scores are in registers. At D = 128 that would be 640 columns of 512:
 // the two tiles take turns with one S, which holds a block's scores for the QK and the load only.
 // (P over S instead, with the next QK behind PV: 1.29 us a block against 0.97 in the causal kernel.)
-// Barriers, all waits bounded: k/v_full, k/v_empty (rings), q_full, q_empty, item_full/empty as in the
-// causal kernel; per tile s_full (QK done), s_free (scores loaded), p_full (P written, O
-// rescaled), pv_done (PV read P and updated O), o_empty (the epilogue has read O).
+// Batches of few rows: a tile of one row costs what a full one does, 0.93 us a block and SM at D = 64, about
+// what HBM takes for the block's keys and values (64 decodes over 1450 keys, 20 heads: 90 us, 70 at the copy
+// rate). Warps without rows that skip their exponentials do not change that (92.2 us both ways) and slow the
+// long case, whose loop they change, from 700 to 731 us.
+// Barriers, all waits bounded: k/v_full, k/v_empty (rings), q_full, q_empty (Q loaded, its last QK done),
+// item_full/empty (two items' numbers, handed on by the K warp); per tile s_full (QK done), s_free (scores
+// loaded), p_full (P written, O rescaled), pv_done (PV read P and updated O), o_empty (the epilogue has
+// read O).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
