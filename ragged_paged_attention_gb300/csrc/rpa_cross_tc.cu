@@ -88,6 +88,13 @@ __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.a
 template <int R>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
+// 32 bytes of eight registers in one store (p 32-byte aligned): whole sectors, half the instructions.
+__device__ __forceinline__ void st_global_32b(void* p, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 template <int D, int TILES>
 __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>::kCtas)
     rpa_cross_tc_kernel(const __grid_constant__ RpaArgs a, const __grid_constant__ CUtensorMap tm_kv,
@@ -325,6 +332,9 @@ __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>
                     if (!ok) s_abort = 1;
                     continue;
                 }
+                // rows of 32-byte units where `out` allows them (64 sequences of 64 queries and keys, 32/8 heads of
+                // 128: 30 us, in 16-byte stores 33; the long case 712 and 727)
+                const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
                 const float inv = l > 0.f ? 1.f / l : 0.f;
                 __nv_bfloat16* dst = a.out + ((size_t)(it.q_start + (rv ? R / G : 0)) * a.num_q_heads + it.head * G +
                                               (rv ? R % G : 0)) * D;
@@ -336,9 +346,14 @@ __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>
                         uint32_t pk[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) pk[i] = pack_bf16(o[2 * i] * inv, o[2 * i + 1] * inv);
-                        uint4* d4 = reinterpret_cast<uint4*>(dst + c * 32);
+                        if (wide) {
+                            st_global_32b(dst + c * 32, pk);
+                            st_global_32b(dst + c * 32 + 16, pk + 8);
+                        } else {
+                            uint4* d4 = reinterpret_cast<uint4*>(dst + c * 32);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) d4[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+                            for (int i = 0; i < 4; ++i) d4[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+                        }
                     }
                 }
                 tc_fence_before();

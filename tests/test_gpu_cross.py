@@ -117,6 +117,21 @@ def test_sequences_cut_along_their_keys(hq, hkv, d, q_lens, kv_lens):
     check(batch(q_lens, kv_lens, hq, hkv, d, 32, seed=hq + d), TOL_BF16)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_output_at_any_16_byte_address(d):
+    b = batch([300, 1, 40], [500, 700, 130], 8, 2, d, 16, seed=12)
+    g, ref, n = b.to("cuda"), reference(b), b.num_tokens
+    got = []
+    for shift in (0, 8, 16):  # elements: 16 and 32 bytes
+        room = torch.full((g.q.numel() + 24,), 7.0, dtype=BF16, device="cuda")
+        out = room[shift:shift + g.q.numel()].view(g.q.shape)
+        api.rpa_cross_forward(g.q, g.kv_pages, g.kv_lens, g.page_indices, g.cu_q_lens, g.num_seqs, sm_scale=b.sm_scale, out=out)
+        assert (out[:n].cpu().double() - ref[:n]).abs().max().item() <= TOL_BF16
+        assert (room[:shift] == 7.0).all() and (room[shift + n * 8 * d:] == 7.0).all()
+        got.append(out[:n].clone())
+    assert torch.equal(got[0], got[1]) and torch.equal(got[0], got[2])
+
+
 def test_no_sequences_and_one_stream_of_nothing():
     b = batch([2, 40], [30, 50], 8, 2, 128, 16, seed=1)
     b.num_seqs[0] = 0
