@@ -407,10 +407,12 @@ __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>
                                     }
                                     umma_commit(&s_full[t]);
                                     umma_commit(&k_empty[slot]);
+                                    if (j + 1 == it.blocks) umma_commit(q_empty);
                                     ++n_own;
                                 } else {
                                     if (!ok) break;
                                     mbar_arrive(&k_empty[slot]);
+                                    if (j + 1 == it.blocks) mbar_arrive(q_empty);
                                 }
                                 if (t == 0 && both) ++n_other;
                             }
@@ -437,12 +439,7 @@ __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>
                                 }
                             }
                         }
-                        if (active) {
-                            umma_commit(q_empty);
-                            ++no;
-                        } else {
-                            mbar_arrive(q_empty);
-                        }
+                        if (active) ++no;
                         if (!ok) s_abort = 1;
                     }
                     ok = __all_sync(0xffffffffu, ok);  // (the other lanes' stays true)
