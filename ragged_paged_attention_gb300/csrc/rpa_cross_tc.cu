@@ -30,10 +30,10 @@
 // what HBM takes for the block's keys and values (64 decodes over 1450 keys, 20 heads: 90 us, 70 at the copy
 // rate). Warps without rows that skip their exponentials do not change that (92.2 us both ways) and slow the
 // long case, whose loop they change, from 700 to 731 us.
-// Barriers, all waits bounded: k/v_full, k/v_empty (rings), q_full, q_empty (Q loaded, its last QK done),
-// item_full/empty (two items' numbers, handed on by the K warp); per tile s_full (QK done), s_free (scores
-// loaded), p_full (P written, O rescaled), pv_done (PV read P and updated O), o_empty (the epilogue has
-// read O).
+// Barriers, all waits bounded: k/v_full, k/v_empty (rings), q_full, q_empty (Q loaded; its last QK done and,
+// where the tiles share S, the scores loaded), item_full/empty (two items' numbers, handed on by the K
+// warp); per tile s_full (QK done), s_free (scores loaded), p_full (P written, O rescaled), pv_done (PV read
+// P and updated O), o_empty (the epilogue has read O).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>
                                     }
                                     umma_commit(&s_full[t]);
                                     umma_commit(&k_empty[slot]);
-                                    if (j + 1 == it.blocks) umma_commit(q_empty);
+                                    if (!T::ONE_S && j + 1 == it.blocks) umma_commit(q_empty);
                                     ++n_own;
                                 } else {
                                     if (!ok) break;
@@ -415,6 +415,14 @@ __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>
                                     if (j + 1 == it.blocks) mbar_arrive(q_empty);
                                 }
                                 if (t == 0 && both) ++n_other;
+                            }
+                            if (T::ONE_S && active && j == it.blocks) {
+                                // With S shared, Q is free once the last scores have been loaded too: the issuer
+                                // that has no tile of this item follows none of the loads, and its wait for the
+                                // next item's would pass at an older phase.
+                                ok = mbar_wait(&s_free[t], (n_own - 1) & 1, err);
+                                if (!ok) break;
+                                mbar_arrive(q_empty);
                             }
                             if (j > 0) {  // PV of block j - 1
                                 const uint32_t slot = jv % NV;

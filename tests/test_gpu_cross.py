@@ -110,6 +110,14 @@ def test_sequences_of_many_lengths_in_any_order(d):
     check(batch(q_lens.tolist(), kv_lens, 4, 2, d, 16, seed=9), TOL_BF16)
 
 
+def test_items_of_one_tile_between_items_of_two():
+    # one CTA takes both kinds in turn; short items, so that one's end meets the next one's start
+    q_lens = [64, 20, 33, 64, 7, 90] * 60
+    kv_lens = [128, 100, 256, 30, 129, 64] * 60
+    for _ in range(3):
+        check(batch(q_lens, kv_lens, 16, 4, 128, 16, seed=14), TOL_BF16)
+
+
 @pytest.mark.parametrize("hq,hkv,d", [(8, 2, 64), (8, 2, 128), (32, 1, 128), (3, 3, 64)])
 @pytest.mark.parametrize("q_lens,kv_lens", [([1], [513]), ([1, 2], [5000, 511]), ([8, 1, 0], [3000, 1, 9]), ([2, 9], [4097, 2048])])
 def test_sequences_cut_along_their_keys(hq, hkv, d, q_lens, kv_lens):
