@@ -339,6 +339,83 @@ def test_step_reports_bad_metadata_and_refuses():
             api.rpa_rope_forward_update(g.q, k, v, g.kv_pages, *meta, t, **kw)
 
 
+def test_all_attention_calls_share_a_workspace():
+    # causal, cross and step take turns on one workspace, nothing waits between them
+    b = batch([1] * 20 + [90, 7], [1500] * 21 + [600], 8, 2, 128, 16, seed=31)
+    e = batch([3, 200, 1], [70, 900, 5000], 8, 2, 128, 16, seed=32)
+    k, v = step_inputs(b, 5)
+    g, ge, k, v = b.to("cuda"), e.to("cuda"), k.cuda(), v.cuda()
+    t, size = api.make_rope_table(128), 1 << 27
+    meta = lambda x: (x.kv_lens, x.page_indices, x.cu_q_lens, x.num_seqs)  # noqa: E731
+    calls = [lambda out, ws: api.rpa_forward(g.q, g.kv_pages, *meta(g), sm_scale=b.sm_scale, out=out, workspace=ws),
+             lambda out, ws: api.rpa_cross_forward(ge.q, ge.kv_pages, *meta(ge), sm_scale=e.sm_scale, out=out, workspace=ws),
+             lambda out, ws: api.rpa_rope_forward_update(g.q, k, v, g.kv_pages, *meta(g), t, sm_scale=b.sm_scale, out=out, workspace=ws),
+             lambda out, ws: api.rpa_cross_forward(g.q, g.kv_pages, *meta(g), sm_scale=b.sm_scale, out=out, workspace=ws)]
+    qs = [g.q, ge.q, g.q, g.q]
+    fresh = lambda: torch.zeros(size, dtype=torch.uint8, device="cuda")  # noqa: E731
+    calls[2](torch.empty_like(g.q), fresh())  # (the step's rows are written: the cache stays as it is from here on)
+    torch.cuda.synchronize()
+    want = []
+    for call, q in zip(calls, qs):
+        want.append(call(torch.full_like(q, 7.0), fresh()))
+        torch.cuda.synchronize()
+    ws, outs = fresh(), [[torch.full_like(q, 7.0) for q in qs] for _ in range(8)]
+    torch.cuda.synchronize()
+    for i, turn in enumerate(outs):
+        for j in range(4):
+            c = (i + j * (1 + 2 * (i % 2))) % 4
+            calls[c](turn[c], ws)
+    assert api.check_device_status(ws) == 0
+    for turn in outs:
+        for out, ref in zip(turn, want):
+            assert torch.equal(out.view(torch.int16), ref.view(torch.int16))
+
+
+@pytest.mark.parametrize("d,dtype,scale", [(64, BF16, None), (128, BF16, None), (128, FP8, 0.5)], ids=str)
+def test_replays_follow_what_the_tensors_hold(d, dtype, scale):
+    """Captured once, replayed on other batches written into the same tensors; two graphs in turn."""
+    hq, hkv, ps, tokens, seqs, pages = 8, 2, 16, 160, 8, 400
+    rng = np.random.default_rng(7)
+    cuda = lambda *shape, **kw: torch.zeros(*shape, device="cuda", **kw)  # noqa: E731
+    i32 = torch.int32
+    q, k, v = (cuda(tokens, h, d, dtype=BF16) for h in (hq, hkv, hkv))
+    kv = torch.from_numpy(rng.standard_normal((pages, ps, 2 * hkv, d), dtype=np.float32)).to(dtype).cuda()
+    lens, cu, num = cuda(seqs, dtype=i32), cuda(seqs + 1, dtype=i32), cuda(1, dtype=i32)
+    tbl = torch.from_numpy(rng.permutation(pages)[:seqs * (pages // seqs)].reshape(seqs, -1).astype(np.int32)).cuda().contiguous()
+    meta, t = (lens, tbl, cu, num), api.make_rope_table(d)
+    outs = [torch.full_like(q, 7.0) for _ in range(2)]
+    run = [lambda out: api.rpa_cross_forward(q, kv, *meta, sm_scale=0.1, k_scale=scale, v_scale=scale, out=out),
+           lambda out: api.rpa_rope_forward_update(q, k, v, kv, *meta, t, sm_scale=0.1, k_scale=scale, v_scale=scale, out=out)]
+    graphs = []
+    for f, out in zip(run, outs):
+        f(out)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            f(out)
+    batches = [([1] * 8, [700, 3, 90, 512, 1, 33, 600, 799]), ([150, 1], [400, 20]), ([], []), ([2, 0, 40, 60], [300, 50, 41, 60])]
+    for q_lens, kv_lens in batches * 2:
+        n = len(q_lens)
+        for x in (q, k, v):
+            x.copy_(torch.from_numpy(rng.standard_normal(tuple(x.shape), dtype=np.float32)).to(BF16))
+        lens[:n] = torch.tensor(kv_lens, dtype=i32)
+        cu[:n + 1] = torch.tensor([0] + list(np.cumsum(q_lens)), dtype=i32)
+        num[0] = n
+        for out in outs:
+            out.fill_(7.0)
+        for g in graphs[::-1]:  # (the step writes its rows first)
+            g.replay()
+        for out, f in zip(outs, run):
+            want = torch.full_like(q, 7.0)
+            f(want)
+            assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+        m = sum(q_lens)
+        ref = plain.attend_all(q.cpu(), kv.cpu(), lens.cpu(), tbl.cpu(), cu.cpu(), n, sm_scale=0.1, k_scale=scale, v_scale=scale)
+        tol = TOL_BF16 if dtype == BF16 else TOL_FP8
+        assert m == 0 or (outs[0][:m].cpu().double() - ref[:m]).abs().max().item() <= tol
+        assert (outs[0][m:].float() == 7.0).all() and (outs[1][m:].float() == 7.0).all()
+
+
 # ------------------------------------------------------------------ together
 @pytest.mark.parametrize("graph", [False, True], ids=["eager", "graph"])
 def test_decoder_layer(graph):
