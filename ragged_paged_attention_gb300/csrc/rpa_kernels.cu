@@ -122,13 +122,14 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
     }
     __syncthreads();
     // SMs for the prefill kernel beside decode: the n minimising max(prefill time on n SMs,
-    // decode time on the rest), one candidate n = tid + 1 per thread
+    // decode time on the rest), one candidate n = tid + 1 per thread (a batch of one class has none)
     const int S = a.num_sms;
-    {
+    const bool both = a.overlap && s_pf > 0.f && s_db > 0.f;
+    if (both) {
         const float pre_flops = s_pf, dec_bytes = s_db;
         float tt = INFINITY;
         int nn = S;
-        if (a.overlap && pre_flops > 0.f && dec_bytes > 0.f && tid + 1 < S) {
+        if (tid + 1 < S) {
             nn = tid + 1;
             const float tp = pre_flops / (a.pre_flops_per_ns_sm * (float)nn);
             const float td = dec_bytes / fminf(kDecHbmBytesPerNs, a.dec_bytes_per_ns_sm * (float)(S - nn));
@@ -146,11 +147,11 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
             best_t[tid >> 5] = tt;
             best_n[tid >> 5] = nn;
         }
+        __syncthreads();
     }
-    __syncthreads();
     float bt = INFINITY;
     int bn = S;
-    if (tid < 32) {  // the best of the warps' candidates, by warp 0
+    if (both && tid < 32) {  // the best of the warps' candidates, by warp 0
         if (tid < (int)(blockDim.x >> 5)) {
             bt = best_t[tid];
             bn = best_n[tid];
@@ -192,8 +193,11 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
         const long long ls = (long long)r * q1;
         // pooled shares: about kPoolPerCta per CTA, at least kMinPoolChunk keys, within the bound
         const long long rest = W - ls;
-        long long q2 = div_nn(rest, (long long)kPoolPerCta * ctas);
-        q2 = max(q2, div_nn(rest + (kMaxDecodeCtas - r) - 1, kMaxDecodeCtas - r));
+        long long q2 = 0;
+        if (rest > kMinPoolChunk) {
+            q2 = div_nn(rest, (long long)kPoolPerCta * ctas);
+            q2 = max(q2, div_nn(rest + (kMaxDecodeCtas - r) - 1, kMaxDecodeCtas - r));
+        }
         q2 = max((long long)kMinPoolChunk, (q2 + kDecodeBK - 1) / kDecodeBK * kDecodeBK);
         // (every share longer than a group's cost holds at least one key)
         q2 = max(q2, (long long)(a.item_cost_keys + kDecodeBK));
@@ -203,13 +207,23 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
         s_r = r;
         hdr->chunk_keys = (int)min(q1, (long long)0x7fffffff);
         hdr->dec_ctas = r;
-        hdr->dec_shares = r + (int)div_nn(rest + q2 - 1, q2);
+        hdr->dec_shares = r + (rest <= q2 ? rest > 0 : (int)div_nn(rest + q2 - 1, q2));
     }
     __syncthreads();
     const long long q1 = s_q1, q2 = s_q2, ls = s_ls;
     const int n_static = s_r;
-    // share holding line position p, and where share c starts
-    auto share_of = [&](long long p) { return p < ls ? div_nn(p, q1) : n_static + div_nn(p - ls, q2); };
+    // share holding line position p, and where share c starts.  (There are at most kMaxDecodeCtas shares of
+    // either size, so the quotient's float32 estimate is off by one at most.  With integer divisions, of
+    // which every item takes several, and the split's search for batches of one class too, the plan took
+    // 13.5 us instead of 12.3 for 130 sequences and 12.1 instead of 10.3 for 7.)
+    const float inv1 = 1.f / (float)q1, inv2 = 1.f / (float)q2;
+    auto share_of = [&](long long p) {
+        const bool in_static = p < ls;
+        const long long off = in_static ? p : p - ls, q = in_static ? q1 : q2;
+        const int c = (int)((float)off * (in_static ? inv1 : inv2));
+        const long long left = off - c * q;
+        return (long long)((in_static ? 0 : n_static) + c + (left >= q) - (left < 0));
+    };
     auto share_start = [&](long long c) { return c < n_static ? c * q1 : ls + (c - n_static) * q2; };
     // pass 2: item counts, scan, emit
     int dec_base = 0, pre_base = 0;
