@@ -133,7 +133,31 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rpa_rope_updat
     // an rpa_forward plan kernel behind may start now: it reads only metadata this kernel does
     // not write, and it ends after this grid has
     pdl_launch_dependents();
+    __shared__ int cu[kRopeCu];
     auto resolve = [&](int t0, int nt) {
+        if (a.max_num_seqs < kRopeCu) {
+            // all of cu_q_lens in one round trip, then a token a thread: two more for all of them (a warp a
+            // token took four or five, again for every eight tokens: 4 x 4096 tokens 74.0 us, now 70.5)
+            for (int i = threadIdx.x; i <= a.max_num_seqs; i += kRopeThreads) cu[i] = a.cu_q_lens[i];
+            const int num = a.num_seqs[0];
+            const bool some = num > 0 && num <= a.max_num_seqs;
+            if (!some && num != 0 && t0 == 0 && threadIdx.x == 0) set_error(a.err, RPA_DEV_ERR_NUM_SEQS);
+            __syncthreads();
+            if (threadIdx.x < nt) {
+                const int t = t0 + threadIdx.x;
+                int pos = 0;
+                uint8_t* slot = nullptr;
+                if (some && cu[0] <= t) {
+                    const int s = seq_of_token(cu, num, t);
+                    const uint32_t bad = rope_slot_of(a, t, s, cu[s], cu[s + 1], cu[num], pos, slot);
+                    if (bad) set_error(a.err, bad);
+                }
+                if (a.positions) pos = a.positions[t];
+                sh.pos[threadIdx.x] = pos;
+                sh.slot[threadIdx.x] = slot;
+            }
+            return;
+        }
         for (int k = threadIdx.x >> 5; k < nt; k += kRopeWarps) {  // a warp a token
             int pos = 0;
             uint8_t* slot = nullptr;
@@ -219,23 +243,37 @@ constexpr int kRopePasses = 5, kRopeBlocks = 16;
 // or one.
 static int rope_vec(const RopeTab& t) { return t.rotary_dim % 16 == 0 ? 8 : t.rotary_dim % 4 == 0 ? 2 : 1; }
 
-// The shares of one kind, whose rows are some of all `total` head rows of a token.  A block finds its
-// tokens' slots and sines before it can store, some 2 us, so it wants several passes over its threads
-// (kRopePasses); more than kRopeBlocks blocks an SM only repeat that; and a small call is spread over
-// every SM twice, by tokens and then by heads.
-static RopeShare rope_share(const RopeTab& tab, int tokens, int heads, int total, int head_dim, int num_sms) {
+// The shares of one kind, `share` head rows each or fewer.
+static RopeShare rope_share(const RopeTab& tab, int tokens, int heads, int head_dim, double share) {
     const int rows = kRopeThreads / (head_dim / 16);  // head rows a block holds at once
     const int most = min(kRopeTokens, tab.rotary_dim ? kRopePairs / (tab.rotary_dim / 2) : kRopeTokens);
     RopeShare s = {1, heads, 1, 0};
     if (heads == 0) return s;
-    const double all = (double)tokens * total;
-    const double share = min(max(kRopePasses * (double)rows, all / (kRopeBlocks * num_sms)), all / (2 * num_sms));
     s.tokens = max(1, min(most, (int)min(share / heads, 1e6)));
     s.parts = max(1, min(cdiv(heads, rows), (int)(heads / max(share, 1.0))));
     s.heads = cdiv(heads, s.parts);
     s.parts = cdiv(heads, s.heads);
     s.blocks = (unsigned)(((long long)tokens + s.tokens - 1) / s.tokens * s.parts);
     return s;
+}
+
+// Shares of both kinds: a's of ha heads, b's of hb, nb times.  A block finds its tokens' slots and sines
+// before it can store, some 2 us, so it wants several passes over its threads (kRopePasses); more than
+// kRopeBlocks blocks an SM only repeat that; and a small call is spread over every SM twice, by tokens and
+// then by heads.
+static void rope_shares(const RopeTab& tab, int tokens, int ha, int hb, int nb, int head_dim, int num_sms, RopeShare& a, RopeShare& b) {
+    const double all = (double)tokens * (ha + nb * hb), passes = kRopePasses * (double)(kRopeThreads / (head_dim / 16));
+    double share = min(max(passes, all / (kRopeBlocks * num_sms)), all / (2 * num_sms));
+    // what the SMs hold at once and up to half as many again goes as one round of longer shares (61 decodes and
+    // 2 x 1021 tokens of 32 heads of 256, 1.4 rounds: 15.9 us, in two 17.7; more rounds are best left as they
+    // come: 8191 tokens of 40 heads, 3.4 rounds: 28.8 us, in three 29.2)
+    const int at_once = kRopeBlocksPerSm * num_sms;
+    for (int i = 0; i < 40; ++i, share *= 1.03) {
+        a = rope_share(tab, tokens, ha, head_dim, share);
+        b = rope_share(tab, tokens, hb, head_dim, share);
+        const double blocks = a.blocks + (double)nb * b.blocks;
+        if (blocks <= at_once || blocks > 1.5 * at_once) break;
+    }
 }
 
 // Blocks of kRopeWarps warps.
@@ -245,9 +283,7 @@ cudaError_t launch_rope_apply(RopeApplyArgs& a, int num_sms, cudaStream_t stream
     ProfScope ps("rope_apply", stream);
     const int vec = rope_vec(a.tab);
     if (vec == 8) {
-        const int heads = a.num_q_heads + a.num_k_heads;
-        a.q_share = rope_share(a.tab, a.num_tokens, a.num_q_heads, heads, a.head_dim, num_sms);
-        a.k_share = rope_share(a.tab, a.num_tokens, a.num_k_heads, heads, a.head_dim, num_sms);
+        rope_shares(a.tab, a.num_tokens, a.num_q_heads, a.num_k_heads, 1, a.head_dim, num_sms, a.q_share, a.k_share);
         const unsigned grid = a.q_share.blocks + a.k_share.blocks;
         if (a.tab.interleaved)
             rope_apply_kernel<true><<<grid, kRopeThreads, 0, stream>>>(a);
@@ -265,9 +301,7 @@ template <int KV>
 static cudaError_t launch_update_kv(RopeUpdateArgs& a, int num_sms, cudaStream_t stream) {
     const int vec = rope_vec(a.tab);
     if (vec == 8) {
-        const int heads = a.num_q_heads + 2 * a.num_kv_heads;
-        a.q_share = rope_share(a.tab, a.max_num_tokens, a.num_q_heads, heads, a.head_dim, num_sms);
-        a.kv_share = rope_share(a.tab, a.max_num_tokens, a.num_kv_heads, heads, a.head_dim, num_sms);
+        rope_shares(a.tab, a.max_num_tokens, a.num_q_heads, a.num_kv_heads, 2, a.head_dim, num_sms, a.q_share, a.kv_share);
         const unsigned grid = a.q_share.blocks + 2 * a.kv_share.blocks;
         if (a.tab.interleaved)
             rpa_rope_update_kernel<true, KV><<<grid, kRopeThreads, 0, stream>>>(a);

@@ -134,10 +134,26 @@ __device__ __forceinline__ void rope_store_kv(uint8_t* row, int at, const float*
     }
 }
 
-// The cache rows of token t's slot, found by the whole warp: its sequence, checked as the plan checks it.  False
-// where the token is padding or its metadata is bad (the error word then says so).  The sequence is
-// found 32 entries of cu_q_lens at a time; the first 32, the count and the checks' values are each
-// one round trip for a batch of up to 31 sequences.
+// The cache rows of token t's slot in sequence s, which has the queries [c0, c1) of `end`: the error bits
+// that its metadata sets, checked as the plan checks it, and `slot` NULL then or where t is padding.
+__device__ __forceinline__ uint32_t rope_slot_of(const RopeUpdateArgs& a, int t, int s, int c0, int c1, int end, int& pos,
+                                                 uint8_t*& slot) {
+    slot = nullptr;
+    const int kl = a.kv_lens[s];
+    if (t >= end) return 0;  // padding
+    if (c0 < 0 || t < c0 || t >= c1 || c1 > a.max_num_tokens) return RPA_DEV_ERR_TOKENS;
+    if (c1 - c0 > kl) return RPA_DEV_ERR_Q_LEN;
+    if ((kl - 1) / a.page_size >= a.pages_per_seq) return RPA_DEV_ERR_KV_LEN;
+    pos = kl - (c1 - t);
+    const int page = a.page_indices[(size_t)s * a.pages_per_seq + pos / a.page_size];
+    if ((unsigned)page >= (unsigned)a.total_num_pages) return RPA_DEV_ERR_PAGE;
+    slot = static_cast<uint8_t*>(a.kv_pages) + ((size_t)page * a.page_size + pos % a.page_size) * 2 * a.num_kv_heads * a.row_bytes;
+    return 0;
+}
+
+// The cache rows of token t's slot, found by the whole warp.  False where the token is padding or its
+// metadata is bad (the error word then says so).  The sequence is found 32 entries of cu_q_lens at a time;
+// the first 32, the count and the checks' values are each one round trip for a batch of up to 31 sequences.
 __device__ __forceinline__ bool rope_slot(const RopeUpdateArgs& a, int t, int& pos, uint8_t*& slot) {
     const int lane = threadIdx.x & 31;
     const int first = a.cu_q_lens[min(lane, a.max_num_seqs)];  // (max_num_seqs + 1 entries, whatever num_seqs)
@@ -155,27 +171,9 @@ __device__ __forceinline__ bool rope_slot(const RopeUpdateArgs& a, int t, int& p
         s += (upto - 1) * stride;
         left = min(stride, left - (upto - 1) * stride);
     }
-    const int c0 = a.cu_q_lens[s], c1 = a.cu_q_lens[s + 1], kl = a.kv_lens[s], end = a.cu_q_lens[num];
-    if (t >= end) return false;  // padding
-    uint32_t bad = 0;
-    if (c0 < 0 || t < c0 || t >= c1 || c1 > a.max_num_tokens)
-        bad = RPA_DEV_ERR_TOKENS;
-    else if (c1 - c0 > kl)
-        bad = RPA_DEV_ERR_Q_LEN;
-    else if ((kl - 1) / a.page_size >= a.pages_per_seq)
-        bad = RPA_DEV_ERR_KV_LEN;
-    int page = 0;
-    if (!bad) {
-        pos = kl - (c1 - t);
-        page = a.page_indices[(size_t)s * a.pages_per_seq + pos / a.page_size];
-        if ((unsigned)page >= (unsigned)a.total_num_pages) bad = RPA_DEV_ERR_PAGE;
-    }
-    if (bad) {
-        if (lane == 0) set_error(a.err, bad);
-        return false;
-    }
-    slot = static_cast<uint8_t*>(a.kv_pages) + ((size_t)page * a.page_size + pos % a.page_size) * 2 * a.num_kv_heads * a.row_bytes;
-    return true;
+    const uint32_t bad = rope_slot_of(a, t, s, a.cu_q_lens[s], a.cu_q_lens[s + 1], a.cu_q_lens[num], pos, slot);
+    if (bad && lane == 0) set_error(a.err, bad);
+    return slot != nullptr;
 }
 
 // ---- a block's walk over head rows: the 16-byte path ----
@@ -198,6 +196,8 @@ struct RopeShared {
     uint8_t* slot[kRopeTokens];
     int pos[kRopeTokens];
 };
+// cu_q_lens of the appending kernel, with the sequences' count behind
+constexpr int kRopeCu = 1024;
 
 // The unit's 16 values turned, two pairs an instruction; cs: its words of RopeShared::cs, `stride`
 // apart.

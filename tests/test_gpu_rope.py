@@ -255,6 +255,22 @@ def test_update_batch_shapes(n, T):
     check_write(b, *write(b, t), f, amp, False)
 
 
+@pytest.mark.parametrize("n", [1022, 1023, 1024, 1100])
+def test_update_of_many_sequences_with_empty_and_bad_ones(n):
+    # either way of finding a token's sequence: lengths 0 to 2, one sequence whose kv_len is past its pages
+    q_lens = [(3 * s + s // 7) % 3 for s in range(n)]
+    b = make_batch(q_lens, [L + (5 * s) % 40 for s, L in enumerate(q_lens)], 4, 2, 64, 16, BF16, seed=n, pad=2)
+    good = {k: v.clone() if isinstance(v, torch.Tensor) else v for k, v in b.items()}
+    bad = next(s for s in range(n // 2, n) if q_lens[s] == 2)
+    b["kv_lens"][bad] = 10**6
+    t, (f, amp) = api.make_rope_table(64), plain.frequencies(64)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    q_out, kv = write(b, t, workspace=ws)
+    assert api.check_device_status(ws) == 0x04
+    first = sum(q_lens[:bad])
+    check_write(good, q_out, kv, f, amp, False, skip=range(first, first + 2))
+
+
 def test_update_of_no_sequences():
     b = make_batch([2, 3], [20, 9], 4, 2, 128, 16, BF16, seed=1)
     b["num"][0] = 0
