@@ -30,10 +30,13 @@ constexpr int kMinChunk = 256;          // smallest split-KV chunk (keys)
 // keys at least, 33.3 with 128, 36.1 with 64 (more to join); batches that fill the SMs are cut longer than
 // either
 constexpr int kStepMinChunk = 128;
-// Cross attention's two-tile kernel: a sequence of up to kCrossSplitRows rows may be cut along its keys
-// into up to kCrossMaxSplits pieces of kCrossMinBlocks 128-key blocks or more, whose results wait in
-// slots of kCrossSlotRows rows
-constexpr int kCrossSplitRows = 32, kCrossMaxSplits = 64, kCrossMinBlocks = 4, kCrossSlotRows = 16;
+// Cross attention's two-tile kernel: a sequence of up to kCrossSplitRows rows (a tile) may be cut along its
+// keys into up to kCrossMaxSplits pieces, whose results wait in slots of kCrossSlotRows rows.  The last
+// piece's CTA joins them alone, so many rows get fewer pieces (kCrossJoinRows rows of partial results a head)
+// of more blocks (kCrossMinBlocks of 128 keys, or one for every 16 rows): 8 x 32 queries of 4 heads each
+// over 1500 keys in two pieces of 6 blocks: 31 us, whole 24; over 8192 keys, one sequence: in 16 pieces 59,
+// in 8 45, whole 74.
+constexpr int kCrossSplitRows = 128, kCrossJoinRows = 1024, kCrossMaxSplits = 64, kCrossMinBlocks = 4, kCrossSlotRows = 16;
 constexpr int kCrossZeroBlocks = 8;      // cross attention: blocks beside the plan for rows without a key
 constexpr int kMaxDecodeCtas = 2048;    // most decode shares (static, one per CTA, and pooled)
 // Pool: the part of the line left after the static shares (here only their rounding

@@ -404,12 +404,12 @@ __global__ void __launch_bounds__(1024) rpa_cross_plan_kernel(RpaArgs a) {
 
 // Cross attention on the kernel with two tiles in flight, which takes every sequence, decode's too: a
 // tile with few rows costs it as many cycles as a full one, but that is still about as fast as HBM gives
-// the keys. When the batch has fewer items than CTAs run at once, its sequences of few rows are cut
-// along their keys, into as many pieces as fill the CTAs, of kCrossMinBlocks blocks at least, as far as
-// the workspace has room for the partial results (slots of 16 rows). Pieces cost: leaving a result and
-// joining takes the softmax warps some 3 us (64 decodes over 1450 keys, 20 heads, which fill the CTAs
-// four times over: 94 us whole, 116 in two pieces each; one decode over 20000 keys, 8 heads of 128: 25 us
-// in pieces, 74 through rpa_forward's launches).
+// the keys. When the batch has fewer items than CTAs run at once, its sequences of up to a tile's rows are
+// cut along their keys, into as many pieces as fill the CTAs, as far as the workspace has room for the
+// partial results (slots of 16 rows) and joining them pays (kCrossSplitRows in kernels.h). Pieces cost:
+// leaving a result and joining takes the softmax warps some 3 us with few rows (64 decodes over 1450 keys,
+// 20 heads, which fill the CTAs four times over: 94 us whole, 116 in two pieces each; one decode over 20000
+// keys, 8 heads of 128: 27 us in pieces, 74 through rpa_forward's launches).
 // (rpa_forward's plan, with decode's equal shares, takes 8 to 10 us, a chain of latencies: this one is kept
 // short, 3 to 4 us.)
 __global__ void __launch_bounds__(1024) rpa_cross_tc_plan_kernel(RpaArgs a, int ctas, int max_slots) {
@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(1024) rpa_cross_tc_plan_kernel(RpaArgs a, int 
             red[warp][1] = v[1];
         }
     }
-    // pieces of a sequence: as many as fill the CTAs, and as every sequence of few rows finds slots for
+    // pieces of a sequence: as many as fill the CTAs, and as every sequence that may be cut finds slots for
     // (a little fewer: the sums are floats)
     if (warp == 0) {
         red[lane][0] = fminf((float)ctas / fmaxf(v[0], 1.f), (float)max_slots / (v[1] * 1.001f + 1.f));
@@ -519,7 +519,9 @@ __global__ void __launch_bounds__(1024) rpa_cross_tc_plan_kernel(RpaArgs a, int 
             rows0 = items_end[tid];
             blocks0 = slots_end[tid];
         }
-        const int pieces = rows0 <= kCrossSplitRows ? max(1, min(most, blocks0 / kCrossMinBlocks)) : 1;
+        int pieces = 1;
+        if (rows0 > 0 && rows0 <= kCrossSplitRows)
+            pieces = max(1, min(min(most, kCrossJoinRows / rows0), blocks0 / max(kCrossMinBlocks, cdiv(rows0, kCrossSlotRows))));
         const int n = cdiv(rows0, a.prefill_rows) * a.num_kv_heads * pieces;
         const int slots = pieces > 1 ? cdiv(rows0, kCrossSlotRows) * a.num_kv_heads * pieces : 0;
         long long total;

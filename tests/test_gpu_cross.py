@@ -110,6 +110,17 @@ def test_sequences_of_many_lengths_in_any_order(d):
     check(batch(q_lens.tolist(), kv_lens, 4, 2, d, 16, seed=9), TOL_BF16)
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(4, 4, 64), (8, 2, 64), (8, 2, 128), (2, 2, 128)])
+@pytest.mark.parametrize("q_lens,kv_lens", [([64], [9000]), ([33, 100], [2500, 5000]), ([128, 17, 1], [4097, 700, 3000]),
+                                            ([32, 130, 31], [6000, 6000, 1030])])
+def test_tiles_cut_along_their_keys(hq, hkv, d, q_lens, kv_lens):
+    # few items of up to a whole tile: more rows, fewer and longer pieces; the same bits every time
+    b = batch(q_lens, kv_lens, hq, hkv, d, 32, seed=hq + d + 1)
+    first = check(b, TOL_BF16)
+    for _ in range(3):
+        assert torch.equal(check(b, TOL_BF16).view(torch.int16), first.view(torch.int16))
+
+
 def test_items_of_one_tile_between_items_of_two():
     # one CTA takes both kinds in turn; short items, so that one's end meets the next one's start
     q_lens = [64, 20, 33, 64, 7, 90] * 60
