@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(1024) rpa_cross_plan_kernel(RpaArgs a) {
 // partial results (slots of 16 rows) and joining them pays (kCrossSplitRows in kernels.h). Pieces cost:
 // leaving a result and joining takes the softmax warps some 3 us with few rows (64 decodes over 1450 keys,
 // 20 heads, which fill the CTAs four times over: 94 us whole, 116 in two pieces each; one decode over 20000
-// keys, 8 heads of 128: 27 us in pieces, 74 through rpa_forward's launches).
+// keys, 8 heads of 128: 25 us in pieces, 74 through rpa_forward's launches).
 // (rpa_forward's plan, with decode's equal shares, takes 8 to 10 us, a chain of latencies: this one is kept
 // short, 3 to 4 us.)
 __global__ void __launch_bounds__(1024) rpa_cross_tc_plan_kernel(RpaArgs a, int ctas, int max_slots) {
