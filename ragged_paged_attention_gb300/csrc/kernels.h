@@ -124,6 +124,7 @@ struct RpaArgs {
     int decode_heads;           // KV heads per decode item (decode_heads_for)
     int num_sms;
     int prefill_rows;           // cross attention's two-tile kernel: rows of an item (128 or 256)
+    int plan_early;             // the plan reads the lengths before the stream's earlier work has ended
     int overlap;                // run prefill beside decode (off while kernels are timed one by one)
     float pre_flops_per_ns_sm;  // prefill kernel rate per SM (this head size and cache type)
     float dec_bytes_per_ns_sm;  // decode kernel rate per SM while SMs, not HBM, limit it

@@ -45,6 +45,7 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
     const int tid = threadIdx.x;
     // the prefill grid behind may become resident now; it waits for this grid's end
     pdl_launch_dependents();
+    if (!a.plan_early) pdl_wait();
     if (tid == 0) {
         int n = a.num_seqs[0];
         if (n < 0 || n > a.max_num_seqs) {
@@ -364,13 +365,14 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
 __global__ void __launch_bounds__(1024) rpa_plan_kernel(RpaArgs a) { plan_body(a); }
 
 // Zero rows of cross attention's sequences without keys (which the plans leave out), by the blocks
-// beside the plan's. They wait for the stream's earlier work first: it may still use `out`.
+// beside the plan's. They wait for the stream's earlier work first: it may still use `out`, or be
+// writing the lengths.
 __device__ __forceinline__ void cross_zero_body(const RpaArgs& a, int block, int nblocks) {
     pdl_launch_dependents();
+    pdl_wait();
     const int num = a.num_seqs[0];
     if (num < 0 || num > a.max_num_seqs) return;  // (the plan records it)
     __shared__ int found[1024], n_found;
-    bool waited = false;
     for (int s0 = 0; s0 < num; s0 += blockDim.x) {
         if (threadIdx.x == 0) n_found = 0;
         __syncthreads();
@@ -381,8 +383,6 @@ __device__ __forceinline__ void cross_zero_body(const RpaArgs& a, int block, int
         }
         __syncthreads();
         const int n = n_found;
-        if (n > 0 && !waited) pdl_wait();
-        waited = waited || n > 0;
         for (int i = 0; i < n; ++i) {
             const int c0 = a.cu_q_lens[found[i]], c1 = a.cu_q_lens[found[i] + 1];
             const size_t row = (size_t)a.num_q_heads * a.head_dim / 8;  // a token's 16-byte chunks
@@ -394,7 +394,9 @@ __device__ __forceinline__ void cross_zero_body(const RpaArgs& a, int block, int
     }
 }
 
-// Cross attention on the launches of rpa_forward.
+// Cross attention on the launches of rpa_forward. (Both cross plans start with a wait for the stream's
+// earlier work: whatever runs there may be writing the lengths, and may have let this grid start before
+// it has. What is left of the early start is the launch itself.)
 __global__ void __launch_bounds__(1024) rpa_cross_plan_kernel(RpaArgs a) {
     if (blockIdx.x == 0)
         plan_body(a);
@@ -422,6 +424,7 @@ __global__ void __launch_bounds__(1024) rpa_cross_tc_plan_kernel(RpaArgs a, int 
     __shared__ int items_end[1024], slots_end[1024], order[1024], s_num, s_most, in_class[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_launch_dependents();
+    pdl_wait();
     if (tid == 0) {
         s_most = 0;
         const int n = a.num_seqs[0];
@@ -564,7 +567,6 @@ __global__ void __launch_bounds__(1024) rpa_cross_tc_plan_kernel(RpaArgs a, int 
         WsHeader* hdr = a.hdr;
         hdr->num_items[1] = min(base, a.max_pre_items);
         hdr->next_item[1] = 0;
-        pdl_wait();  // (as the end of plan_body)
     }
 }
 
