@@ -406,7 +406,6 @@ static int rpa_prepare(const rpa_params* p, const void* q, const void* kv_pages,
     a.decode_heads = decode_heads_for(p->head_dim, p->kv_dtype != RPA_DTYPE_BF16);
     a.num_sms = sms;
     a.overlap = prof_enabled() ? 0 : 1;
-    a.plan_early = 1;
     rpa_rates(p->head_dim, a.kv_byte != 0, a.has_scale != 0,
               rpa_pow2_scale(a.k_scale_or_one) && rpa_pow2_scale(a.v_scale_or_one), &a.pre_flops_per_ns_sm,
               &a.dec_bytes_per_ns_sm);
@@ -702,6 +701,7 @@ int rpa_rope_forward_update(const rpa_params* p, const rope_table* t, const rope
     if (a.batch_kind == RPA_BATCH_MIXED && (long long)p->max_num_tokens * (a.num_q_heads / a.num_kv_heads) <= 16)
         a.batch_kind = RPA_BATCH_DECODE_ONLY;
     a.min_chunk = kStepMinChunk + a.item_cost_keys;
+    a.plan_early = 1;  // (behind the cache write, which writes no lengths and started after all that did)
     cudaError_t e = launch_rope_update(u, sms, reinterpret_cast<cudaStream_t>(stream));
     if (e == cudaSuccess) e = launch_rpa_forward(a, sms, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "rpa_rope_forward_update launch");
@@ -755,7 +755,6 @@ int rpa_cross_forward(const rpa_params* p, const void* q, const void* kv_pages, 
     rc = check_workspace(workspace, workspace_bytes, c.total);
     if (rc) return rc;
     a.causal = 0;
-    a.plan_early = 0;
     if (rpa_cross_tc_takes(a)) {
         a.pre_items = reinterpret_cast<WorkItem*>(static_cast<uint8_t*>(workspace) + c.items);
         a.max_pre_items = c.max_items;

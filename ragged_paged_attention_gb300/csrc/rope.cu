@@ -130,7 +130,7 @@ __device__ __forceinline__ void update_out(const RopeUpdateArgs& a, int t, int h
 template <bool INTER, int KV>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rpa_rope_update_kernel(const __grid_constant__ RopeUpdateArgs a) {
     __shared__ RopeShared sh;
-    // an rpa_forward plan kernel behind may start now: it reads only metadata this kernel does
+    // rpa_rope_forward_update's plan behind may start now: it reads only metadata this kernel does
     // not write, and it ends after this grid has
     pdl_launch_dependents();
     __shared__ int cu[kRopeCu];

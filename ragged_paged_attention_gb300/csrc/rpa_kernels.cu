@@ -45,6 +45,8 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
     const int tid = threadIdx.x;
     // the prefill grid behind may become resident now; it waits for this grid's end
     pdl_launch_dependents();
+    // The stream's earlier work may be writing the lengths, and may have let this grid start before it
+    // has: wait for it, unless it is known not to.
     if (!a.plan_early) pdl_wait();
     if (tid == 0) {
         int n = a.num_seqs[0];
@@ -356,8 +358,8 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
         hdr->next_item[0] = 0;
         hdr->next_item[1] = 0;  // prefill queue
         hdr->next_item[2] = 0;  // pooled decode shares taken
-        // started beside the cache write (programmatic launch): end after it, so that the
-        // attention grids behind see the new rows (no-op on an ordinary launch)
+        // started beside the cache write (plan_early): end after it, so that the attention grids
+        // behind see the new rows (no-op otherwise)
         pdl_wait();
     }
 }
@@ -577,8 +579,7 @@ __device__ __forceinline__ void update_body(const RpaUpdateArgs& a, int block, i
     // cu_q_lens[0..max_num_seqs] then kv_lens[0..max_num_seqs), when they fit (update_cache_ints)
     extern __shared__ int s_cu[];
     __shared__ int s_num;
-    // an rpa_forward plan kernel behind may start now: it reads only metadata this kernel does
-    // not write, and it ends after this grid has
+    // a plan kernel behind may be launched now; it waits for this grid's end
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     const int Hkv = a.num_kv_heads, C = 2 * Hkv;

@@ -50,7 +50,7 @@ def parts(m):
 
 
 @pytest.mark.parametrize("graph", [False, True], ids=["stream", "graph"])
-@pytest.mark.parametrize("call", ["cross"])
+@pytest.mark.parametrize("call", ["cross", "forward", "update", "step"])
 @pytest.mark.parametrize("d,dtype", [(64, BF16), (128, BF16), (256, BF16), (128, FP8)], ids=str)
 def test_lengths_written_just_before_the_call(late_write, call, d, dtype, graph):
     hq, hkv, ps = 8, 2, 16
