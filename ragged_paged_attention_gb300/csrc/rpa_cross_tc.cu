@@ -166,17 +166,19 @@ __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>
     pdl_wait();
 
     uint32_t items = 0;  // items this CTA has taken (ring slots, q phases)
-    // Reads the next item (every warp); false when there is none.
-    auto next_item = [&](CrossItem& it) -> bool {
+    // Reads the next item (every warp, or the one thread that speaks for it); false when there is none.
+    auto next_item_of = [&](CrossItem& it, auto alone) -> bool {
+        constexpr bool kAlone = decltype(alone)::value;
         const uint32_t slot = items & 1, ph = (items >> 1) & 1;
         it.seq = -1;
         if (mbar_wait(&item_full[slot], ph, err)) it = s_items[slot];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&item_empty[slot]);
+        if (!kAlone) __syncwarp();
+        if (kAlone || lane == 0) mbar_arrive(&item_empty[slot]);
         if (it.seq < 0 || s_abort) return false;
         ++items;
         return true;
     };
+    auto next_item = [&](CrossItem& it) { return next_item_of(it, std::false_type()); };
 
     CrossItem it;
     if (warp < T::kSoft) {
@@ -400,9 +402,10 @@ __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>
         regs_dec<T::kRegsRest>();
         if (warp >= kMma0 && warp < kMma0 + TILES) {
             // ---------------- MMA issuer of tile t (a constant in either branch) ----------------
-            // The issuing lane is an elected one: under a test for lane 0 the compiler does not know that
-            // one lane issues, and an MMA took some 80 cycles to issue (long queries at D = 128: 868 us
-            // against 676).
+            // One lane, elected once, does all of it: the ring positions and phases are its registers, and a
+            // commit tracks the products of its own thread alone. Under a test for lane 0 the compiler does
+            // not know that one lane issues, and an MMA took some 80 cycles to issue (long queries at D =
+            // 128: 868 us against 676).
             auto issue = [&](auto tile) {
                 constexpr int t = decltype(tile)::value;
                 constexpr uint32_t idesc_qk = umma_idesc_bf16(128, BK, false, false);
@@ -415,84 +418,81 @@ __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>
                 uint32_t n_own = 0, n_other = 0;  // QKs of this tile, and of the other one before the next of these
                 uint32_t npv = 0, no = 0;        // PVs, and items this tile has had
                 bool ok = true;
-                while (ok && next_item(it)) {
+                while (ok && next_item_of(it, std::true_type())) {
                     const bool active = it.row + t * 128 < it.n_rows, both = TILES == 2 && it.row + 128 < it.n_rows;
-                    if (elect_one()) {
-                        ok = mbar_wait(q_full, (items - 1) & 1, err);
-                        for (int j = 0; ok && j <= it.blocks; ++j) {
-                            if (j < it.blocks) {  // QK of block j
-                                const uint32_t slot = jk % NK;
-                                ok = mbar_wait(&k_full[slot], (jk / NK) & 1, err);
-                                ++jk;
-                                if (t == 1) ++n_other;  // in turn: tile 0's QK of a block, then tile 1's
-                                if (active) {
-                                    // the scores that lie there have been read
-                                    if (T::ONE_S && n_other > 0) ok = ok && mbar_wait(&s_free[1 - t], (n_other - 1) & 1, err);
-                                    if (n_own > 0) ok = ok && mbar_wait(&s_free[t], (n_own - 1) & 1, err);
-                                    if (!ok) break;
-                                    tc_fence_after();
-                                    const uint64_t kb = kdesc + (uint64_t)((slot * T::kTile) >> 4);
-#pragma unroll
-                                    for (int ks = 0; ks < D / 16; ++ks) {
-                                        const uint32_t off = ((ks >> 2) * T::kPanel + (ks & 3) * 32) >> 4;
-                                        umma_bf16(col_s, qdesc + off, kb + off, idesc_qk, ks > 0 ? 1u : 0u);
-                                    }
-                                    umma_commit(&s_full[t]);
-                                    umma_commit(&k_empty[slot]);
-                                    if (!T::ONE_S && j + 1 == it.blocks) umma_commit(q_empty);
-                                    ++n_own;
-                                } else {
-                                    if (!ok) break;
-                                    mbar_arrive(&k_empty[slot]);
-                                    if (j + 1 == it.blocks) mbar_arrive(q_empty);
-                                }
-                                if (t == 0 && both) ++n_other;
-                            }
-                            if (T::ONE_S && active && j == it.blocks) {
-                                // With S shared, Q is free once the last scores have been loaded too: the issuer
-                                // that has no tile of this item follows none of the loads, and its wait for the
-                                // next item's would pass at an older phase.
-                                ok = mbar_wait(&s_free[t], (n_own - 1) & 1, err);
+                    ok = mbar_wait(q_full, (items - 1) & 1, err);
+                    for (int j = 0; ok && j <= it.blocks; ++j) {
+                        if (j < it.blocks) {  // QK of block j
+                            const uint32_t slot = jk % NK;
+                            ok = mbar_wait(&k_full[slot], (jk / NK) & 1, err);
+                            ++jk;
+                            if (t == 1) ++n_other;  // in turn: tile 0's QK of a block, then tile 1's
+                            if (active) {
+                                // the scores that lie there have been read
+                                if (T::ONE_S && n_other > 0) ok = ok && mbar_wait(&s_free[1 - t], (n_other - 1) & 1, err);
+                                if (n_own > 0) ok = ok && mbar_wait(&s_free[t], (n_own - 1) & 1, err);
                                 if (!ok) break;
-                                mbar_arrive(q_empty);
-                            }
-                            if (j > 0) {  // PV of block j - 1
-                                const uint32_t slot = jv % NV;
-                                ok = mbar_wait(&v_full[slot], (jv / NV) & 1, err);
-                                ++jv;
-                                if (active) {
-                                    if (j == 1 && no > 0) ok = ok && mbar_wait(&o_empty[t], (no - 1) & 1, err);
-                                    const uint64_t vb = vdesc + (uint64_t)((slot * T::kTile) >> 4);
-                                    ok = ok && mbar_wait(&p_full[t], npv & 1, err);
-                                    if (!ok) break;
-                                    tc_fence_after();
+                                tc_fence_after();
+                                const uint64_t kb = kdesc + (uint64_t)((slot * T::kTile) >> 4);
 #pragma unroll
-                                    for (int kk = 0; kk < BK / 16; ++kk)
-                                        umma_bf16_ta(col_o, col_p + kk * 8, vb + ((kk * 16 * 128) >> 4), idesc_pv,
-                                                     (j > 1 || kk > 0) ? 1u : 0u);
-                                    umma_commit(&pv_done[t]);
-                                    umma_commit(&v_empty[slot]);
-                                    ++npv;
-                                } else {
-                                    if (!ok) break;
-                                    mbar_arrive(&v_empty[slot]);
+                                for (int ks = 0; ks < D / 16; ++ks) {
+                                    const uint32_t off = ((ks >> 2) * T::kPanel + (ks & 3) * 32) >> 4;
+                                    umma_bf16(col_s, qdesc + off, kb + off, idesc_qk, ks > 0 ? 1u : 0u);
                                 }
+                                umma_commit(&s_full[t]);
+                                umma_commit(&k_empty[slot]);
+                                if (!T::ONE_S && j + 1 == it.blocks) umma_commit(q_empty);
+                                ++n_own;
+                            } else {
+                                if (!ok) break;
+                                mbar_arrive(&k_empty[slot]);
+                                if (j + 1 == it.blocks) mbar_arrive(q_empty);
+                            }
+                            if (t == 0 && both) ++n_other;
+                        }
+                        if (T::ONE_S && active && j == it.blocks) {
+                            // With S shared, Q is free once the last scores have been loaded too: the issuer
+                            // that has no tile of this item follows none of the loads, and its wait for the
+                            // next item's would pass at an older phase.
+                            ok = mbar_wait(&s_free[t], (n_own - 1) & 1, err);
+                            if (!ok) break;
+                            mbar_arrive(q_empty);
+                        }
+                        if (j > 0) {  // PV of block j - 1
+                            const uint32_t slot = jv % NV;
+                            ok = mbar_wait(&v_full[slot], (jv / NV) & 1, err);
+                            ++jv;
+                            if (active) {
+                                if (j == 1 && no > 0) ok = ok && mbar_wait(&o_empty[t], (no - 1) & 1, err);
+                                const uint64_t vb = vdesc + (uint64_t)((slot * T::kTile) >> 4);
+                                ok = ok && mbar_wait(&p_full[t], npv & 1, err);
+                                if (!ok) break;
+                                tc_fence_after();
+#pragma unroll
+                                for (int kk = 0; kk < BK / 16; ++kk)
+                                    umma_bf16_ta(col_o, col_p + kk * 8, vb + ((kk * 16 * 128) >> 4), idesc_pv,
+                                                 (j > 1 || kk > 0) ? 1u : 0u);
+                                umma_commit(&pv_done[t]);
+                                umma_commit(&v_empty[slot]);
+                                ++npv;
+                            } else {
+                                if (!ok) break;
+                                mbar_arrive(&v_empty[slot]);
                             }
                         }
-                        if (active) ++no;
-                        if (!ok) s_abort = 1;
                     }
-                    ok = __all_sync(0xffffffffu, ok);  // (the other lanes' stays true)
+                    if (active) ++no;
+                    if (!ok) s_abort = 1;
                 }
-            };
-            if (warp == kMma0)
-                issue(std::integral_constant<int, 0>());
-            else
-                issue(std::integral_constant<int, TILES - 1>());
-            // the products (and the arrivals committed behind them) end before shared memory goes
-            if (lane == 0) {
+                // the products (and the arrivals committed behind them) end before shared memory goes
                 umma_commit(fin);
                 mbar_wait(fin, 0, err);
+            };
+            if (elect_one()) {
+                if (warp == kMma0)
+                    issue(std::integral_constant<int, 0>());
+                else
+                    issue(std::integral_constant<int, TILES - 1>());
             }
             __syncwarp();
         } else if (warp == kKw || warp == kVw) {
