@@ -126,6 +126,14 @@ int check_workspace(const void* ws, size_t have, size_t need) {
     return RPA_OK;
 }
 
+// The workspace of a cache write: optional, and only its error word is used.
+int check_status_workspace(const void* ws, size_t have) {
+    if (!ws) return RPA_OK;
+    if (have < (size_t)kWsHeaderBytes) return fail(RPA_ERR_WORKSPACE, "workspace smaller than 256 bytes");
+    if (reinterpret_cast<uintptr_t>(ws) % alignof(WsHeader)) return fail(RPA_ERR_WORKSPACE, "workspace must be aligned");
+    return RPA_OK;
+}
+
 // ---------------------------- MLA ----------------------------------------
 struct LatLayout {
     size_t items, tickets, pml, po, total;
@@ -471,9 +479,10 @@ int rpa_forward(const rpa_params* p, const void* q, const void* kv_pages, const 
 int rpa_update_kv_cache(const rpa_params* p, const void* new_k, const void* new_v, void* kv_pages,
                         const int32_t* kv_lens, const int32_t* page_indices, const int32_t* cu_q_lens,
                         const int32_t* num_seqs, void* workspace, size_t workspace_bytes, rpa_stream_t stream) {
-    if (workspace && workspace_bytes < (size_t)kWsHeaderBytes) return fail(RPA_ERR_WORKSPACE, "workspace smaller than 256 bytes");
+    int rc = check_status_workspace(workspace, workspace_bytes);
+    if (rc) return rc;
     RpaUpdateArgs a;
-    const int rc = rpa_update_prepare(p, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs,
+    rc = rpa_update_prepare(p, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs,
                                       workspace ? &reinterpret_cast<WsHeader*>(workspace)->error_bits : nullptr, a);
     if (rc) return rc;
     const int sms = num_sms_current();
@@ -668,9 +677,10 @@ int rpa_rope_update_kv_cache(const rpa_params* p, const rope_table* t, const rop
                              const int32_t* page_indices, const int32_t* cu_q_lens, const int32_t* num_seqs,
                              const int32_t* positions, void* q_out, void* workspace, size_t workspace_bytes,
                              rpa_stream_t stream) {
-    if (workspace && workspace_bytes < (size_t)kWsHeaderBytes) return fail(RPA_ERR_WORKSPACE, "workspace smaller than 256 bytes");
+    int rc = check_status_workspace(workspace, workspace_bytes);
+    if (rc) return rc;
     RopeUpdateArgs a;
-    const int rc = rope_update_prepare(p, t, strides, q, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs,
+    rc = rope_update_prepare(p, t, strides, q, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs,
                                        positions, q_out,
                                        workspace ? &reinterpret_cast<WsHeader*>(workspace)->error_bits : nullptr, a);
     if (rc) return rc;
@@ -806,7 +816,8 @@ int mla_update_kv_cache(const mla_params* p, const void* new_kv_c, const void* n
         return fail(RPA_ERR_NULL, "a tensor pointer is NULL");
     if (!aligned16(new_kv_c) || !aligned16(new_k_pe) || !aligned16(cache_kv_c) || !aligned16(cache_k_pe))
         return fail(RPA_ERR_VALUE, "tensors must be 16-byte aligned");
-    if (workspace && workspace_bytes < (size_t)kWsHeaderBytes) return fail(RPA_ERR_WORKSPACE, "workspace smaller than 256 bytes");
+    rc = check_status_workspace(workspace, workspace_bytes);
+    if (rc) return rc;
     const int sms = num_sms_current();
     if (!sms) return fail(RPA_ERR_CUDA, "no CUDA device");
     MlaUpdateArgs a;
@@ -1024,7 +1035,8 @@ int sparse_mla_write_and_attend_ragged(const sparse_ragged_params* p, const void
 
 int rpa_selftest_bounded_wait(void* workspace, size_t workspace_bytes, rpa_stream_t stream) {
     if (!workspace) return fail(RPA_ERR_NULL, "workspace is NULL");
-    if (workspace_bytes < (size_t)kWsHeaderBytes) return fail(RPA_ERR_WORKSPACE, "workspace smaller than 256 bytes");
+    const int rc = check_status_workspace(workspace, workspace_bytes);
+    if (rc) return rc;
     cudaError_t e = launch_wait_selftest(&reinterpret_cast<WsHeader*>(workspace)->error_bits,
                                          reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "rpa_selftest_bounded_wait launch");
