@@ -302,7 +302,9 @@ typedef struct {
 /* q [num_tokens, num_q_heads, head_dim] and k [num_tokens, num_k_heads, head_dim], bf16, turned by
  * positions int32 [num_tokens] (any value, negative ones too) into q_out and k_out, bf16: computed
  * in float32, rounded once.  q_out may be q and k_out may be k (with the same strides); otherwise
- * outputs overlap neither inputs nor each other. */
+ * outputs overlap neither inputs nor each other.  Operands that share no element may lie between one
+ * another where their token strides are equal, and their head strides are or each stays inside a part
+ * of the token; other interleaved layouts are refused. */
 RPA_API int rope_apply(const rope_apply_params* p, const rope_table* t, const void* q, const void* k,
                        const int32_t* positions, void* q_out, void* k_out, rpa_stream_t stream);
 

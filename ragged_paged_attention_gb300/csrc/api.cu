@@ -5,6 +5,7 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "common.cuh"
@@ -317,26 +318,39 @@ int rope_rows(const char* name, const void* p, int tokens, int heads, int dim, i
     return RPA_OK;
 }
 
-// Whether two operands share elements. Rows of one token stride that stay inside it (slices of
-// one projection's output) are compared by their place in it, others by their extent.
+// Whether two operands share elements. Rows of one token stride that stay inside it (slices of one
+// projection's output) are compared by their place in it; operands whose head strides are equal too (parts
+// of the same heads) row by row; others by their extents. The stride of a dimension of one entry is any.
 bool rope_overlap(const RopeRows& a, int ha, const RopeRows& b, int hb, int tokens, int dim) {
     if (tokens <= 0) return false;
     const int64_t ra = (ha - 1) * a.head + dim, rb = (hb - 1) * b.head + dim;  // a token's elements
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
     const uintptr_t a1 = a0 + 2 * ((tokens - 1) * a.token + ra), b1 = b0 + 2 * ((tokens - 1) * b.token + rb);
     if (a1 <= b0 || b1 <= a0) return false;
-    if (a.token == b.token && tokens > 1 && ra <= a.token && rb <= b.token) {
-        const int64_t step = 2 * a.token;
-        const int64_t off = b0 >= a0 ? (int64_t)((b0 - a0) % step) : (step - (int64_t)((a0 - b0) % step)) % step;
-        return !(off >= 2 * ra && off + 2 * rb <= step);
+    if (tokens > 1 && a.token != b.token) return true;
+    const int64_t token = a.token, off = ((int64_t)b0 - (int64_t)a0) / 2;  // (both are 16-byte aligned)
+    auto floor_div = [](int64_t x, int64_t y) { return x / y - (x % y < 0); };
+    if (tokens > 1 && ra <= token && rb <= token) {
+        const int64_t in = off - floor_div(off, token) * token;
+        if (in >= ra && in + rb <= token) return false;
     }
-    return true;
+    if (ha > 1 && hb > 1 && a.head != b.head) return true;
+    // Rows dt tokens and dh heads apart begin off + dt token + dh head elements apart: for each dh the dt that
+    // brings them nearest is one of two.
+    const int64_t head = ha > 1 ? a.head : b.head, most = tokens - 1;
+    for (int64_t dh = 1 - ha; dh < hb; ++dh) {
+        const int64_t x = off + dh * head, dt = floor_div(-x, token);
+        for (int64_t t : {dt, dt + 1}) {
+            const int64_t y = x + std::min(std::max(t, -most), most) * token;
+            if (y > -dim && y < dim) return true;
+        }
+    }
+    return false;
 }
 
 // An output beside an input: the same rows (in place) or none of them.
 bool rope_in_place_or_apart(const RopeRows& in, const RopeRows& out, int heads, int tokens, int dim) {
-    if (in.p == out.p && in.token == out.token && in.head == out.head) return true;
-    if (in.p == out.p && tokens <= 1 && (heads <= 1 || in.head == out.head)) return true;
+    if (in.p == out.p && (tokens <= 1 || in.token == out.token) && (heads <= 1 || in.head == out.head)) return true;
     return !rope_overlap(in, heads, out, heads, tokens, dim);
 }
 

@@ -1,0 +1,33 @@
+"""Calls of the rotating, appending and cross-attention operators that their documentation allows and that
+the parity tests beside this file do not make."""
+import pytest
+import torch
+
+import plain
+from ragged_paged_attention_gb300 import api
+from test_gpu_rope import bits, near, randn
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP8, INT8, INT4 = torch.bfloat16, torch.float8_e4m3fn, torch.int8, torch.uint8
+
+
+@pytest.mark.parametrize("T,H", [(1, 1), (1, 5), (19, 1), (19, 5), (300, 16)])
+@pytest.mark.parametrize("rot,inter", [(64, False), (48, True), (24, False), (6, True)])
+def test_parts_of_the_same_heads_in_place(T, H, rot, inter):
+    # [T, H, 3, D]: q and k of a head beside one another, turned where they are; v stays
+    x = randn(T + H, T, H, 3, 64)
+    g, pos = x.cuda(), torch.arange(5, 5 + T, dtype=torch.int32)
+    t, (f, amp) = api.make_rope_table(rot, interleaved=inter), plain.frequencies(rot)
+    q, k = g[:, :, 0], g[:, :, 1]
+    api.rope_apply(q, k, pos.cuda(), t, q_out=q, k_out=k)
+    for i in (0, 1):
+        near(g[:, :, i].cpu(), plain.rope(x[:, :, i], pos, f, amp, inter), plain.rope_slack(x[:, :, i], f, amp, inter))
+    assert torch.equal(bits(g[:, :, 2].cpu()), bits(x[:, :, 2]))
+    # q's result into v's place, k's into q's
+    g = x.cuda()
+    with pytest.raises(api.RpaError):
+        api.rope_apply(g[:, :, 0], g[:, :, 1], pos.cuda(), t, q_out=g[:, :, 2], k_out=g[:, :, 0])
+    api.rope_apply(g[:, :, 0], None, pos.cuda(), t, q_out=g[:, :, 2])
+    near(g[:, :, 2].cpu(), plain.rope(x[:, :, 0], pos, f, amp, inter), plain.rope_slack(x[:, :, 0], f, amp, inter))
+    assert torch.equal(bits(g[:, :, :2].cpu()), bits(x[:, :, :2]))
