@@ -217,25 +217,33 @@ class Workspace:
         return buf
 
 
-_workspaces: dict = {}
+_kept = threading.local()  # .workspaces: this thread's {(device, stream): workspace}; they go with the thread
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 _current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _BF16, _I32 = torch.bfloat16, torch.int32
 
 
+def _own_workspaces() -> dict:
+    try:
+        return _kept.workspaces
+    except AttributeError:
+        _kept.workspaces = {}
+        return _kept.workspaces
+
+
 def _own_workspace(nbytes: int, device: int, stream: int) -> torch.Tensor:
     """The workspace of an attention call that was given none: one per device, stream and thread, so that
-    calls that overlap share none; while the stream is captured a new one, owned by the graph.  Of that
-    one only the header, with the error word, is zeroed on every replay: the plan writes the rest before
-    it is read."""
+    calls that overlap share none, kept until the thread ends; while the stream is captured a new one,
+    owned by the graph.  Of that one only the header, with the error word, is zeroed on every replay: the
+    plan writes the rest before it is read."""
     if torch.cuda.is_current_stream_capturing():
         ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
         ws[:256].zero_()
         return ws
-    key = (device, stream, threading.get_ident())
-    ws = _workspaces.get(key)
+    kept = _own_workspaces()
+    ws = kept.get((device, stream))
     if ws is None or ws.numel() < nbytes:
-        ws = _workspaces[key] = torch.zeros(nbytes, dtype=torch.uint8, device=device)
+        ws = kept[device, stream] = torch.zeros(nbytes, dtype=torch.uint8, device=device)
     return ws
 
 

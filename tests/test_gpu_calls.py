@@ -1,10 +1,14 @@
 """Calls of the rotating, appending and cross-attention operators that their documentation allows and that
 the parity tests beside this file do not make."""
+import threading
+
 import pytest
 import torch
 
 import plain
+from parity import TOL_BF16
 from ragged_paged_attention_gb300 import api
+from test_gpu_cross import batch, reference
 from test_gpu_rope import bits, near, randn
 
 pytestmark = pytest.mark.gpu
@@ -31,3 +35,32 @@ def test_parts_of_the_same_heads_in_place(T, H, rot, inter):
     api.rope_apply(g[:, :, 0], None, pos.cuda(), t, q_out=g[:, :, 2])
     near(g[:, :, 2].cpu(), plain.rope(x[:, :, 0], pos, f, amp, inter), plain.rope_slack(x[:, :, 0], f, amp, inter))
     assert torch.equal(bits(g[:, :, :2].cpu()), bits(x[:, :, :2]))
+
+
+# ------------------------------------------------------------------ workspaces of calls that were given none
+def cross(b, g, **kw):
+    return api.rpa_cross_forward(g.q, g.kv_pages, g.kv_lens, g.page_indices, g.cu_q_lens, g.num_seqs, sm_scale=b.sm_scale, **kw)
+
+
+def test_own_workspaces_go_with_their_thread():
+    b = batch([1, 20], [300, 64], 8, 2, 128, 16, seed=1)
+    g, ref, n = b.to("cuda"), reference(b), b.num_tokens
+    outs, all_called = [], threading.Barrier(4)
+
+    def work(stream):
+        with torch.cuda.stream(stream):
+            outs.append(cross(b, g))
+        stream.synchronize()
+        all_called.wait(60)
+
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    threads = [threading.Thread(target=work, args=(torch.cuda.Stream(),)) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    size = api.rpa_cross_workspace_size(api.make_rpa_params(g.q, g.kv_pages, g.page_indices))
+    assert torch.cuda.memory_allocated() - before < size  # (four outputs of some KB)
+    for out in outs:
+        assert (out[:n].cpu().double() - ref[:n]).abs().max().item() <= TOL_BF16
