@@ -893,9 +893,18 @@ def selftest_bounded_wait(workspace: torch.Tensor) -> None:
     _check(load_library().rpa_selftest_bounded_wait(_ptr(workspace), workspace.numel(), _stream()))
 
 
-def check_device_status(workspace: torch.Tensor) -> int:
-    """Synchronise, read and clear the workspace error word; returns its bits (0 = fine)."""
+def check_device_status(workspace: torch.Tensor | None = None) -> int:
+    """Synchronise, read and clear the workspace error word; returns its bits (0 = fine).
+
+    Without a workspace: that of this thread's ``rpa_cross_forward`` and ``rpa_rope_forward_update`` calls on
+    the current stream that were given none.  (A captured call's own workspace is the graph's: give it one
+    to read its word.)"""
     lib = load_library()
+    if workspace is None:
+        device = _current()
+        workspace = _own_workspaces().get((device, _raw_stream(device)))
+        if workspace is None:
+            return 0
     bits = ctypes.c_uint32(0)
     rc = lib.rpa_check_device_status(_ptr(workspace), ctypes.byref(bits), _stream())
     if rc not in (0, -7):

@@ -64,3 +64,22 @@ def test_own_workspaces_go_with_their_thread():
     assert torch.cuda.memory_allocated() - before < size  # (four outputs of some KB)
     for out in outs:
         assert (out[:n].cpu().double() - ref[:n]).abs().max().item() <= TOL_BF16
+
+
+def test_the_error_word_of_an_own_workspace():
+    b = batch([2, 40, 3], [100, 200, 50], 8, 2, 128, 16, seed=5)
+    b.kv_lens[1] = 10**6
+    g = b.to("cuda")
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(streams[0]):
+        cross(b, g)
+        seen = []
+        t = threading.Thread(target=lambda: seen.append(api.check_device_status()))  # that thread has made no call
+        t.start()
+        t.join()
+    with torch.cuda.stream(streams[1]):
+        seen.append(api.check_device_status())  # nor has this stream seen one of ours
+    with torch.cuda.stream(streams[0]):
+        seen += [api.check_device_status(), api.check_device_status()]
+    assert seen == [0, 0, 0x04, 0]
