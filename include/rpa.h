@@ -32,7 +32,9 @@
  *     aligned, must be zero-filled once after it is allocated (the library keeps it
  *     consistent from then on), and must not be shared by two calls in flight at once.
  *   - Calls are asynchronous on `stream` and never synchronise with the host, so
- *     they can be captured in a CUDA graph.  Sizes read from device memory
+ *     they can be captured in a CUDA graph.  A call may stand right behind kernels of the
+ *     caller's that write its tensors, lengths and page tables, also ones that let the next
+ *     launch of the stream start early.  Sizes read from device memory
  *     (num_seqs, cu_q_lens, kv_lens, page tables, indices) are validated on the
  *     device: a bad value sets a bit in the workspace's error word, the offending
  *     sequence/query is skipped (its output rows are left untouched), and no
@@ -323,9 +325,11 @@ typedef struct {
  *   positions     int32 [max_num_tokens], or NULL: the position of the token's slot,
  *                 kv_len - q_len + j (the slot is that one either way)
  *   q_out         [max_num_tokens, num_q_heads, head_dim] bf16, dense; may be q if q is dense
- * The cache gets x / k_scale (x / v_scale; no division with scale 0), x in float32 after the turn,
- * rounded to nearest even: to bf16; to e4m3, +-448 at most, NaN kept; to int8 or int4, within
- * [-128, 127] or [-8, 7], NaN as 0.  rpa_forward with the same scales reads it back.
+ * The cache gets x / k_scale (x / v_scale; no division with scale 0), x in float32 after the turn and
+ * the quotient as its product with the scale's float32 reciprocal (exact for powers of two, else within
+ * 2^-23 of itself for scales up to 2^126), rounded to nearest even: to bf16; to e4m3, +-448 at most,
+ * NaN kept; to int8 or int4, within [-128, 127] or [-8, 7], NaN as 0.  rpa_forward with the same
+ * scales reads it back.
  * head_dim and kv_dtype as rpa_update_kv_cache; int4 takes rotary_dim a multiple of 4.
  * A scale's reciprocal must be finite.  Only the slots of the batch's tokens are written, and the
  * q_out rows of those tokens: a token whose metadata is bad is skipped whole, as are the tokens

@@ -497,7 +497,9 @@ def rope_apply(q, k, positions, table, *, inverse=False, q_out=None, k_out=None)
     """Turns q [T, Hq, D] and k [T, Hk, D] (or None) to ``positions`` [T] int32; returns ``(q_out, k_out)``.
 
     q and k are bf16 with any token and head strides; ``q_out=q`` and ``k_out=k`` work in place.
-    ``inverse`` turns back by the same angles (the map of an output's gradient to the input's)."""
+    ``inverse`` turns back by the same angles (the map of an output's gradient to the input's).  Autograd does
+    not see the call: outputs carry no history, and a turn in place leaves the tensor's version as it was; a
+    training program calls it and its inverse from an ``autograd.Function`` of its own."""
     lib = _lib or load_library()
     _is_table(table)
     dev = _cuda_index(q, "q")

@@ -26,9 +26,11 @@ __host__ __device__ inline int update_cache_ints(int max_num_seqs) {
 constexpr int kPrefillRows = 128;       // (token, q-head) rows per prefill item (one TMEM tile)
 constexpr int kMinChunk = 256;          // smallest split-KV chunk (keys)
 // rpa_rope_forward_update's, beside a group's cost on the line (so that every share holds keys), which its
-// small decode batches meet: 7 decodes over some 1500 fp8 keys of 8 heads take 37.9 us with chunks of 256
-// keys at least, 33.3 with 128, 36.1 with 64 (more to join); batches that fill the SMs are cut longer than
-// either
+// small decode batches meet. 1 to 24 decodes of 8 KV heads of 128, with chunks of at least 256, 128 and 64
+// keys: over 100-3000 keys 37-43, 30-46 and 31-46 us in fp8 (7 of them 37, 32 and 37), 41-58, 34-53 and 32-52
+// in bf16; over 20-200 keys 23-40, 22-32 and 20-27 in fp8, 24-37, 20-30 and 21-29 in bf16; over 6000-9000 keys
+// equal from 12 decodes on, and with fewer 64 loses up to a third (more to join) and 128 up to a sixth against
+// 256. Batches that fill the SMs are cut longer than any
 constexpr int kStepMinChunk = 128;
 // Cross attention's two-tile kernel: a sequence of up to kCrossSplitRows rows (a tile) may be cut along its
 // keys into up to kCrossMaxSplits pieces, whose results wait in slots of kCrossSlotRows rows.  The last
@@ -320,7 +322,7 @@ cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, c
 // 3-D bf16 tensor [d2][d1][d0] (d0 contiguous) with a box of {64, b1, b2}, 128-byte swizzle.
 bool make_tmap_bf16(struct CUtensorMap_st* tm, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b1,
                     uint32_t b2);
-// Cross attention's prefill-class work with two tiles in flight an SM, for the batches it takes.
+// Cross attention with two tiles in flight an SM: every sequence, decode's too, of the batches it takes.
 bool rpa_cross_tc_takes(const RpaArgs& a);
 int rpa_cross_tile_rows(const RpaArgs& a);  // 256 or 128: the rows of an item
 cudaError_t launch_rpa_cross_tc(const RpaArgs& a, int num_sms, cudaStream_t stream);

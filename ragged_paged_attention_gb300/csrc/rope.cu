@@ -2,6 +2,8 @@
 // for sm_103a.
 //
 // Both only move memory: a turned element costs two fused multiply-adds against four bytes.
+// rope_apply of 8191 tokens, 32 + 8 heads of 128: 28.7 us in a graph, 0.87 of the copy rate; the cache write of
+// 4 x 4096 tokens, 32 + 8 + 8 heads of 128: bf16 70, fp8 62, int8 64, int4 65 us.
 #include "common.cuh"
 #include "kernels.h"
 #include "profile.h"
@@ -9,8 +11,9 @@
 
 namespace rpa {
 
-// The narrow path (rotary_dim not a multiple of 16): calls body(u, turns, cs, head) for every unit u
-// of heads [h_begin, h_end) of head_dim elements.
+// The narrow path (rotary_dim not a multiple of 16): a warp a token, chunks of 4 or 2 bytes, its own sines, no
+// row's loads ahead of another's. Calls body(u, turns, cs, head) for every unit u of `heads` heads of head_dim
+// elements. (8191 tokens of 32 + 8 heads of 128: rotary_dim 24 61 us, 6 100 us, 128 on the other path 28.7.)
 template <int VEC, typename F>
 __device__ __forceinline__ void rope_units(const RopeTab& tab, int head_dim, int heads, int pos, F&& body) {
     const int lane = threadIdx.x & 31, units = head_dim / (2 * VEC);
@@ -127,6 +130,10 @@ __device__ __forceinline__ void update_out(const RopeUpdateArgs& a, int t, int h
     *reinterpret_cast<Chunk*>(dst + cb) = xb;
 }
 
+// At four blocks an SM a thread has 64 registers, and every form spills 40 to 120 bytes of them (three copies of
+// the walk, with the slots' search in each). At three, without spills, 61 decodes and 2 x 1021 tokens of 16 + 8 +
+// 8 heads of 256 take bf16 14.6, fp8 12.2, int8 13.2 and int4 13.3 us instead of 12.4, 12.3, 12.7 and 13.1; 4 x
+// 4096 tokens 69, 64, 66 and 64 instead of 69, 62, 64 and 65.
 template <bool INTER, int KV>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rpa_rope_update_kernel(const __grid_constant__ RopeUpdateArgs a) {
     __shared__ RopeShared sh;
@@ -264,9 +271,11 @@ static RopeShare rope_share(const RopeTab& tab, int tokens, int heads, int head_
 static void rope_shares(const RopeTab& tab, int tokens, int ha, int hb, int nb, int head_dim, int num_sms, RopeShare& a, RopeShare& b) {
     const double all = (double)tokens * (ha + nb * hb), passes = kRopePasses * (double)(kRopeThreads / (head_dim / 16));
     double share = min(max(passes, all / (kRopeBlocks * num_sms)), all / (2 * num_sms));
-    // what the SMs hold at once and up to half as many again goes as one round of longer shares (61 decodes and
-    // 2 x 1021 tokens of 32 heads of 256, 1.4 rounds: 15.9 us, in two 17.7; more rounds are best left as they
-    // come: 8191 tokens of 40 heads, 3.4 rounds: 28.8 us, in three 29.2)
+    // what the SMs hold at once and up to half as many again goes as one round of longer shares (a cache write of
+    // 61 decodes and 2 x 1021 tokens of 32 heads of 256 15.9 us, in two rounds 17.7; of 2700 tokens of 48 heads of
+    // 128 12.6 and 13.9, 2200 of them 11.3 and 11.1, 2000 of 32 heads of 256 11.9 and 11.4; rope_apply of 3000
+    // tokens of 40 heads 11.1 and 11.5). Between one and a half and two and a half one round would gain 2 to 8 %
+    // more, beyond it nothing (8191 tokens, either way the same)
     const int at_once = kRopeBlocksPerSm * num_sms;
     for (int i = 0; i < 40; ++i, share *= 1.03) {
         a = rope_share(tab, tokens, ha, head_dim, share);

@@ -97,7 +97,9 @@ __device__ __forceinline__ uint32_t quant_e4m3x2(float x, float y) {
     return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
 }
 
-// VEC values, divided by the scale and rounded once, to the cache at element `at` of a head row.
+// VEC values times the scale's float32 reciprocal, rounded to the cache's type, at element `at` of a head row.
+// (A power of two's reciprocal is exact; with another scale the product is up to 2^-23 of itself off the quotient,
+// a division, which takes several instructions an element, 2^-24.)
 template <int KV, int VEC>
 __device__ __forceinline__ void rope_store_kv(uint8_t* row, int at, const float* x, float inv) {
     float y[VEC];

@@ -9,13 +9,19 @@
 // the row maximum, the exponentials and P to the next product some 1650 cycles of one warp's latencies
 // and issue slots (measured by clock reads; the 32 exponentials a cycle are not what it waits for).
 // So two tiles of 128 rows are in flight on every SM, each with warps of its own: while one tile's
-// softmax runs, the tensor pipe works for the other. With a row's 128 scores in one thread no maximum
-// is exchanged between warps (two warps a row quarter, half a row a thread: 745 us against 676 for 4 x
-// 4096 queries over 4096 keys, 32/8 heads of 128, which is 1626 TFLOP/s). The causal kernel keeps one tile
-// in flight, its rows split over two warps: 839 us. The two tiles are
+// softmax runs, the tensor pipe works for the other. "Long" below is 4 x 4096 queries over 4096 keys, 32/8
+// heads of 128: 722 us (1523 TFLOP/s) called again and again on fresh inputs, 691 in a graph on the same ones;
+// shares of it are of two builds timed in turn. With a row's 128 scores in one thread no maximum is exchanged
+// between warps (two warps a row quarter, half a row a thread: long 10 % slower). The causal kernel keeps one
+// tile in flight, its rows split over two warps: long 24 % slower. The two tiles are
 //   TILES = 2 (D = 128): 256 rows of one KV head in one CTA, which share the K/V stream;
 //   TILES = 1 (D = 64): two CTAs an SM with a tile each, whose softmaxes drift apart by themselves
-//              (8 x 4864 queries over 1536 keys, 20 heads: 323 us; with TILES = 2: 351 us).
+//              (8 x 4864 queries over 1536 keys, 20 heads: 318 us; with TILES = 2 9 % slower). It is
+//              compiled for 128 registers a thread, two CTAs' worth, and spills two of them.
+// Fewer bits than 32: P goes to the tensor pipe as bf16 (2^-8 of an element at most), since V is bf16 and the
+// two operands of an MMA have one type, while l adds the unrounded values; exponentials are ex2.approx (2^-22).
+// Scores, maxima, sums and O are float32. In the root mean square the outputs are 2.3e-3 of themselves off the
+// float64 softmax, where the exact ones rounded to bf16 are 1.7e-3 off.
 // Per CTA: 4 softmax warps a tile (a row a thread); then warps
 //   0 .. TILES - 1: an MMA issuer a tile;
 //   2: streams K (and takes the items and loads Q); 3: streams V. One 3-D tensor copy per page-sized
@@ -28,8 +34,8 @@
 // (P over S instead, with the next QK behind PV: 1.29 us a block against 0.97 in the causal kernel.)
 // Batches of few rows: a tile of one row costs what a full one does, 0.93 us a block and SM at D = 64, about
 // what HBM takes for the block's keys and values (64 decodes over 1450 keys, 20 heads: 90 us, 70 at the copy
-// rate). Warps without rows that skip their exponentials do not change that (92.2 us both ways) and slow the
-// long case, whose loop they change, from 700 to 731 us.
+// rate). Warps without rows that skip their exponentials do not change that (92.2 us both ways) and slow long,
+// whose loop they change, by 4 %.
 // Barriers, all waits bounded: k/v_full, k/v_empty (rings), q_full, q_empty (Q loaded; its last QK done and,
 // where the tiles share S, the scores loaded), item_full/empty (two items' numbers, handed on by the K
 // warp); per tile s_full (QK done), s_free (scores loaded), p_full (P written, O rescaled), pv_done (PV read
@@ -367,7 +373,7 @@ __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>
                     continue;
                 }
                 // rows of 32-byte units where `out` allows them (64 sequences of 64 queries and keys, 32/8 heads of
-                // 128: 30 us, in 16-byte stores 33; the long case 712 and 727)
+                // 128: 30 us, in 16-byte stores 33; long 2 % slower in those)
                 const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
                 const float inv = l > 0.f ? 1.f / l : 0.f;
                 __nv_bfloat16* dst = a.out + ((size_t)(it.q_start + (rv ? R / G : 0)) * a.num_q_heads + it.head * G +
@@ -404,8 +410,7 @@ __global__ void __launch_bounds__(CrossTc<D, TILES>::kThreads, CrossTc<D, TILES>
             // ---------------- MMA issuer of tile t (a constant in either branch) ----------------
             // One lane, elected once, does all of it: the ring positions and phases are its registers, and a
             // commit tracks the products of its own thread alone. Under a test for lane 0 the compiler does
-            // not know that one lane issues, and an MMA took some 80 cycles to issue (long queries at D =
-            // 128: 868 us against 676).
+            // not know that one lane issues, and an MMA took some 80 cycles to issue (long 28 % slower).
             auto issue = [&](auto tile) {
                 constexpr int t = decltype(tile)::value;
                 constexpr uint32_t idesc_qk = umma_idesc_bf16(128, BK, false, false);
