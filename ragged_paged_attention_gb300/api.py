@@ -203,9 +203,11 @@ def _opt(x, default=0.0):
 
 
 class Workspace:
-    """A zero-initialised device buffer reused across calls (one per device and purpose)."""
+    """A zero-initialised device buffer reused across calls (one per device and purpose).  One that a call was
+    captured with stays when a larger one replaces it: the graph holds its address."""
 
     _cache: dict = {}
+    _captured: dict = {}
 
     @classmethod
     def get(cls, nbytes: int, device, tag: str = "default") -> torch.Tensor:
@@ -214,6 +216,8 @@ class Workspace:
         if buf is None or buf.numel() < nbytes:
             buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
             cls._cache[key] = buf
+        if torch.cuda.is_current_stream_capturing():
+            cls._captured[buf.data_ptr()] = buf
         return buf
 
 

@@ -88,6 +88,24 @@ def test_the_error_word_of_an_own_workspace():
     assert seen == [0, 0, 0x04, 0]
 
 
+def test_a_graph_of_a_call_with_the_shared_workspace_after_a_larger_call():
+    b, big = batch([1, 20], [300, 64], 8, 2, 128, 16, seed=1), batch([1] * 900, [40] * 900, 32, 16, 256, 16, seed=2)
+    g, n = b.to("cuda"), b.num_tokens
+    run = lambda b, g, out: api.rpa_forward(g.q, g.kv_pages, g.kv_lens, g.page_indices, g.cu_q_lens, g.num_seqs, out=out, **b.options())  # noqa: E731
+    want, out = run(b, g, torch.full_like(g.q, 7.0)), torch.full_like(g.q, 7.0)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(b, g, out)
+    gb = big.to("cuda")
+    run(big, gb, torch.empty_like(gb.q))
+    torch.cuda.synchronize()
+    filler = [torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda") for _ in range(200)]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(bits(out[:n]), bits(want[:n])) and all((f == 255).all() for f in filler)
+
+
 # ------------------------------------------------------------------ cross attention
 LENS = ([1, 3, 0, 2, 40, 1, 150, 17, 5], [1, 700, 64, 0, 9, 1500, 130, 0, 600])
 

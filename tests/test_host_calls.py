@@ -110,3 +110,19 @@ def test_overlap_is_told_from_interleaving(lib):
                 assert rc == (-4 if shared else NO_GPU), (d, head, token, T, hq, hk, shift)
                 seen[shared] += 1
     assert min(seen.values()) > 100
+
+
+def test_a_captured_calls_cached_workspace_outlives_its_replacement(monkeypatch):
+    # (rpa_forward's and the others' that share one per device: a graph holds the address)
+    import weakref
+
+    import torch
+    monkeypatch.setattr(api.Workspace, "_cache", {})
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    eager = weakref.ref(api.Workspace.get(300, "cpu", "a"))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    captured = weakref.ref(api.Workspace.get(1000, "cpu", "a"))
+    assert eager() is None and captured().numel() == 1000
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    assert api.Workspace.get(5000, "cpu", "a").numel() == 5000
+    assert captured() is not None and captured().numel() == 1000
