@@ -18,6 +18,10 @@
  *                        _sparse_mla_kernel_chunked_hminor).
  *   rpa_cross_forward    attention to all the keys of a sequence, whatever their number.
  *   rope_apply           rotary positions on packed queries and keys.
+ *   rpa_g4_forward       rpa_forward over a cache of 4-bit values with a scale and a minimum a group,
+ *                        which rpa_g4_update_kv_cache writes and rpa_g4_read_kv_cache reads back.
+ *   rpa_key_weights      the attention that each cached key gets, added up over calls, and
+ *   rpa_evict_kv_cache   the keys with the most of it kept at the front of their pages.
  *   rpa_rope_update_kv_cache
  *                        rpa_update_kv_cache with the rotation, and the rounding to the
  *                        cache's type, on the way; rpa_rope_forward_update attends in the
@@ -90,6 +94,9 @@ typedef enum {
     RPA_DTYPE_FP8_E4M3 = 2,
     RPA_DTYPE_F32 = 3,
     RPA_DTYPE_INT8 = 4,          /* two's-complement bytes (RPA K/V only) */
+    RPA_DTYPE_G4 = 6,            /* rows of 4-bit values with a scale and a minimum for each group of them (the
+                                  * rpa_g4_* calls, rpa_key_weights and rpa_evict_kv_cache only; their layout is
+                                  * described there) */
     RPA_DTYPE_INT4 = 5           /* two's-complement 4-bit values, two to a byte along the head
                                   * dimension: element 2i of a row in the low nibble (bits 0-3) of
                                   * the row's byte i, element 2i+1 in the high nibble (RPA K/V only;
@@ -368,6 +375,47 @@ RPA_API int rpa_cross_workspace_size(const rpa_params* p, size_t* bytes);
 RPA_API int rpa_cross_forward(const rpa_params* p, const void* q, const void* kv_pages, const int32_t* kv_lens,
                               const int32_t* page_indices, const int32_t* cu_q_lens, const int32_t* num_seqs, void* out,
                               void* workspace, size_t workspace_bytes, rpa_stream_t stream);
+
+/* ---------------------------------------------------------------------- */
+/* 4-bit caches with a scale and a minimum a group                          */
+/* ---------------------------------------------------------------------- */
+
+/* A cache of RPA_DTYPE_G4 is uint8 [total_num_pages, page_size, num_kv_heads, RPA_G4_ROW_BYTES(head_dim)]
+ * (num_kv_heads = num_combined_kv_heads / 2).  A row holds a token's K and V of one KV head:
+ *   bytes [0, head_dim / 2)         K's numbers, element 2i in the low half of byte i, 2i + 1 in the high half
+ *   bytes [head_dim / 2, head_dim)  V's
+ *   then                            (s, m), two bf16, of each group of K and then of each group of V
+ * A group is RPA_G4_GROUP(head_dim) elements; an element is s n + m with its number n in 0..15.  head_dim is 64,
+ * 128 or 256; kv_dtype RPA_DTYPE_G4, k_scale and v_scale 0, mask_value NaN. */
+#define RPA_G4_GROUP(head_dim) ((head_dim) == 64 ? 32 : 64)
+#define RPA_G4_ROW_BYTES(head_dim) ((head_dim) + 8 * ((head_dim) / RPA_G4_GROUP(head_dim)))
+
+/* rpa_rope_update_kv_cache into such a cache: the same arguments, the same rows and slots.  K (after its turn) and V
+ * are rounded to bf16, as a bf16 cache would hold them; a NaN then counts as 0 and what lies beyond +-2^48 as
+ * that.  Of a group, m is the least, s the bf16 nearest to (greatest - least) / 15, and n is (x - m) / s
+ * rounded to nearest even, 15 at most (0 where s is 0).  rotary_dim is a multiple of 16. */
+RPA_API int rpa_g4_update_kv_cache(const rpa_params* p, const rope_table* t, const rope_strides* strides, const void* q,
+                                   const void* new_k, const void* new_v, void* kv_pages, const int32_t* kv_lens,
+                                   const int32_t* page_indices, const int32_t* cu_q_lens, const int32_t* num_seqs,
+                                   const int32_t* positions, void* q_out, void* workspace, size_t workspace_bytes,
+                                   rpa_stream_t stream);
+
+/* The K and V rows of the batch's tokens as bf16 (s n + m rounded once): token j of sequence i from position
+ * kv_len - q_len + j, where the update put it; with q_len = kv_len a whole sequence.
+ *   k_out, v_out  [max_num_tokens, num_kv_heads, head_dim] bf16, dense; rows of tokens that are skipped (bad
+ *                 metadata, or past cu_q_lens[num_seqs]) are not written
+ * `workspace` is optional, as for the update.  num_q_heads is num_kv_heads or any multiple. */
+RPA_API int rpa_g4_read_kv_cache(const rpa_params* p, const void* kv_pages, const int32_t* kv_lens,
+                                 const int32_t* page_indices, const int32_t* cu_q_lens, const int32_t* num_seqs, void* k_out,
+                                 void* v_out, void* workspace, size_t workspace_bytes, rpa_stream_t stream);
+
+/* rpa_forward over such a cache: the same arguments, masks and options (sliding_window, soft_cap, batch_kind).
+ * `workspace`: rpa_g4_workspace_size bytes.  Sequences of more than 16 query rows a KV head see K and V rounded to
+ * bf16. */
+RPA_API int rpa_g4_workspace_size(const rpa_params* p, size_t* bytes);
+RPA_API int rpa_g4_forward(const rpa_params* p, const void* q, const void* kv_pages, const int32_t* kv_lens,
+                           const int32_t* page_indices, const int32_t* cu_q_lens, const int32_t* num_seqs, void* out,
+                           void* workspace, size_t workspace_bytes, rpa_stream_t stream);
 
 /* ---------------------------------------------------------------------- */
 /* MLA latent ragged paged attention                                       */

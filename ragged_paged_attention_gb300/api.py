@@ -20,7 +20,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "librpa_gb300.so")
 ABI_VERSION = 1
 
-BF16, FP8_E4M3, F32, INT8, INT4 = 1, 2, 3, 4, 5
+BF16, FP8_E4M3, F32, INT8, INT4, G4 = 1, 2, 3, 4, 5, 6
 
 STATUS = {0: "RPA_OK", -1: "RPA_ERR_NULL", -2: "RPA_ERR_SHAPE", -3: "RPA_ERR_DTYPE", -4: "RPA_ERR_VALUE",
           -5: "RPA_ERR_UNSUPPORTED", -6: "RPA_ERR_CUDA", -7: "RPA_ERR_DEVICE_CHECK", -8: "RPA_ERR_WORKSPACE"}
@@ -31,7 +31,8 @@ EXPORTS = ("rpa_workspace_size", "rpa_forward", "rpa_update_kv_cache", "mla_work
            "rpa_profile_reset", "rpa_profile_read", "rpa_forward_noalloc", "rpa_launch_count",
            "rpa_forward_update", "sparse_mla_ragged_workspace_size", "sparse_mla_write_and_attend_ragged",
            "rpa_selftest_bounded_wait", "rope_table_init", "rope_apply", "rpa_rope_update_kv_cache",
-           "rpa_rope_forward_update", "rpa_cross_workspace_size", "rpa_cross_forward")
+           "rpa_rope_forward_update", "rpa_cross_workspace_size", "rpa_cross_forward", "rpa_g4_update_kv_cache",
+           "rpa_g4_read_kv_cache", "rpa_g4_workspace_size", "rpa_g4_forward")
 
 
 class RpaError(RuntimeError):
@@ -156,6 +157,10 @@ def load_library(path: str = LIB_PATH):
                                                 ctypes.POINTER(rope_strides)] + [P] * 12 + [sz, P]
         lib.rpa_cross_workspace_size.argtypes = [ctypes.POINTER(rpa_params), szp]
         lib.rpa_cross_forward.argtypes = [ctypes.POINTER(rpa_params), P, P, P, P, P, P, P, P, sz, P]
+        lib.rpa_g4_update_kv_cache.argtypes = lib.rpa_rope_update_kv_cache.argtypes
+        lib.rpa_g4_read_kv_cache.argtypes = [ctypes.POINTER(rpa_params)] + [P] * 8 + [sz, P]
+        lib.rpa_g4_workspace_size.argtypes = [ctypes.POINTER(rpa_params), szp]
+        lib.rpa_g4_forward.argtypes = lib.rpa_cross_forward.argtypes
         lib.rpa_check_device_status.argtypes = [P, ctypes.POINTER(ctypes.c_uint32), P]
         lib.rpa_selftest_bounded_wait.argtypes = [P, sz, P]
         lib.rpa_profile_enable.argtypes = [ctypes.c_int]
@@ -540,17 +545,34 @@ def rope_apply(q, k, positions, table, *, inverse=False, q_out=None, k_out=None)
     return q_out, k_out
 
 
+_G4_ROWS = {64: 80, 128: 144, 256: 288}  # head_dim: bytes of a 4-bit cache's row
+_G4_DIMS = {v: k for k, v in _G4_ROWS.items()}
+
+
+def g4_row_bytes(head_dim: int) -> int:
+    """Bytes of a 4-bit cache's row (``RPA_G4_ROW_BYTES``): the cache is a uint8 tensor [pages, page_size, num_kv_heads,
+    row_bytes]."""
+    if head_dim not in _G4_ROWS:
+        raise ValueError(f"4-bit caches take head_dim 64, 128 or 256, got {head_dim}")
+    return _G4_ROWS[head_dim]
+
+
 def _batch_params(dev, tokens, hq, d, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, sm_scale=1.0, sliding_window=None,
-                  soft_cap=None, mask_value=None, k_scale=None, v_scale=None, batch_kind=BATCH_MIXED) -> rpa_params:
+                  soft_cap=None, mask_value=None, k_scale=None, v_scale=None, batch_kind=BATCH_MIXED, g4=False) -> rpa_params:
     """rpa_params of a batch of ``tokens`` queries of ``hq`` heads, its cache and metadata checked."""
     if not isinstance(kv_pages, torch.Tensor) or kv_pages.get_device() != dev or kv_pages.dim() != 4:
         raise ValueError(f"kv_pages must be [pages, page_size, heads, head_dim] on device {dev}")
     if not kv_pages.is_contiguous():
         raise ValueError("kv_pages must be contiguous")
-    code = _kv_code(kv_pages.dtype)
     pages, ps, combined, width = kv_pages.shape
-    if (width * 2 if code == INT4 else width) != d:
-        raise ValueError(f"kv_pages hold heads of {kv_head_dim(kv_pages)}, the rows {d}")
+    if g4:
+        code, combined = G4, 2 * combined
+        if kv_pages.dtype is not torch.uint8 or _G4_DIMS.get(width) != d:
+            raise ValueError(f"kv_pages must be a uint8 cache of rows of {g4_row_bytes(d)} bytes, got {kv_pages.dtype} rows of {width}")
+    else:
+        code = _kv_code(kv_pages.dtype)
+        if (width * 2 if code == INT4 else width) != d:
+            raise ValueError(f"kv_pages hold heads of {kv_head_dim(kv_pages)}, the rows {d}")
     _on(dev, page_indices, "page_indices", _I32)
     if page_indices.dim() != 2:
         raise ValueError("page_indices must be [max_num_seqs, pages_per_seq]")
@@ -669,6 +691,117 @@ def rpa_rope_forward_update(q, new_k, new_v, kv_pages, kv_lens, page_indices, cu
         kv_pages.data_ptr(), kv_lens.data_ptr(), page_indices.data_ptr(), cu_q_lens.data_ptr(), num_seqs.data_ptr(),
         None if positions is None else positions.data_ptr(), q_rot.data_ptr(), out.data_ptr(), workspace.data_ptr(),
         workspace.numel(), stream)
+    if rc:
+        _check(rc)
+    return out
+
+
+def rpa_g4_update_kv_cache(q, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, table, *,
+                           positions=None, q_out=None, workspace=None):
+    """``rpa_rope_update_kv_cache`` into a 4-bit cache (uint8 [pages, page_size, Hkv, g4_row_bytes(D)]): K is turned, both
+    are rounded to bf16 and held as s n + m, n in 0..15, with s and m for each group of 64 elements (32 at D = 64).
+    Returns ``(q_out, kv_pages)``."""
+    lib = _lib or load_library()
+    dev = _cuda_index(new_k, "new_k")
+    if dev != _current():
+        with torch.cuda.device(dev):
+            return rpa_g4_update_kv_cache(q, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, table,
+                                          positions=positions, q_out=q_out, workspace=workspace)
+    prm, st, q_out = _rope_update_args(dev, q, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, table,
+                                       positions, q_out, g4=True)
+    if workspace is not None:
+        _on(dev, workspace, "workspace", torch.uint8)
+    if prm.max_num_tokens == 0:
+        return q_out, kv_pages
+    rc = lib.rpa_g4_update_kv_cache(
+        ctypes.byref(prm), ctypes.byref(table), ctypes.byref(st), None if q is None else q.data_ptr(), new_k.data_ptr(),
+        new_v.data_ptr(), kv_pages.data_ptr(), kv_lens.data_ptr(), page_indices.data_ptr(), cu_q_lens.data_ptr(),
+        num_seqs.data_ptr(), None if positions is None else positions.data_ptr(), None if q is None else q_out.data_ptr(),
+        None if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.numel(), _raw_stream(dev))
+    if rc:
+        _check(rc)
+    return q_out, kv_pages
+
+
+def rpa_g4_read_kv_cache(kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, num_tokens=None, *, k_out=None, v_out=None,
+                         workspace=None):
+    """The rows that ``rpa_g4_update_kv_cache`` wrote for the batch's tokens, as bf16: returns ``(k, v)``
+    [num_tokens, Hkv, D] (``num_tokens``, the batch's padded count, is k_out's where that is given).  With ``cu_q_lens`` of
+    the whole sequences it reads them whole."""
+    lib = _lib or load_library()
+    dev = _cuda_index(kv_pages, "kv_pages")
+    if dev != _current():
+        with torch.cuda.device(dev):
+            return rpa_g4_read_kv_cache(kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, num_tokens, k_out=k_out,
+                                        v_out=v_out, workspace=workspace)
+    d = _G4_DIMS.get(kv_pages.shape[-1]) if kv_pages.dim() == 4 else None
+    if d is None:
+        raise ValueError(f"kv_pages must be [pages, page_size, heads, row_bytes] of a 4-bit cache, got {tuple(kv_pages.shape)}")
+    if num_tokens is None:
+        if k_out is None:
+            raise ValueError("num_tokens or k_out must be given")
+        num_tokens = k_out.shape[0]
+    shape = (num_tokens, kv_pages.shape[2], d)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=kv_pages.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=kv_pages.device)
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        _on(dev, t, name, _BF16)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+    prm = _batch_params(dev, num_tokens, shape[1], d, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, g4=True)
+    if workspace is not None:
+        _on(dev, workspace, "workspace", torch.uint8)
+    if num_tokens == 0:
+        return k_out, v_out
+    rc = lib.rpa_g4_read_kv_cache(ctypes.byref(prm), kv_pages.data_ptr(), kv_lens.data_ptr(), page_indices.data_ptr(),
+                                  cu_q_lens.data_ptr(), num_seqs.data_ptr(), k_out.data_ptr(), v_out.data_ptr(),
+                                  None if workspace is None else workspace.data_ptr(),
+                                  0 if workspace is None else workspace.numel(), _raw_stream(dev))
+    if rc:
+        _check(rc)
+    return k_out, v_out
+
+
+def make_g4_params(q, kv_pages, page_indices, *, sm_scale=1.0, sliding_window=None, soft_cap=None,
+                   batch_kind=BATCH_MIXED) -> rpa_params:
+    """rpa_params of a call over a 4-bit cache (for ``rpa_g4_workspace_size``)."""
+    pages, ps, hkv, _ = kv_pages.shape
+    seqs, pps = page_indices.shape
+    return rpa_params(_PARAMS_SIZE, ABI_VERSION, q.shape[0], q.shape[1], 2 * hkv, q.shape[2], pages, ps, seqs, pps, BF16, G4,
+                      sm_scale, sliding_window or 0, soft_cap or 0.0, math.nan, 0.0, 0.0, batch_kind)
+
+
+def rpa_g4_workspace_size(params: rpa_params) -> int:
+    lib = load_library()
+    n = ctypes.c_size_t(0)
+    _check(lib.rpa_g4_workspace_size(ctypes.byref(params), ctypes.byref(n)))
+    return n.value
+
+
+def rpa_g4_forward(q, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, *, sm_scale=1.0, sliding_window=None,
+                   soft_cap=None, out=None, workspace=None, batch_kind=BATCH_MIXED):
+    """``rpa_forward`` over a 4-bit cache (uint8 [pages, page_size, Hkv, g4_row_bytes(D)]); returns ``out`` [T, Hq, D] bf16."""
+    lib = _lib or load_library()
+    dev = _cuda_index(q, "q")
+    if dev != _current():
+        with torch.cuda.device(dev):
+            return rpa_g4_forward(q, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, sm_scale=sm_scale,
+                                  sliding_window=sliding_window, soft_cap=soft_cap, out=out, workspace=workspace,
+                                  batch_kind=batch_kind)
+    _on(dev, q, "q", torch.bfloat16)
+    if q.dim() != 3:
+        raise ValueError(f"q must be [tokens, heads, head_dim], got {tuple(q.shape)}")
+    T, hq, d = q.shape
+    prm = _batch_params(dev, T, hq, d, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, sm_scale, sliding_window, soft_cap,
+                        batch_kind=batch_kind, g4=True)
+    out, workspace, stream = _attention_buffers(dev, lib.rpa_g4_workspace_size, prm, q, out, workspace)
+    if T == 0:
+        return out
+    rc = lib.rpa_g4_forward(ctypes.byref(prm), q.data_ptr(), kv_pages.data_ptr(), kv_lens.data_ptr(), page_indices.data_ptr(),
+                            cu_q_lens.data_ptr(), num_seqs.data_ptr(), out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                            stream)
     if rc:
         _check(rc)
     return out

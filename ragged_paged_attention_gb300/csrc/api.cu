@@ -66,7 +66,7 @@ struct RpaLayout {
     int max_dec, max_pre;
 };
 
-int check_rpa_params(const rpa_params* p) {
+int check_rpa_params(const rpa_params* p, bool g4 = false) {
     if (!p) return fail(RPA_ERR_NULL, "params is NULL");
     if (p->struct_size < offsetof(rpa_params, batch_kind)) return fail(RPA_ERR_VALUE, "rpa_params.struct_size too small");
     if (rpa_batch_kind(p) < RPA_BATCH_MIXED || rpa_batch_kind(p) > RPA_BATCH_PREFILL_ONLY)
@@ -81,7 +81,13 @@ int check_rpa_params(const rpa_params* p) {
     if (p->head_dim != 64 && p->head_dim != 96 && p->head_dim != 128 && p->head_dim != 192 && p->head_dim != 256)
         return fail(RPA_ERR_UNSUPPORTED, "head_dim %d (supported: 64, 96, 128, 192, 256)", p->head_dim);
     if (p->q_dtype != RPA_DTYPE_BF16) return fail(RPA_ERR_DTYPE, "q_dtype must be bf16");
-    if (p->kv_dtype != RPA_DTYPE_BF16 && p->kv_dtype != RPA_DTYPE_FP8_E4M3 && p->kv_dtype != RPA_DTYPE_INT8 &&
+    if (g4) {
+        if (p->kv_dtype != RPA_DTYPE_G4) return fail(RPA_ERR_DTYPE, "kv_dtype must be RPA_DTYPE_G4");
+        if (p->head_dim != 64 && p->head_dim != 128 && p->head_dim != 256)
+            return fail(RPA_ERR_UNSUPPORTED, "4-bit caches take head_dim 64, 128 or 256 (got %d)", p->head_dim);
+        if (p->k_scale != 0.f || p->v_scale != 0.f) return fail(RPA_ERR_VALUE, "4-bit caches hold their own scales: k_scale and v_scale must be 0");
+        if (!isnan(p->mask_value)) return fail(RPA_ERR_VALUE, "4-bit caches: mask_value must be NaN");
+    } else if (p->kv_dtype != RPA_DTYPE_BF16 && p->kv_dtype != RPA_DTYPE_FP8_E4M3 && p->kv_dtype != RPA_DTYPE_INT8 &&
         p->kv_dtype != RPA_DTYPE_INT4)
         return fail(RPA_ERR_DTYPE, "kv_dtype must be bf16, fp8 e4m3, int8 or int4");
     if (!isfinite(p->sm_scale)) return fail(RPA_ERR_VALUE, "sm_scale must be finite");
@@ -373,8 +379,8 @@ int rpa_workspace_size(const rpa_params* p, size_t* bytes) {
 // Validates an rpa_forward call and fills the kernels' argument block.
 static int rpa_prepare(const rpa_params* p, const void* q, const void* kv_pages, const int32_t* kv_lens,
                        const int32_t* page_indices, const int32_t* cu_q_lens, const int32_t* num_seqs, void* out,
-                       void* workspace, size_t workspace_bytes, RpaArgs& a, int& sms) {
-    int rc = check_rpa_params(p);
+                       void* workspace, size_t workspace_bytes, RpaArgs& a, int& sms, bool g4 = false) {
+    int rc = check_rpa_params(p, g4);
     if (rc) return rc;
     if (!q || !kv_pages || !kv_lens || !page_indices || !cu_q_lens || !num_seqs || !out)
         return fail(RPA_ERR_NULL, "a tensor pointer is NULL");
@@ -431,9 +437,15 @@ static int rpa_prepare(const rpa_params* p, const void* q, const void* kv_pages,
     rpa_rates(p->head_dim, a.kv_byte != 0, a.has_scale != 0,
               rpa_pow2_scale(a.k_scale_or_one) && rpa_pow2_scale(a.v_scale_or_one), &a.pre_flops_per_ns_sm,
               &a.dec_bytes_per_ns_sm);
+    a.dec_hbm_bytes_per_ns = kDecHbmBytesPerNs;
     a.item_cost_keys = rpa_item_cost_keys(a.kv_byte || a.has_scale);
     a.min_chunk = kMinChunk;
-    a.decode_per_sm = rpa_decode_ctas_per_sm(a);
+    a.prefill_rows = kPrefillRows;
+    if (g4) {
+        a.prefill_rows = g4_prefill_rows(p->head_dim);
+        g4_rates(p->head_dim, &a.pre_flops_per_ns_sm, &a.dec_bytes_per_ns_sm, &a.dec_hbm_bytes_per_ns);
+    }
+    a.decode_per_sm = g4 ? g4_decode_ctas_per_sm(a) : rpa_decode_ctas_per_sm(a);
     if (a.decode_per_sm <= 0) return fail(RPA_ERR_CUDA, "decode kernel occupancy query failed");
     a.hdr = reinterpret_cast<WsHeader*>(ws);
     a.dec_items = reinterpret_cast<WorkItem*>(ws + L.items_dec);
@@ -632,8 +644,8 @@ int rope_apply(const rope_apply_params* p, const rope_table* t, const void* q, c
 static int rope_update_prepare(const rpa_params* p, const rope_table* t, const rope_strides* st, const void* q,
                                const void* new_k, const void* new_v, void* kv_pages, const int32_t* kv_lens,
                                const int32_t* page_indices, const int32_t* cu_q_lens, const int32_t* num_seqs,
-                               const int32_t* positions, void* q_out, uint32_t* err, RopeUpdateArgs& a) {
-    int rc = check_rpa_params(p);
+                               const int32_t* positions, void* q_out, uint32_t* err, RopeUpdateArgs& a, bool g4 = false) {
+    int rc = check_rpa_params(p, g4);
     if (!rc) rc = check_rope_table(t);
     if (rc) return rc;
     if (st && st->struct_size < sizeof(rope_strides)) return fail(RPA_ERR_VALUE, "rope_strides.struct_size too small");
@@ -643,6 +655,8 @@ static int rope_update_prepare(const rpa_params* p, const rope_table* t, const r
     if ((q != nullptr) != (q_out != nullptr)) return fail(RPA_ERR_NULL, "q and q_out go together");
     if (!aligned16(kv_pages)) return fail(RPA_ERR_VALUE, "kv_pages must be 16-byte aligned");
     if (t->rotary_dim > p->head_dim) return fail(RPA_ERR_SHAPE, "rotary_dim %d exceeds head_dim %d", t->rotary_dim, p->head_dim);
+    if (g4 && t->rotary_dim % 16)
+        return fail(RPA_ERR_UNSUPPORTED, "4-bit caches take a rotary_dim that is a multiple of 16 (got %d)", t->rotary_dim);
     if (p->kv_dtype == RPA_DTYPE_INT4 && t->rotary_dim % 4)
         return fail(RPA_ERR_UNSUPPORTED, "int4 caches take a rotary_dim that is a multiple of 4 (got %d)", t->rotary_dim);
     memset(&a, 0, sizeof a);
@@ -674,7 +688,7 @@ static int rope_update_prepare(const rpa_params* p, const rope_table* t, const r
     a.positions = positions;
     a.err = err;
     a.kv_dtype = p->kv_dtype;
-    a.row_bytes = p->kv_dtype == RPA_DTYPE_BF16 ? d * 2 : p->kv_dtype == RPA_DTYPE_INT4 ? d / 2 : d;
+    a.row_bytes = g4 ? RPA_G4_ROW_BYTES(d) / 2 : p->kv_dtype == RPA_DTYPE_BF16 ? d * 2 : p->kv_dtype == RPA_DTYPE_INT4 ? d / 2 : d;
     a.max_num_tokens = T;
     a.num_q_heads = hq;
     a.num_kv_heads = hkv;
@@ -729,6 +743,83 @@ int rpa_rope_forward_update(const rpa_params* p, const rope_table* t, const rope
     cudaError_t e = launch_rope_update(u, sms, reinterpret_cast<cudaStream_t>(stream));
     if (e == cudaSuccess) e = launch_rpa_forward(a, sms, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "rpa_rope_forward_update launch");
+    return RPA_OK;
+}
+
+int rpa_g4_update_kv_cache(const rpa_params* p, const rope_table* t, const rope_strides* strides, const void* q,
+                           const void* new_k, const void* new_v, void* kv_pages, const int32_t* kv_lens,
+                           const int32_t* page_indices, const int32_t* cu_q_lens, const int32_t* num_seqs,
+                           const int32_t* positions, void* q_out, void* workspace, size_t workspace_bytes,
+                           rpa_stream_t stream) {
+    int rc = check_status_workspace(workspace, workspace_bytes);
+    if (rc) return rc;
+    RopeUpdateArgs a;
+    rc = rope_update_prepare(p, t, strides, q, new_k, new_v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, positions,
+                             q_out, workspace ? &reinterpret_cast<WsHeader*>(workspace)->error_bits : nullptr, a, true);
+    if (rc) return rc;
+    const int sms = num_sms_current();
+    if (!sms) return fail(RPA_ERR_CUDA, "no CUDA device");
+    cudaError_t e = launch_rope_update(a, sms, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "rpa_g4_update_kv_cache launch");
+    return RPA_OK;
+}
+
+int rpa_g4_read_kv_cache(const rpa_params* p, const void* kv_pages, const int32_t* kv_lens, const int32_t* page_indices,
+                         const int32_t* cu_q_lens, const int32_t* num_seqs, void* k_out, void* v_out, void* workspace,
+                         size_t workspace_bytes, rpa_stream_t stream) {
+    int rc = check_rpa_params(p, true);
+    if (!rc) rc = check_status_workspace(workspace, workspace_bytes);
+    if (rc) return rc;
+    if (!kv_pages || !kv_lens || !page_indices || !cu_q_lens || !num_seqs || !k_out || !v_out)
+        return fail(RPA_ERR_NULL, "a tensor pointer is NULL");
+    if (!aligned16(kv_pages) || !aligned16(k_out) || !aligned16(v_out))
+        return fail(RPA_ERR_VALUE, "kv_pages, k_out and v_out must be 16-byte aligned");
+    if (k_out == v_out || k_out == kv_pages || v_out == kv_pages) return fail(RPA_ERR_VALUE, "k_out, v_out and kv_pages must not alias");
+    const int sms = num_sms_current();
+    if (!sms) return fail(RPA_ERR_CUDA, "no CUDA device");
+    RopeUpdateArgs a;
+    memset(&a, 0, sizeof a);
+    a.kv_pages = const_cast<void*>(kv_pages);  // (read only)
+    a.kv_lens = kv_lens;
+    a.page_indices = page_indices;
+    a.cu_q_lens = cu_q_lens;
+    a.num_seqs = num_seqs;
+    a.err = workspace ? &reinterpret_cast<WsHeader*>(workspace)->error_bits : nullptr;
+    a.row_bytes = RPA_G4_ROW_BYTES(p->head_dim) / 2;
+    a.max_num_tokens = p->max_num_tokens;
+    a.num_kv_heads = p->num_combined_kv_heads / 2;
+    a.head_dim = p->head_dim;
+    a.total_num_pages = p->total_num_pages;
+    a.page_size = p->page_size;
+    a.max_num_seqs = p->max_num_seqs;
+    a.pages_per_seq = p->pages_per_seq;
+    cudaError_t e = launch_g4_read(a, static_cast<__nv_bfloat16*>(k_out), static_cast<__nv_bfloat16*>(v_out), sms,
+                                   reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "rpa_g4_read_kv_cache launch");
+    return RPA_OK;
+}
+
+int rpa_g4_workspace_size(const rpa_params* p, size_t* bytes) {
+    const int rc = check_rpa_params(p, true);
+    if (rc) return rc;
+    if (!bytes) return fail(RPA_ERR_NULL, "bytes is NULL");
+    *bytes = rpa_layout(p).total;
+    return RPA_OK;
+}
+
+int rpa_g4_forward(const rpa_params* p, const void* q, const void* kv_pages, const int32_t* kv_lens, const int32_t* page_indices,
+                   const int32_t* cu_q_lens, const int32_t* num_seqs, void* out, void* workspace, size_t workspace_bytes,
+                   rpa_stream_t stream) {
+    RpaArgs a;
+    int sms = 0;
+    const int rc = rpa_prepare(p, q, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, out, workspace, workspace_bytes, a, sms, true);
+    if (rc) return rc;
+    // so few query rows that every sequence is decode-class: the prefill launches are left out
+    if (a.batch_kind == RPA_BATCH_MIXED && (long long)p->max_num_tokens * (a.num_q_heads / a.num_kv_heads) <= 16)
+        a.batch_kind = RPA_BATCH_DECODE_ONLY;
+    a.min_chunk = kStepMinChunk + a.item_cost_keys;
+    cudaError_t e = launch_g4_forward(a, sms, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "rpa_g4_forward launch");
     return RPA_OK;
 }
 

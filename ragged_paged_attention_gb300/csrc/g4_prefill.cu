@@ -1,0 +1,603 @@
+// Prefill-class attention over the 4-bit cache (rpa_g4_forward: sequences of more than 16 query rows a KV head) on the
+// 5th-generation tensor cores of sm_103a.
+//
+//   S = Q K^T, P = 2^(c S - m), O += P V, l += sum P, out = O / l, K = s n + m and V = s n + m rounded to bf16.
+//
+// Tiles of 128 rows (token, q head of the group; a row a thread), blocks of 128 keys (64 at head_dim 256). Four warps
+// turn the 4-bit rows into the bf16 panels that the products read: a thread a row, which it has brought to shared
+// memory itself by cp.async (any page size, no barrier on the way), 8 numbers in some 20 instructions (a permute and a
+// mask put two numbers into the halves as 128 + n, one subtraction and one fused multiply-add give both values, the
+// latter rounding once). Two tiles of a KV head (head_dim 64 and 128) share each converted block, and while
+// one's softmax runs the tensor pipe works for the other; at head_dim 256 tensor memory holds one tile.
+// The rounding of K and V to bf16 (2^-9 of a value) is what a bf16 cache has too.
+// Warps: 4 softmax warps a tile; an MMA issuer a tile; one that takes items and loads Q; one idle; 4 converters.
+// Barriers, all waits bounded: k/v_full, k/v_empty (panels), q_full, q_empty, item_full/empty; per tile s_full (QK
+// done), s_free (scores loaded), p_full (P written, O rescaled), pv_done, o_empty.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <type_traits>
+
+#include "common.cuh"
+#include "g4.cuh"
+#include "kernels.h"
+#include "profile.h"
+
+namespace rpa {
+
+struct __align__(16) G4Item {
+    int seq, head, row, q_start, q_len, kv_len, block0, blocks;
+};
+
+template <int D>
+struct G4Pre {
+    static constexpr int TILES = D == 256 ? 1 : 2;
+    static constexpr int BK = D == 256 ? 64 : 128;
+    static constexpr int DP = D / 64;                      // 64-wide panels
+    static constexpr int kQPanel = 128 * 128, kQTile = DP * kQPanel;
+    static constexpr int kPanel = BK * 128, kTile = DP * kPanel;
+    static constexpr bool ONE_S = D == 128;                // the two tiles take turns with one S buffer
+    static constexpr int NK = 2, NV = D == 64 ? 2 : 1;
+    static constexpr int NR = 3;                           // raw blocks on their way
+    static constexpr int kRaw = BK * G4<D>::kRow;
+    static constexpr int kOffK = TILES * kQTile;
+    static constexpr int kOffV = kOffK + NK * kTile;
+    static constexpr int kOffRaw = kOffV + NV * kTile;
+    static constexpr int kOffBar = kOffRaw + NR * kRaw;
+    static constexpr int kBars = 2 * (NK + NV) + 7 + 5 * TILES;
+    static constexpr int kOffItem = (kOffBar + kBars * 8 + 15) / 16 * 16;  // [2] G4Item, abort, TMEM base, exit
+    static constexpr int kSmem = kOffItem + 2 * (int)sizeof(G4Item) + 16;
+    static constexpr int kSoft = 4 * TILES;
+    static constexpr int kThreads = (kSoft + 8) * 32;
+    static constexpr int kColS = 0, kColSStep = ONE_S ? 0 : BK;
+    static constexpr int kColP = ONE_S ? BK : TILES * BK, kColO = kColP + TILES * (BK / 2);
+    static constexpr int kTmemCols = 512;
+    // registers: the launch's share of the SM, dealt out again by warpgroup (setmaxnreg)
+    static constexpr int kRegsLaunch = TILES == 2 ? 128 : 168;
+    static constexpr int kRegsSoft = 192, kRegsRest = 64;
+    static_assert(TILES == 1 || 256 * kRegsSoft + 256 * kRegsRest <= kThreads * kRegsLaunch, "register split");
+    static_assert(kSmem <= 232448 && kOffK % 1024 == 0 && kOffV % 1024 == 0 && kOffRaw % 16 == 0 && kOffBar % 8 == 0, "shared memory");
+    static_assert(kColO + TILES * D <= kTmemCols, "tensor memory");
+};
+
+template <int R>
+__device__ __forceinline__ void g4_regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R>
+__device__ __forceinline__ void g4_regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+
+// 8 numbers of a word -> 8 bf16 of s n + m, in order: byte i's two numbers to the low bits of two halves, which are then
+// 128 + n; the difference is exact and the fused multiply-add rounds once.
+__device__ __forceinline__ uint4 g4_panel8(uint32_t w, uint32_t s2, uint32_t m2) {
+    const uint32_t h = w >> 4;
+    uint32_t r[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        uint32_t t = __byte_perm(w, h, e | (e << 4) | ((4 + e) << 8) | ((4 + e) << 12));
+        t = (t & 0x000f000fu) | 0x43004300u;
+        asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(t) : "r"(0x43004300u));
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r[e]) : "r"(t), "r"(s2), "r"(m2));
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+template <int D>
+__global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
+    g4_prefill_kernel(const __grid_constant__ RpaArgs a, const __grid_constant__ CUtensorMap tm_q, int q_tma, int tail) {
+    using T = G4Pre<D>;
+    using F = G4<D>;
+    constexpr int BK = T::BK, NK = T::NK, NV = T::NV, TILES = T::TILES, NR = T::NR;
+    // first launch (tail == 0): started early behind the plan, it waits for it, then lets the decode grid behind
+    // start; only the plan's share of its CTAs works. Either launch leaves at once when the list is empty.
+    if (!tail) {
+        pdl_wait();
+        pdl_launch_dependents();
+    }
+    extern __shared__ __align__(1024) uint8_t smem[];
+    volatile int* flags = reinterpret_cast<volatile int*>(smem + T::kOffItem + 2 * sizeof(G4Item));
+    volatile int& s_abort = flags[0];
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + T::kOffItem + 2 * sizeof(G4Item) + 4);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    WsHeader* hdr = a.hdr;
+    if (tid == 0)  // one decision for the whole CTA
+        flags[2] = (!tail && (int)blockIdx.x >= hdr->prefill_ctas) || *(volatile const int*)&hdr->next_item[1] >= hdr->num_items[1];
+    __syncthreads();
+    if (flags[2]) return;
+    uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + T::kOffBar);
+    uint64_t* k_empty = k_full + NK;
+    uint64_t* v_full = k_empty + NK;
+    uint64_t* v_empty = v_full + NV;
+    uint64_t* q_full = v_empty + NV;
+    uint64_t* q_empty = q_full + 1;
+    uint64_t* item_full = q_full + 2;   // [2]
+    uint64_t* item_empty = q_full + 4;  // [2]
+    uint64_t* fin = q_full + 6;         // every product has completed
+    uint64_t* s_full = q_full + 7;      // [TILES] each
+    uint64_t* s_free = s_full + TILES;
+    uint64_t* o_empty = s_full + 2 * TILES;
+    uint64_t* p_full = s_full + 3 * TILES;
+    uint64_t* pv_done = s_full + 4 * TILES;
+    G4Item* s_items = reinterpret_cast<G4Item*>(smem + T::kOffItem);
+    uint32_t* err = &hdr->error_bits;
+    const int G = a.num_q_heads / a.num_kv_heads;
+    constexpr int kMma0 = T::kSoft, kQw = T::kSoft + 2, kConv0 = T::kSoft + 4;
+
+    if (tid == 0) {
+        for (int i = 0; i < NK; ++i) {
+            mbar_init(&k_full[i], 4);
+            mbar_init(&k_empty[i], TILES);
+        }
+        for (int i = 0; i < NV; ++i) {
+            mbar_init(&v_full[i], 4);
+            mbar_init(&v_empty[i], TILES);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, TILES);
+        mbar_init(fin, TILES);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&item_full[i], 1);
+            mbar_init(&item_empty[i], T::kThreads / 32);
+        }
+        for (int t = 0; t < TILES; ++t) {
+            mbar_init(&s_full[t], 1);
+            mbar_init(&s_free[t], 4);
+            mbar_init(&p_full[t], 4);
+            mbar_init(&o_empty[t], 4);
+            mbar_init(&pv_done[t], 1);
+        }
+        s_abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMma0) tmem_alloc(tmem_slot, T::kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    uint32_t items = 0;  // items this CTA has taken (ring slots, q phases)
+    auto next_item_of = [&](G4Item& it, auto alone) -> bool {
+        constexpr bool kAlone = decltype(alone)::value;
+        const uint32_t slot = items & 1, ph = (items >> 1) & 1;
+        it.seq = -1;
+        if (mbar_wait(&item_full[slot], ph, err)) it = s_items[slot];
+        if (!kAlone) __syncwarp();
+        if (kAlone || lane == 0) mbar_arrive(&item_empty[slot]);
+        if (it.seq < 0 || s_abort) return false;
+        ++items;
+        return true;
+    };
+    auto next_item = [&](G4Item& it) { return next_item_of(it, std::false_type()); };
+
+    G4Item it;
+    if (warp < T::kSoft) {
+        // ---------------- softmax and epilogue: thread = row of its tile ----------------
+        if constexpr (TILES == 2) g4_regs_inc<T::kRegsSoft>();
+        const int t = warp >> 2, quarter = warp & 3;
+        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+        const uint32_t col_s = tmem + lane_off + T::kColS + t * T::kColSStep, col_p = tmem + lane_off + T::kColP + t * (BK / 2),
+                       col_o = tmem + lane_off + T::kColO + t * D;
+        const float cap = a.soft_cap, cap_k2 = cap != 0.f ? 2.f * kLog2e / cap : 0.f, c_log2 = a.sm_scale * kLog2e;
+        // without a soft cap (and with a positive scale) the maximum is taken on the raw scores and the scale goes into
+        // the exponent's multiply-add
+        const bool fold = cap == 0.f && c_log2 > 0.f;
+        const float cs = fold ? c_log2 : 1.f;
+        uint32_t nblk = 0;  // blocks this tile has processed
+        bool ok = true;
+        while (ok && next_item(it)) {
+            const int n_rows = it.q_len * G;
+            if (it.row + t * 128 >= n_rows) continue;  // this item has no such tile
+            const int R = it.row + t * 128 + quarter * 32 + lane;
+            const bool rv = R < n_rows;
+            // (a row that is not there sees what the first one does)
+            const int qpos = it.kv_len - it.q_len + (rv ? R : it.row) / G;
+            const int wlo = a.sliding_window > 0 ? qpos - a.sliding_window + 1 : 0;
+            float m_use = -INFINITY, l = 0.f;
+            for (int j = 0; ok && j < it.blocks; ++j, ++nblk) {
+                const uint32_t par = nblk & 1;
+                if (!mbar_wait(&s_full[t], par, err)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                float x[BK];
+#pragma unroll
+                for (int c = 0; c < BK / 32; ++c) tmem_ld32_nowait(col_s + c * 32, x + c * 32);
+                tmem_ld_wait();
+                tmem_landed<BK>(x);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_free[t]);
+                if (cap != 0.f) {
+#pragma unroll
+                    for (int i = 0; i < BK; ++i) x[i] = soft_cap(x[i] * a.sm_scale, cap, cap_k2) * kLog2e;
+                } else if (!fold) {
+#pragma unroll
+                    for (int i = 0; i < BK; ++i) x[i] *= c_log2;
+                }
+                const int lo = wlo - (it.block0 + j) * BK, hi = qpos - (it.block0 + j) * BK;  // columns [lo, hi] are seen
+                if (__any_sync(0xffffffffu, lo > 0 || hi < BK - 1)) {
+#pragma unroll
+                    for (int i = 0; i < BK; ++i) x[i] = i >= lo && i <= hi ? x[i] : -INFINITY;
+                }
+                float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int i = 0; i < BK; i += 2) mx4[(i >> 1) & 3] = fmax3(mx4[(i >> 1) & 3], x[i], x[i + 1]);
+                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * cs;  // log2 units
+                // lazy: the reference maximum moves only when it has grown by more than 2^8
+                const bool had = m_use > -INFINITY, rescale = mx > m_use + 8.f;
+                float alpha = 1.f;
+                if (rescale) {
+                    alpha = fast_exp2(m_use - mx);
+                    m_use = mx;
+                }
+                const float nmu = m_use == -INFINITY ? 0.f : -m_use;
+                const bool row_rescale = rescale && had;
+                if (__any_sync(0xffffffffu, row_rescale)) {
+                    if (!mbar_wait(&pv_done[t], par ^ 1, err)) {  // the previous block's PV has written O
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const float f = row_rescale ? alpha : 1.f;
+#pragma unroll 1
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint32_t o[16];
+                        tmem_ld16(col_o + c * 16, o);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tmem_st16_nowait(col_o + c * 16, o);
+                    }
+                }
+                float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                const float2 cs2 = make_float2(cs, cs), nmu2 = make_float2(nmu, nmu);
+                // the previous block's PV has read P
+                if (nblk > 0 && !mbar_wait(&pv_done[t], par ^ 1, err)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < BK / 32; ++c) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float2 p = ffma2(make_float2(x[c * 32 + 2 * e], x[c * 32 + 2 * e + 1]), cs2, nmu2);
+                        p.x = fast_exp2(p.x);
+                        p.y = fast_exp2(p.y);
+                        sum2[e & 1] = fadd2(sum2[e & 1], p);
+                        pk[e] = pack_bf16(p.x, p.y);
+                    }
+                    tmem_st16_nowait(col_p + c * 16, pk);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[t]);
+                l = l * alpha + ((sum2[0].x + sum2[1].x) + (sum2[0].y + sum2[1].y));
+            }
+            // epilogue: O of the last PV
+            if (ok && mbar_wait(&pv_done[t], (nblk - 1) & 1, err)) {
+                tc_fence_after();
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                __nv_bfloat16* dst = a.out + ((size_t)(it.q_start + (rv ? R / G : 0)) * a.num_q_heads + it.head * G + (rv ? R % G : 0)) * D;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[32];
+                    tmem_ld32(col_o + c * 32, o);
+                    if (rv) {
+                        uint4* d4 = reinterpret_cast<uint4*>(dst + c * 32);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            d4[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                               pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&o_empty[t]);
+            } else {
+                ok = false;
+            }
+            if (!ok) s_abort = 1;
+        }
+    } else {
+        if constexpr (TILES == 2) g4_regs_dec<T::kRegsRest>();
+        if (warp >= kMma0 && warp < kMma0 + TILES) {
+            // ---------------- MMA issuer of tile t (a constant in either branch) ----------------
+            // One lane, elected once, does all of it: the ring positions and phases are its registers, and a commit
+            // tracks the products of its own thread alone.
+            auto issue = [&](auto tile) {
+                constexpr int t = decltype(tile)::value;
+                constexpr uint32_t idesc_qk = umma_idesc_bf16(128, BK, false, false);
+                constexpr uint32_t idesc_pv = umma_idesc_bf16(128, D, false, true);
+                const uint64_t qdesc = umma_desc_sw128(smem_u32(smem + t * T::kQTile), 16, 1024);
+                const uint64_t kdesc = umma_desc_sw128(smem_u32(smem + T::kOffK), 16, 1024);
+                const uint64_t vdesc = umma_desc_sw128(smem_u32(smem + T::kOffV), T::kPanel, 1024);
+                const uint32_t col_s = tmem + T::kColS + t * T::kColSStep, col_p = tmem + T::kColP + t * (BK / 2), col_o = tmem + T::kColO + t * D;
+                uint32_t jk = 0, jv = 0;          // ring positions
+                uint32_t n_own = 0, n_other = 0;  // QKs of this tile, and of the other one before the next of these
+                uint32_t npv = 0, no = 0;         // PVs, and items this tile has had
+                bool ok = true;
+                while (ok && next_item_of(it, std::true_type())) {
+                    const int n_rows = it.q_len * G;
+                    const bool active = it.row + t * 128 < n_rows, both = TILES == 2 && it.row + 128 < n_rows;
+                    ok = mbar_wait(q_full, (items - 1) & 1, err);
+                    for (int j = 0; ok && j <= it.blocks; ++j) {
+                        if (j < it.blocks) {  // QK of block j
+                            const uint32_t slot = jk % NK;
+                            ok = mbar_wait(&k_full[slot], (jk / NK) & 1, err);
+                            ++jk;
+                            if (t == 1) ++n_other;  // in turn: tile 0's QK of a block, then tile 1's
+                            if (active) {
+                                // the scores that lie there have been read
+                                if (T::ONE_S && n_other > 0) ok = ok && mbar_wait(&s_free[TILES - 1 - t], (n_other - 1) & 1, err);
+                                if (n_own > 0) ok = ok && mbar_wait(&s_free[t], (n_own - 1) & 1, err);
+                                if (!ok) break;
+                                tc_fence_after();
+                                const uint64_t kb = kdesc + (uint64_t)((slot * T::kTile) >> 4);
+#pragma unroll
+                                for (int ks = 0; ks < D / 16; ++ks)
+                                    umma_bf16(col_s, qdesc + (((ks >> 2) * T::kQPanel + (ks & 3) * 32) >> 4),
+                                              kb + (((ks >> 2) * T::kPanel + (ks & 3) * 32) >> 4), idesc_qk, ks > 0 ? 1u : 0u);
+                                umma_commit(&s_full[t]);
+                                umma_commit(&k_empty[slot]);
+                                if (!T::ONE_S && j + 1 == it.blocks) umma_commit(q_empty);
+                                ++n_own;
+                            } else {
+                                if (!ok) break;
+                                mbar_arrive(&k_empty[slot]);
+                                if (j + 1 == it.blocks) mbar_arrive(q_empty);
+                            }
+                            if (t == 0 && both) ++n_other;
+                        }
+                        if (T::ONE_S && active && j == it.blocks) {
+                            // With S shared, Q is free once the last scores have been loaded too: the issuer that has
+                            // no tile of this item follows none of the loads, and its wait for the next item's
+                            // would pass at an older phase.
+                            ok = mbar_wait(&s_free[t], (n_own - 1) & 1, err);
+                            if (!ok) break;
+                            mbar_arrive(q_empty);
+                        }
+                        if (j > 0) {  // PV of block j - 1
+                            const uint32_t slot = jv % NV;
+                            ok = mbar_wait(&v_full[slot], (jv / NV) & 1, err);
+                            ++jv;
+                            if (active) {
+                                if (j == 1 && no > 0) ok = ok && mbar_wait(&o_empty[t], (no - 1) & 1, err);
+                                const uint64_t vb = vdesc + (uint64_t)((slot * T::kTile) >> 4);
+                                ok = ok && mbar_wait(&p_full[t], npv & 1, err);
+                                if (!ok) break;
+                                tc_fence_after();
+#pragma unroll
+                                for (int kk = 0; kk < BK / 16; ++kk)
+                                    umma_bf16_ta(col_o, col_p + kk * 8, vb + ((kk * 16 * 128) >> 4), idesc_pv, (j > 1 || kk > 0) ? 1u : 0u);
+                                umma_commit(&pv_done[t]);
+                                umma_commit(&v_empty[slot]);
+                                ++npv;
+                            } else {
+                                if (!ok) break;
+                                mbar_arrive(&v_empty[slot]);
+                            }
+                        }
+                    }
+                    if (active) ++no;
+                    if (!ok) s_abort = 1;
+                }
+                // the products (and the arrivals committed behind them) end before shared memory goes
+                umma_commit(fin);
+                mbar_wait(fin, 0, err);
+            };
+            if (elect_one()) {
+                if (warp == kMma0)
+                    issue(std::integral_constant<int, 0>());
+                else
+                    issue(std::integral_constant<int, TILES - 1>());
+            }
+            __syncwarp();
+        } else if (warp == kQw) {
+            // ---------------- items and Q ----------------
+            const int n_items = hdr->num_items[1];
+            uint32_t fetched = 0;
+            auto fetch = [&]() {
+                const uint32_t slot = fetched & 1, ph = (fetched >> 1) & 1;
+                G4Item n;
+                n.seq = -1;
+                if (!mbar_wait(&item_empty[slot], ph ^ 1, err)) s_abort = 1;
+                // beside decode, no new item once most decode CTAs with a share are out of work: what is left goes to
+                // the launch after decode, on every SM
+                const bool stop = s_abort || (!tail && a.overlap && hdr->dec_ctas > 0 &&
+                                              *(volatile const int*)&hdr->next_item[0] >= max(1, hdr->dec_ctas * kPrefillStopPercent / 100));
+                const int place = stop ? n_items : atomicAdd(&hdr->next_item[1], 1);
+                if (place < n_items) {
+                    const WorkItem w = a.pre_items[place];
+                    n.seq = w.seq;
+                    n.head = w.head;
+                    n.row = w.row_begin;
+                    n.q_start = a.cu_q_lens[w.seq];
+                    n.q_len = a.cu_q_lens[w.seq + 1] - n.q_start;
+                    n.kv_len = a.kv_lens[w.seq];
+                    const int last = min(n.row + 128 * TILES, n.q_len * G) - 1;
+                    const int qmin = n.kv_len - n.q_len + n.row / G, qmax = n.kv_len - n.q_len + last / G;
+                    n.block0 = a.sliding_window > 0 ? max(0, qmin - a.sliding_window + 1) / BK : 0;
+                    n.blocks = qmax / BK + 1 - n.block0;
+                }
+                s_items[slot] = n;
+                mbar_arrive(&item_full[slot]);
+                ++fetched;
+            };
+            bool ok = true;
+            while (ok) {
+                if (lane == 0) fetch();
+                __syncwarp();
+                if (!next_item(it)) break;
+                ok = mbar_wait(q_empty, items & 1, err);  // the previous item's last QK
+                if (!ok) break;
+                const int n_rows = it.q_len * G, tiles = min(TILES, cdiv(n_rows - it.row, 128));
+                if (q_tma) {
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(q_full, tiles * T::kQTile);
+                        for (int t = 0; t < tiles; ++t)
+#pragma unroll
+                            for (int p = 0; p < T::DP; ++p)
+                                tma_load_3d(smem_u32(smem + t * T::kQTile + p * T::kQPanel), &tm_q, 64 * p, it.head * G,
+                                            it.q_start + (it.row + t * 128) / G, q_full);
+                    }
+                } else {
+                    // a group size that does not divide a tile: 16 bytes at a time, rows that are not there as zeros
+                    for (int i = lane; i < tiles * 128 * (D / 8); i += 32) {
+                        const int r = i / (D / 8), c = i % (D / 8), R = it.row + r, t = r >> 7, tr = r & 127;
+                        const bool rv = R < n_rows;
+                        cp_async16(smem_u32(smem + t * T::kQTile + (c >> 3) * T::kQPanel + tr * 128 + (((c & 7) ^ (tr & 7)) << 4)),
+                                   a.q + ((size_t)(it.q_start + (rv ? R / G : 0)) * a.num_q_heads + it.head * G + (rv ? R % G : 0)) * D + c * 8, rv);
+                    }
+                    cp_async_commit();
+                    cp_async_wait<0>();
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(q_full);
+                }
+            }
+            if (!ok) s_abort = 1;
+            if (lane == 0 && s_abort) {
+                // an aborted warp still ends the other warps' wait for an item; a copy under way lands (bounded)
+                if (!ok) fetch();
+                if (items > 0) mbar_wait(q_full, (items - 1) & 1, err);
+            }
+            __syncwarp();
+        } else if (warp >= kConv0) {
+            // ---------------- converters: a thread a row, or (head_dim 256) half of one ----------------
+            constexpr int TPR = D == 256 ? 2 : 1;        // threads a row
+            constexpr int DT = D / TPR;                  // dims of K (and V) a thread
+            constexpr int CH = DT / 32;                  // 16-byte chunks of them
+            static_assert(BK * TPR == 128, "a thread's share");
+            const int ct = tid - kConv0 * 32, row = ct / TPR, half = ct % TPR;
+            // this thread's bytes of a raw block: its K, its V, the row's parameters
+            uint8_t* const mine = smem + T::kOffRaw + row * F::kRow;
+            const uint8_t* kv = static_cast<const uint8_t*>(a.kv_pages);
+            const size_t slot_bytes = (size_t)a.num_kv_heads * F::kRow;
+            uint32_t jb = 0, jr = 0;  // blocks converted, and raw blocks asked for
+            bool ok = true;
+            while (ok && next_item(it)) {
+                const int* tbl = a.page_indices + (size_t)it.seq * a.pages_per_seq;
+                const int ke = min(it.kv_len, it.kv_len - it.q_len + (min(it.row + 128 * TILES, it.q_len * G) - 1) / G + 1);
+                // (a window leaves out the first block's keys before its first row's)
+                const int k0 = a.sliding_window > 0 ? it.kv_len - it.q_len + it.row / G - a.sliding_window + 1 : 0;
+                const int key_first = it.block0 * BK + row;
+                auto page_of = [&](int j) -> int {
+                    const int key = key_first + j * BK;
+                    return j < it.blocks && key < ke ? __ldg(tbl + key / a.page_size) : -1;
+                };
+                auto ask = [&](int j, int page) {  // block j's row on its way (an empty group where there is none)
+                    const int key = key_first + j * BK;
+                    if (j < it.blocks && key < ke) {
+                        if ((unsigned)page >= (unsigned)a.total_num_pages) {
+                            set_error(err, RPA_DEV_ERR_PAGE);
+                            page = 0;
+                        }
+                        const uint8_t* src = kv + ((size_t)page * a.page_size + key % a.page_size) * slot_bytes + (size_t)it.head * F::kRow;
+                        const uint32_t dst = smem_u32(mine + (jr % NR) * T::kRaw);
+#pragma unroll
+                        for (int part = 0; part < 2; ++part)
+#pragma unroll
+                            for (int c = 0; c < CH; ++c) {
+                                const int off = part * F::kPart + half * (DT / 2) + c * 16;
+                                cp_async16(dst + off, src + off, true);
+                            }
+                        // (both threads of a row bring its parameters: the same bytes)
+#pragma unroll
+                        for (int c = 0; c < F::NG / 2; ++c) cp_async16(dst + F::kParams + c * 16, src + F::kParams + c * 16, true);
+                    }
+                    cp_async_commit();
+                    ++jr;
+                };
+#pragma unroll
+                for (int j = 0; j < NR - 1; ++j) ask(j, page_of(j));
+                int page_next = page_of(NR - 1);
+                for (int j = 0; j < it.blocks; ++j, ++jb) {
+                    const int page = page_next;
+                    page_next = page_of(j + NR);
+                    ask(j + NR - 1, page);
+                    cp_async_wait<NR - 1>();
+                    const uint8_t* src = mine + ((jr - NR) % NR) * T::kRaw;
+                    const bool in = key_first + j * BK < ke && key_first + j * BK >= k0;
+#pragma unroll
+                    for (int part = 0; part < 2; ++part) {
+                        const uint32_t slot = part ? jb % NV : jb % NK, ph = (part ? jb / NV : jb / NK) & 1;
+                        if (!mbar_wait(part ? &v_empty[slot] : &k_empty[slot], ph ^ 1, err)) {
+                            ok = false;
+                            break;
+                        }
+                        uint8_t* stage = smem + (part ? T::kOffV + slot * T::kTile : T::kOffK + slot * T::kTile) + row * 128;
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) {
+                            const int d0 = half * DT + c * 32;
+                            uint32_t sm = *reinterpret_cast<const uint32_t*>(src + F::kParams + 4 * (part * F::NG + d0 / F::kGroup));
+                            if (!in) sm = 0;  // rows that no query sees: zeros, whatever lies there
+                            const uint4 w = *reinterpret_cast<const uint4*>(src + part * F::kPart + d0 / 2);
+                            const uint32_t s2 = __byte_perm(sm, sm, 0x1010), m2 = __byte_perm(sm, sm, 0x3232);
+                            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int chunk = d0 / 8 + e;
+                                *reinterpret_cast<uint4*>(stage + (chunk >> 3) * T::kPanel + (((chunk & 7) ^ (row & 7)) << 4)) = g4_panel8(ww[e], s2, m2);
+                            }
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(part ? &v_full[slot] : &k_full[slot]);
+                    }
+                    if (!ok) break;
+                }
+                cp_async_wait<0>();
+                if (!ok) s_abort = 1;
+            }
+        } else {
+            while (next_item(it)) {
+            }
+        }
+    }
+    // every role has left its loop
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMma0) tmem_dealloc(tmem, T::kTmemCols);
+}
+
+template <int D>
+static cudaError_t launch_pre(const RpaArgs& a, int num_sms, cudaStream_t stream, int tail) {
+    using T = G4Pre<D>;
+    auto kern = g4_prefill_kernel<D>;
+    static bool configured[64] = {};  // (by device: the attribute is the device's)
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!configured[dev]) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
+        if (e != cudaSuccess) return e;
+        // the warpgroups' register shares are dealt out of what the launch holds
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, kern);
+        if (e != cudaSuccess) return e;
+        if (T::TILES == 2 && fa.numRegs != T::kRegsLaunch) return cudaErrorLaunchOutOfResources;
+        configured[dev] = true;
+    }
+    CUtensorMap tq;
+    memset(&tq, 0, sizeof tq);
+    const int G = a.num_q_heads / a.num_kv_heads;
+    const int q_tma = 128 % G == 0 && make_tmap_bf16(&tq, a.q, D, a.num_q_heads, a.max_num_tokens, G, 128 / G);
+    ProfScope ps(tail == 1 ? "rpa_g4_prefill_tail" : "rpa_g4_prefill", stream);
+    return launch_pdl(kern, dim3(num_sms), dim3(T::kThreads), T::kSmem, stream, a.overlap && !tail, a, tq, q_tma, tail);
+}
+
+cudaError_t launch_g4_prefill(const RpaArgs& a, int num_sms, cudaStream_t stream, int tail) {
+    switch (a.head_dim) {
+        case 64: return launch_pre<64>(a, num_sms, stream, tail);
+        case 128: return launch_pre<128>(a, num_sms, stream, tail);
+        case 256: return launch_pre<256>(a, num_sms, stream, tail);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+int g4_prefill_rows(int head_dim) { return head_dim == 256 ? 128 : 256; }
+
+}  // namespace rpa

@@ -75,6 +75,13 @@ inline void rpa_rates(int head_dim, bool fp8, bool scale, bool pow2, float* pre,
     *dec = conv ? (fp8 && pow2 ? 38.f : 26.f) : 60.f;
 }
 
+// The same of the 4-bit cache's kernels, its bytes counted as one an element.
+inline void g4_rates(int head_dim, float* pre, float* dec, float* hbm) {
+    *pre = head_dim >= 256 ? 3000.f : head_dim >= 128 ? 6500.f : 4500.f;
+    *dec = 45.f;
+    *hbm = 10000.f;
+}
+
 // A scale the f16 paths may take: a power of two with e4m3 * scale inside bf16's normal range
 // (bf16(float(x) * scale) is then exactly x * scale, so the scale can move onto S and O).
 inline bool rpa_pow2_scale(float s) {
@@ -125,11 +132,12 @@ struct RpaArgs {
     int decode_per_sm;          // decode CTAs resident per SM (occupancy of the chosen kernel)
     int decode_heads;           // KV heads per decode item (decode_heads_for)
     int num_sms;
-    int prefill_rows;           // cross attention's two-tile kernel: rows of an item (128 or 256)
+    int prefill_rows;           // rows of a prefill item (128; the kernels with two tiles in flight 256)
     int plan_early;             // the plan reads the lengths before the stream's earlier work has ended
     int overlap;                // run prefill beside decode (off while kernels are timed one by one)
     float pre_flops_per_ns_sm;  // prefill kernel rate per SM (this head size and cache type)
     float dec_bytes_per_ns_sm;  // decode kernel rate per SM while SMs, not HBM, limit it
+    float dec_hbm_bytes_per_ns; // and with HBM saturated
     int item_cost_keys;         // per-group cost on the decode line (a multiple of 16 keys)
     int min_chunk;              // smallest static decode share (a multiple of 16 above item_cost_keys)
     // workspace
@@ -326,6 +334,13 @@ bool make_tmap_bf16(struct CUtensorMap_st* tm, const void* base, uint64_t d0, ui
 bool rpa_cross_tc_takes(const RpaArgs& a);
 int rpa_cross_tile_rows(const RpaArgs& a);  // 256 or 128: the rows of an item
 cudaError_t launch_rpa_cross_tc(const RpaArgs& a, int num_sms, cudaStream_t stream);
+// Attention over the 4-bit cache: the plan, then prefill beside decode on kernels of their own.
+cudaError_t launch_g4_forward(const RpaArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_g4_decode(const RpaArgs& a, int num_sms, cudaStream_t stream);
+int g4_decode_ctas_per_sm(const RpaArgs& a);
+cudaError_t launch_g4_prefill(const RpaArgs& a, int num_sms, cudaStream_t stream, int tail);
+int g4_prefill_rows(int head_dim);  // rows of an item
+cudaError_t launch_g4_read(const RopeUpdateArgs& a, __nv_bfloat16* k_out, __nv_bfloat16* v_out, int num_sms, cudaStream_t stream);
 cudaError_t launch_rpa_decode(const RpaArgs& a, int num_sms, cudaStream_t stream);
 int rpa_decode_ctas_per_sm(const RpaArgs& a);  // resident CTAs per SM of the kernel launch_rpa_decode picks
 cudaError_t launch_rpa_prefill(const RpaArgs& a, int num_sms, cudaStream_t stream, int tail);

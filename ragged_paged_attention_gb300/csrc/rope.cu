@@ -5,6 +5,7 @@
 // rope_apply of 8191 tokens, 32 + 8 heads of 128: 28.7 us in a graph, 0.87 of the copy rate; the cache write of
 // 4 x 4096 tokens, 32 + 8 + 8 heads of 128: bf16 70, fp8 62, int8 64, int4 65 us.
 #include "common.cuh"
+#include "g4.cuh"
 #include "kernels.h"
 #include "profile.h"
 #include "rope.cuh"
@@ -141,41 +142,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rpa_rope_updat
     // not write, and it ends after this grid has
     pdl_launch_dependents();
     __shared__ int cu[kRopeCu];
-    auto resolve = [&](int t0, int nt) {
-        if (a.max_num_seqs < kRopeCu) {
-            // all of cu_q_lens in one round trip, then a token a thread: two more for all of them (a warp a
-            // token took four or five, again for every eight tokens: 4 x 4096 tokens 74.0 us, now 70.5)
-            for (int i = threadIdx.x; i <= a.max_num_seqs; i += kRopeThreads) cu[i] = a.cu_q_lens[i];
-            const int num = a.num_seqs[0];
-            const bool some = num > 0 && num <= a.max_num_seqs;
-            if (!some && num != 0 && t0 == 0 && threadIdx.x == 0) set_error(a.err, RPA_DEV_ERR_NUM_SEQS);
-            __syncthreads();
-            if (threadIdx.x < nt) {
-                const int t = t0 + threadIdx.x;
-                int pos = 0;
-                uint8_t* slot = nullptr;
-                if (some && cu[0] <= t) {
-                    const int s = seq_of_token(cu, num, t);
-                    const uint32_t bad = rope_slot_of(a, t, s, cu[s], cu[s + 1], cu[num], pos, slot);
-                    if (bad) set_error(a.err, bad);
-                }
-                if (a.positions) pos = a.positions[t];
-                sh.pos[threadIdx.x] = pos;
-                sh.slot[threadIdx.x] = slot;
-            }
-            return;
-        }
-        for (int k = threadIdx.x >> 5; k < nt; k += kRopeWarps) {  // a warp a token
-            int pos = 0;
-            uint8_t* slot = nullptr;
-            if (!rope_slot(a, t0 + k, pos, slot)) slot = nullptr;
-            if (a.positions) pos = a.positions[t0 + k];
-            if ((threadIdx.x & 31) == 0) {
-                sh.pos[k] = pos;
-                sh.slot[k] = slot;
-            }
-        }
-    };
+    auto resolve = [&](int t0, int nt) { rope_slots(a, t0, nt, cu, sh.pos, sh.slot); };
     unsigned share = blockIdx.x;
     if (share < a.q_share.blocks) {
         rope_block<true, INTER>(
@@ -194,7 +161,10 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rpa_rope_updat
         uint8_t* slot = sh.slot[k];
         if (!slot) return;
         uint8_t* row = slot + (2 * h + part) * a.row_bytes;
-        if (KV != RPA_DTYPE_BF16 || inv != 1.f) {
+        if constexpr (KV == RPA_DTYPE_G4) {
+            if (turns) turn_chunks<INTER>(xa, xb, cs, stride);
+            g4_store_unit(slot + 2 * h * a.row_bytes, part, a.head_dim, ca, cb, xa, xb);
+        } else if (KV != RPA_DTYPE_BF16 || inv != 1.f) {
             float x[16];
             rope_unpack<8>(xa, x);
             rope_unpack<8>(xb, x + 8);
@@ -242,6 +212,40 @@ __global__ void __launch_bounds__(kRopeThreads) rpa_rope_update_narrow_kernel(co
                                             *reinterpret_cast<const Chunk*>(src + cb),
                                             [&](float (&x)[2 * VEC]) { rope_turn<VEC>(a.tab.interleaved, cs, x); });
                     });
+}
+
+// The values that the 4-bit rows of the batch's tokens stand for, s n + m rounded to bf16: the inverse of the write
+// above.  A thread takes 16 elements of K or V: 8 bytes in, two 16-byte stores; the pair (s, m) is one word.
+constexpr int kG4ReadThreads = 256;
+__global__ void __launch_bounds__(kG4ReadThreads) rpa_g4_read_kernel(const __grid_constant__ RopeUpdateArgs a, __nv_bfloat16* k_out,
+                                                                     __nv_bfloat16* v_out, int tokens) {
+    __shared__ int cu[kRopeCu], pos[kRopeTokens];
+    __shared__ uint8_t* slot[kRopeTokens];
+    const int t0 = blockIdx.x * tokens, nt = min(tokens, a.max_num_tokens - t0);
+    rope_slots(a, t0, nt, cu, pos, slot);
+    __syncthreads();
+    const int d = a.head_dim, lg = d == 64 ? 5 : 6, per_head = d / 16, per_part = a.num_kv_heads * per_head;
+    for (int i = threadIdx.x; i < nt * 2 * per_part; i += kG4ReadThreads) {
+        const int tok = i / (2 * per_part), r = i - tok * 2 * per_part, part = r >= per_part, u = r - part * per_part;
+        const int h = u / per_head, at = (u - h * per_head) * 16;
+        if (!slot[tok]) continue;
+        const uint8_t* row = slot[tok] + 2 * h * a.row_bytes;
+        const uint2 w = *reinterpret_cast<const uint2*>(row + part * (d / 2) + at / 2);
+        const uint32_t sm = *reinterpret_cast<const uint32_t*>(row + d + 4 * (part * (d >> lg) + (at >> lg)));
+        __nv_bfloat16* out = (part ? v_out : k_out) + ((size_t)(t0 + tok) * a.num_kv_heads + h) * d + at;
+        reinterpret_cast<uint4*>(out)[0] = g4_values8(w.x, bf16_lo(sm), bf16_hi(sm));
+        reinterpret_cast<uint4*>(out)[1] = g4_values8(w.y, bf16_lo(sm), bf16_hi(sm));
+    }
+}
+
+cudaError_t launch_g4_read(const RopeUpdateArgs& a, __nv_bfloat16* k_out, __nv_bfloat16* v_out, int num_sms, cudaStream_t stream) {
+    ProfScope ps("rpa_g4_read", stream);
+    const int units = a.num_kv_heads * a.head_dim / 8;  // of a token
+    // a few passes of the block's threads, fewer where the batch would not fill the SMs
+    int tokens = max(1, min(kRopeTokens, 4 * kG4ReadThreads / units));
+    tokens = max(1, min(tokens, a.max_num_tokens / (4 * num_sms)));
+    rpa_g4_read_kernel<<<(a.max_num_tokens + tokens - 1) / tokens, kG4ReadThreads, 0, stream>>>(a, k_out, v_out, tokens);
+    return cudaGetLastError();
 }
 
 constexpr int kRopePasses = 5, kRopeBlocks = 16;
@@ -316,6 +320,8 @@ static cudaError_t launch_update_kv(RopeUpdateArgs& a, int num_sms, cudaStream_t
             rpa_rope_update_kernel<true, KV><<<grid, kRopeThreads, 0, stream>>>(a);
         else
             rpa_rope_update_kernel<false, KV><<<grid, kRopeThreads, 0, stream>>>(a);
+    } else if constexpr (KV == RPA_DTYPE_G4) {
+        return cudaErrorInvalidValue;  // (the host refuses it)
     } else if (vec == 2) {
         rpa_rope_update_narrow_kernel<2, KV><<<rope_blocks(a.max_num_tokens), kRopeThreads, 0, stream>>>(a);
     } else {
@@ -334,6 +340,7 @@ cudaError_t launch_rope_update(RopeUpdateArgs& a, int num_sms, cudaStream_t stre
         case RPA_DTYPE_FP8_E4M3: return launch_update_kv<RPA_DTYPE_FP8_E4M3>(a, num_sms, stream);
         case RPA_DTYPE_INT8: return launch_update_kv<RPA_DTYPE_INT8>(a, num_sms, stream);
         case RPA_DTYPE_INT4: return launch_update_kv<RPA_DTYPE_INT4>(a, num_sms, stream);
+        case RPA_DTYPE_G4: return launch_update_kv<RPA_DTYPE_G4>(a, num_sms, stream);
         default: return cudaErrorInvalidValue;
     }
 }

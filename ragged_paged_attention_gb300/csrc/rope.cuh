@@ -178,6 +178,46 @@ __device__ __forceinline__ bool rope_slot(const RopeUpdateArgs& a, int t, int& p
     return slot != nullptr;
 }
 
+// Positions and slots (NULL where the token has none) of the block's tokens t0 .. t0 + nt - 1, by the whole block;
+// cu: kRopeCu ints of shared memory.  Behind it a barrier.
+constexpr int kRopeCu = 1024;
+constexpr int kRopeTokens = 32;     // most tokens of a block
+__device__ __forceinline__ void rope_slots(const RopeUpdateArgs& a, int t0, int nt, int* cu, int* pos_of, uint8_t** slot_of) {
+    if (a.max_num_seqs < kRopeCu) {
+        // all of cu_q_lens in one round trip, then a token a thread: two more for all of them (a warp a
+        // token took four or five, again for every eight tokens: 4 x 4096 tokens 74.0 us, now 70.5)
+        for (int i = threadIdx.x; i <= a.max_num_seqs; i += blockDim.x) cu[i] = a.cu_q_lens[i];
+        const int num = a.num_seqs[0];
+        const bool some = num > 0 && num <= a.max_num_seqs;
+        if (!some && num != 0 && t0 == 0 && threadIdx.x == 0) set_error(a.err, RPA_DEV_ERR_NUM_SEQS);
+        __syncthreads();
+        if (threadIdx.x < nt) {
+            const int t = t0 + threadIdx.x;
+            int pos = 0;
+            uint8_t* slot = nullptr;
+            if (some && cu[0] <= t) {
+                const int s = seq_of_token(cu, num, t);
+                const uint32_t bad = rope_slot_of(a, t, s, cu[s], cu[s + 1], cu[num], pos, slot);
+                if (bad) set_error(a.err, bad);
+            }
+            if (a.positions) pos = a.positions[t];
+            pos_of[threadIdx.x] = pos;
+            slot_of[threadIdx.x] = slot;
+        }
+        return;
+    }
+    for (int k = threadIdx.x >> 5; k < nt; k += blockDim.x >> 5) {  // a warp a token
+        int pos = 0;
+        uint8_t* slot = nullptr;
+        if (!rope_slot(a, t0 + k, pos, slot)) slot = nullptr;
+        if (a.positions) pos = a.positions[t0 + k];
+        if ((threadIdx.x & 31) == 0) {
+            pos_of[k] = pos;
+            slot_of[k] = slot;
+        }
+    }
+}
+
 // ---- a block's walk over head rows: the 16-byte path ----
 // A block takes head rows of one kind (q, k or v): of whole tokens, or of a part of one token's
 // heads.  Its threads stand for the units of as many rows as they hold (256 / units) and walk down
@@ -188,7 +228,6 @@ constexpr int kRopeThreads = 256;
 constexpr int kRopeWarps = kRopeThreads / 32;
 constexpr int kRopeBlocksPerSm = 4;
 constexpr int kRopeAhead = 3;
-constexpr int kRopeTokens = 32;     // most tokens of a block
 constexpr int kRopePairs = 2048;    // most pairs whose sines a block keeps (16 KB)
 
 struct RopeShared {
@@ -198,8 +237,6 @@ struct RopeShared {
     uint8_t* slot[kRopeTokens];
     int pos[kRopeTokens];
 };
-// cu_q_lens of the appending kernel, with the sequences' count behind
-constexpr int kRopeCu = 1024;
 
 // The unit's 16 values turned, two pairs an instruction; cs: its words of RopeShared::cs, `stride`
 // apart.

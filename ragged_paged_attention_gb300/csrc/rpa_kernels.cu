@@ -7,7 +7,7 @@
 //     (sequences whose q_len * G rows fit one 16-row tile, split along the keys and, past
 //     8 rows, into two 8-row halves) and
 //     "prefill" items (128-row tiles of one KV head over the whole causal key range)
-//     (prefill items are 128 rows of one KV head: kPrefillRows).
+//     (prefill items are a.prefill_rows rows of one KV head: kPrefillRows unless the kernel takes two tiles).
 //   * the prefill items run on tcgen05/TMEM (rpa_prefill_tc.cu), the decode items on
 //     the streaming split-KV kernel (rpa_decode.cu); both are persistent CTAs that
 //     steal items from their list.
@@ -135,7 +135,7 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
         if (tid + 1 < S) {
             nn = tid + 1;
             const float tp = pre_flops / (a.pre_flops_per_ns_sm * (float)nn);
-            const float td = dec_bytes / fminf(kDecHbmBytesPerNs, a.dec_bytes_per_ns_sm * (float)(S - nn));
+            const float td = dec_bytes / fminf(a.dec_hbm_bytes_per_ns, a.dec_bytes_per_ns_sm * (float)(S - nn));
             tt = fmaxf(tp, td);
         }
         for (int o = 16; o > 0; o >>= 1) {
@@ -177,7 +177,7 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
             n_pre = 0;
         } else if (a.overlap && dec_bytes > 0.f && S > 1) {
             const float serial = pre_flops / (a.pre_flops_per_ns_sm * (float)S) +
-                                 dec_bytes / fminf(kDecHbmBytesPerNs, a.dec_bytes_per_ns_sm * (float)S);
+                                 dec_bytes / fminf(a.dec_hbm_bytes_per_ns, a.dec_bytes_per_ns_sm * (float)S);
             if (bt < 0.9f * serial) n_pre = bn;
         }
         hdr->prefill_ctas = n_pre;
@@ -249,7 +249,7 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
                 nrh = cdiv(ql * G, kDecodeRows);
                 wk = (round_bk(kl - klo) + a.item_cost_keys) * n_groups * nrh;
             } else {
-                np = cdiv(ql * G, kPrefillRows) * a.num_kv_heads;
+                np = cdiv(ql * G, a.prefill_rows) * a.num_kv_heads;
             }
         }
         long long tot_w;
@@ -338,7 +338,7 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
             WorkItem w;
             w.seq = s0 + k;
             w.head = h;
-            w.row_begin = r * kPrefillRows;
+            w.row_begin = r * a.prefill_rows;
             w.key_begin = 0;
             w.key_end = e_kl[k];
             w.first_item = it;
@@ -718,6 +718,25 @@ static cudaError_t launch_attention(const RpaArgs& a, int num_sms, cudaStream_t 
     e = launch_rpa_decode(a, num_sms, stream);
     if (e != cudaSuccess || !a.overlap) return e;
     return launch_rpa_prefill(a, num_sms, stream, 1);
+}
+
+// The same over the 4-bit cache.
+cudaError_t launch_g4_forward(const RpaArgs& a, int num_sms, cudaStream_t stream) {
+    cudaError_t e;
+    {
+        ProfScope ps("rpa_plan", stream);
+        e = launch_pdl(rpa_plan_kernel, dim3(1), dim3(1024), 0, stream, a.overlap != 0, a);
+    }
+    if (e != cudaSuccess) return e;
+    if (a.batch_kind == RPA_BATCH_DECODE_ONLY) {
+        RpaArgs d = a;
+        d.overlap = 0;
+        return launch_g4_decode(d, num_sms, stream);
+    }
+    if (a.batch_kind == RPA_BATCH_PREFILL_ONLY) return launch_g4_prefill(a, num_sms, stream, 2);
+    e = launch_g4_prefill(a, num_sms, stream, 0);
+    if (e == cudaSuccess) e = launch_g4_decode(a, num_sms, stream);
+    return e != cudaSuccess || !a.overlap ? e : launch_g4_prefill(a, num_sms, stream, 1);
 }
 
 cudaError_t launch_rpa_forward(const RpaArgs& a, int num_sms, cudaStream_t stream) {
