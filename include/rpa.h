@@ -112,6 +112,7 @@ typedef enum {
 #define RPA_DEV_ERR_POSITION   0x20u  /* sparse: query position outside [0, seq_len) */
 #define RPA_DEV_ERR_TIMEOUT    0x40u  /* a pipeline wait gave up after its time limit (2 s) */
 #define RPA_DEV_ERR_BATCH_KIND 0x80u  /* a sequence of the class rpa_params.batch_kind excludes */
+#define RPA_DEV_ERR_BUDGET     0x100u /* eviction: a budget outside [0, max_keys] */
 
 /* rpa_params.batch_kind: what the caller knows of the batch's mix (the MLA v1 page keys its
  * decode-only, prefill-only and mixed kernels on its `distribution`).  A sequence is decode-class
@@ -416,6 +417,62 @@ RPA_API int rpa_g4_workspace_size(const rpa_params* p, size_t* bytes);
 RPA_API int rpa_g4_forward(const rpa_params* p, const void* q, const void* kv_pages, const int32_t* kv_lens,
                            const int32_t* page_indices, const int32_t* cu_q_lens, const int32_t* num_seqs, void* out,
                            void* workspace, size_t workspace_bytes, rpa_stream_t stream);
+
+/* ---------------------------------------------------------------------- */
+/* Key weights and eviction                                                 */
+/* ---------------------------------------------------------------------- */
+
+/* The attention that each cached key gets from the batch's queries, added to what it had:
+ *   weights_out[page, h, slot] = keep * weights[page, h, slot] + the sum, over the sequence's query tokens in the
+ *   batch and the q heads of KV head h's group, of the key's softmax probability (scores, soft cap, causal mask and
+ *   window as rpa_forward's)
+ *   weights, weights_out  float32 [total_num_pages, num_kv_heads, page_size]; weights_out may be weights; weights may
+ *                         be NULL with keep 0, and is not read then
+ * for every key of the batch's sequences (0 new weight where no query sees it); other entries are left as they are, as
+ * are those of sequences without queries.  A slot that two sequences of a batch share gets either's.  kv_dtype is
+ * RPA_DTYPE_BF16 or RPA_DTYPE_G4, head_dim 64, 128 or 256, k_scale and v_scale 0, mask_value NaN.  Queries: a decode
+ * step's, to add up over steps, or a prompt's last ones.  `workspace`: rpa_key_weights_workspace_size bytes. */
+RPA_API int rpa_key_weights_workspace_size(const rpa_params* p, size_t* bytes);
+RPA_API int rpa_key_weights(const rpa_params* p, const void* q, const void* kv_pages, const int32_t* kv_lens,
+                            const int32_t* page_indices, const int32_t* cu_q_lens, const int32_t* num_seqs, const float* weights,
+                            float* weights_out, float keep, void* workspace, size_t workspace_bytes, rpa_stream_t stream);
+
+typedef struct {
+    uint32_t struct_size;        /* sizeof(rpa_evict_params) */
+    uint32_t version;            /* RPA_ABI_VERSION */
+    int32_t num_kv_heads;
+    int32_t row_bytes;           /* bytes of a token's K and V of one KV head, adjacent in the cache: 4 head_dim (bf16),
+                                    2 head_dim (fp8, int8), head_dim (int4), RPA_G4_ROW_BYTES; a multiple of 16 */
+    int32_t total_num_pages;
+    int32_t page_size;
+    int32_t max_num_seqs;
+    int32_t pages_per_seq;
+    int32_t max_keys;            /* > 0, >= sinks + recent: places of slots_out a head */
+    int32_t sinks;               /* >= 0: a sequence's first keys, which always stay */
+    int32_t recent;              /* >= 0: and its last ones */
+    int32_t reserved;            /* 0 */
+} rpa_evict_params;
+
+/* Leaves each sequence and KV head its budgets[i] keys of the largest weights, in the first slots of its pages.
+ *   kv_pages    the cache, written in place: [total_num_pages, page_size, num_kv_heads, row_bytes]
+ *   kv_lens     int32 [max_num_seqs]   keys now; page_indices, num_seqs as everywhere
+ *   weights     float32 [total_num_pages, num_kv_heads, page_size], as rpa_key_weights leaves them
+ *   budgets     int32 [max_num_seqs]   0 to max_keys
+ *   kv_lens_out int32 [max_num_seqs]   keys afterwards: min(kv_len, max(budget, sinks + recent)); may be kv_lens, or NULL
+ *   slots_out   int32 [max_num_seqs, num_kv_heads, max_keys]   the slot that the key in slot j had; places from the new
+ *               length on are not written
+ *   weights_out float32, as weights: the kept keys' weights in their new slots; may be weights, or NULL
+ * The first `sinks` and the last `recent` keys come before all others, then larger weights (NaN last), then lower slots.
+ * Kept keys in the first slots stay where they are; the others move, in their order, to the slots of the keys that
+ * go, in theirs.  (A key's own position is in its rotation: attention over what is left is by rpa_forward without a
+ * window, new tokens with `positions` of their own.)  Slots behind the new length keep what they hold.  No page may belong to two
+ * sequences of the batch.  A sequence whose metadata is bad is left alone.  `workspace`: rpa_evict_workspace_size
+ * bytes. */
+RPA_API int rpa_evict_workspace_size(const rpa_evict_params* p, size_t* bytes);
+RPA_API int rpa_evict_kv_cache(const rpa_evict_params* p, void* kv_pages, const int32_t* kv_lens, const int32_t* page_indices,
+                               const int32_t* num_seqs, const float* weights, const int32_t* budgets, int32_t* kv_lens_out,
+                               int32_t* slots_out, float* weights_out, void* workspace, size_t workspace_bytes,
+                               rpa_stream_t stream);
 
 /* ---------------------------------------------------------------------- */
 /* MLA latent ragged paged attention                                       */

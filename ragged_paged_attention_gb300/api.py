@@ -32,7 +32,8 @@ EXPORTS = ("rpa_workspace_size", "rpa_forward", "rpa_update_kv_cache", "mla_work
            "rpa_forward_update", "sparse_mla_ragged_workspace_size", "sparse_mla_write_and_attend_ragged",
            "rpa_selftest_bounded_wait", "rope_table_init", "rope_apply", "rpa_rope_update_kv_cache",
            "rpa_rope_forward_update", "rpa_cross_workspace_size", "rpa_cross_forward", "rpa_g4_update_kv_cache",
-           "rpa_g4_read_kv_cache", "rpa_g4_workspace_size", "rpa_g4_forward")
+           "rpa_g4_read_kv_cache", "rpa_g4_workspace_size", "rpa_g4_forward", "rpa_key_weights_workspace_size", "rpa_key_weights",
+           "rpa_evict_workspace_size", "rpa_evict_kv_cache")
 
 
 class RpaError(RuntimeError):
@@ -84,6 +85,13 @@ class sparse_ragged_params(ctypes.Structure):
                 ("rope", ctypes.c_int32), ("row_stride", ctypes.c_int32), ("topk", ctypes.c_int32),
                 ("read_block", ctypes.c_int32), ("page_size", ctypes.c_int32), ("num_page_ids", ctypes.c_int32),
                 ("total_num_pages", ctypes.c_int32), ("sm_scale", ctypes.c_float)]
+
+
+class rpa_evict_params(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_uint32), ("version", ctypes.c_uint32), ("num_kv_heads", ctypes.c_int32),
+                ("row_bytes", ctypes.c_int32), ("total_num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_num_seqs", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32), ("max_keys", ctypes.c_int32),
+                ("sinks", ctypes.c_int32), ("recent", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 ROPE_HALF, ROPE_INTERLEAVED, ROPE_MAX_DIM = 0, 1, 256
@@ -161,6 +169,10 @@ def load_library(path: str = LIB_PATH):
         lib.rpa_g4_read_kv_cache.argtypes = [ctypes.POINTER(rpa_params)] + [P] * 8 + [sz, P]
         lib.rpa_g4_workspace_size.argtypes = [ctypes.POINTER(rpa_params), szp]
         lib.rpa_g4_forward.argtypes = lib.rpa_cross_forward.argtypes
+        lib.rpa_key_weights_workspace_size.argtypes = [ctypes.POINTER(rpa_params), szp]
+        lib.rpa_key_weights.argtypes = [ctypes.POINTER(rpa_params)] + [P] * 8 + [ctypes.c_float, P, sz, P]
+        lib.rpa_evict_workspace_size.argtypes = [ctypes.POINTER(rpa_evict_params), szp]
+        lib.rpa_evict_kv_cache.argtypes = [ctypes.POINTER(rpa_evict_params)] + [P] * 10 + [sz, P]
         lib.rpa_check_device_status.argtypes = [P, ctypes.POINTER(ctypes.c_uint32), P]
         lib.rpa_selftest_bounded_wait.argtypes = [P, sz, P]
         lib.rpa_profile_enable.argtypes = [ctypes.c_int]
@@ -805,6 +817,145 @@ def rpa_g4_forward(q, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, *, s
     if rc:
         _check(rc)
     return out
+
+
+def _is_g4(kv_pages) -> bool:
+    return isinstance(kv_pages, torch.Tensor) and kv_pages.dtype is torch.uint8
+
+
+def _page_weights(dev, t, name, kv_pages, hkv):
+    """Checks float32 weights [pages, Hkv, page_size] of a cache."""
+    _on(dev, t, name, torch.float32)
+    want = (kv_pages.shape[0], hkv, kv_pages.shape[1])
+    if tuple(t.shape) != want:
+        raise ValueError(f"{name} must be {want}, got {tuple(t.shape)}")
+
+
+def rpa_key_weights_workspace_size(params: rpa_params) -> int:
+    lib = load_library()
+    n = ctypes.c_size_t(0)
+    _check(lib.rpa_key_weights_workspace_size(ctypes.byref(params), ctypes.byref(n)))
+    return n.value
+
+
+def rpa_key_weights(q, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, weights, *, sm_scale=1.0, sliding_window=None,
+                    soft_cap=None, keep=1.0, weights_out=None, workspace=None):
+    """The attention that each cached key gets from the batch's queries, added up: ``weights_out`` = ``keep * weights`` + the sum of
+    the softmax probabilities of the sequence's queries and the group's heads, float32 [pages, Hkv, page_size], at the
+    slots of the batch's keys. Returns ``weights_out`` (``weights`` itself where none is given). The cache is bf16 or 4-bit
+    (``rpa_g4_update_kv_cache``'s)."""
+    lib = _lib or load_library()
+    dev = _cuda_index(q, "q")
+    if dev != _current():
+        with torch.cuda.device(dev):
+            return rpa_key_weights(q, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, weights, sm_scale=sm_scale,
+                                   sliding_window=sliding_window, soft_cap=soft_cap, keep=keep, weights_out=weights_out,
+                                   workspace=workspace)
+    _on(dev, q, "q", torch.bfloat16)
+    if q.dim() != 3:
+        raise ValueError(f"q must be [tokens, heads, head_dim], got {tuple(q.shape)}")
+    T, hq, d = q.shape
+    prm = _batch_params(dev, T, hq, d, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, sm_scale, sliding_window, soft_cap,
+                        g4=_is_g4(kv_pages))
+    hkv = prm.num_combined_kv_heads // 2
+    if weights is not None or keep != 0.0:
+        _page_weights(dev, weights, "weights", kv_pages, hkv)
+    if weights_out is None:
+        if weights is None:
+            raise ValueError("weights or weights_out must be given")
+        weights_out = weights
+    _page_weights(dev, weights_out, "weights_out", kv_pages, hkv)
+    if T == 0:
+        return weights_out
+    stream = _raw_stream(dev)
+    if workspace is not None:
+        _on(dev, workspace, "workspace", torch.uint8)
+    else:
+        n = ctypes.c_size_t(0)
+        _check(lib.rpa_key_weights_workspace_size(ctypes.byref(prm), ctypes.byref(n)))
+        workspace = _own_workspace(n.value, dev, stream)
+    rc = lib.rpa_key_weights(ctypes.byref(prm), q.data_ptr(), kv_pages.data_ptr(), kv_lens.data_ptr(), page_indices.data_ptr(),
+                             cu_q_lens.data_ptr(), num_seqs.data_ptr(), None if weights is None else weights.data_ptr(),
+                             weights_out.data_ptr(), keep, workspace.data_ptr(), workspace.numel(), stream)
+    if rc:
+        _check(rc)
+    return weights_out
+
+
+def make_evict_params(kv_pages, page_indices, max_keys, *, sinks=0, recent=0) -> rpa_evict_params:
+    """rpa_evict_params of a cache: [pages, page_size, 2 Hkv, D] of any type, or a 4-bit one [pages, page_size, Hkv, row_bytes]
+    (a uint8 cache whose rows are ``g4_row_bytes`` long; int4 rows never are)."""
+    pages, ps, heads, width = kv_pages.shape
+    g4 = _is_g4(kv_pages) and width in _G4_DIMS
+    if not g4:
+        _kv_code(kv_pages.dtype)
+        if heads % 2:
+            raise ValueError(f"kv_pages must have K and V of each head, got {heads} combined heads")
+    hkv = heads if g4 else heads // 2
+    row = width * kv_pages.element_size() * (1 if g4 else 2)
+    seqs, pps = page_indices.shape
+    return rpa_evict_params(_EVICT_SIZE, ABI_VERSION, hkv, row, pages, ps, seqs, pps, max_keys, sinks, recent, 0)
+
+
+_EVICT_SIZE = ctypes.sizeof(rpa_evict_params)
+
+
+def rpa_evict_workspace_size(params: rpa_evict_params) -> int:
+    lib = load_library()
+    n = ctypes.c_size_t(0)
+    _check(lib.rpa_evict_workspace_size(ctypes.byref(params), ctypes.byref(n)))
+    return n.value
+
+
+def rpa_evict_kv_cache(kv_pages, kv_lens, page_indices, num_seqs, weights, budgets, max_keys, *, sinks=0, recent=0,
+                       kv_lens_out=None, slots_out=None, weights_out=None, workspace=None):
+    """Leaves each sequence and KV head its ``budgets[i]`` (at most ``max_keys``) keys of the largest ``weights``
+    (``rpa_key_weights``'s), its first ``sinks`` and last ``recent`` before all others, in the first slots of its pages;
+    writes ``kv_pages`` in place. Returns ``(kv_lens_out, slots_out)``: the new lengths (a new tensor where none is given;
+    ``kv_lens`` itself works) and, int32 [max_num_seqs, Hkv, max_keys], the slot that each kept key had. ``weights_out``
+    (``weights`` itself works) gets the kept keys' weights in their new slots."""
+    lib = _lib or load_library()
+    dev = _cuda_index(kv_pages, "kv_pages")
+    if dev != _current():
+        with torch.cuda.device(dev):
+            return rpa_evict_kv_cache(kv_pages, kv_lens, page_indices, num_seqs, weights, budgets, max_keys, sinks=sinks,
+                                      recent=recent, kv_lens_out=kv_lens_out, slots_out=slots_out, weights_out=weights_out,
+                                      workspace=workspace)
+    if kv_pages.dim() != 4 or not kv_pages.is_contiguous():
+        raise ValueError("kv_pages must be contiguous, [pages, page_size, heads, row]")
+    _on(dev, page_indices, "page_indices", _I32)
+    if page_indices.dim() != 2:
+        raise ValueError("page_indices must be [max_num_seqs, pages_per_seq]")
+    prm = make_evict_params(kv_pages, page_indices, max_keys, sinks=sinks, recent=recent)
+    seqs, hkv = prm.max_num_seqs, prm.num_kv_heads
+    _on(dev, kv_lens, "kv_lens", _I32, seqs)
+    _on(dev, budgets, "budgets", _I32, seqs)
+    _on(dev, num_seqs, "num_seqs", _I32, 1)
+    _page_weights(dev, weights, "weights", kv_pages, hkv)
+    if weights_out is not None:
+        _page_weights(dev, weights_out, "weights_out", kv_pages, hkv)
+    if kv_lens_out is None:
+        kv_lens_out = kv_lens.clone()
+    _on(dev, kv_lens_out, "kv_lens_out", _I32, seqs)
+    if slots_out is None:
+        slots_out = torch.empty((seqs, hkv, max_keys), dtype=torch.int32, device=kv_pages.device)
+    _on(dev, slots_out, "slots_out", _I32)
+    if tuple(slots_out.shape) != (seqs, hkv, max_keys):
+        raise ValueError(f"slots_out must be {(seqs, hkv, max_keys)}, got {tuple(slots_out.shape)}")
+    stream = _raw_stream(dev)
+    if workspace is not None:
+        _on(dev, workspace, "workspace", torch.uint8)
+    else:
+        n = ctypes.c_size_t(0)
+        _check(lib.rpa_evict_workspace_size(ctypes.byref(prm), ctypes.byref(n)))
+        workspace = _own_workspace(n.value, dev, stream)
+    rc = lib.rpa_evict_kv_cache(ctypes.byref(prm), kv_pages.data_ptr(), kv_lens.data_ptr(), page_indices.data_ptr(),
+                                num_seqs.data_ptr(), weights.data_ptr(), budgets.data_ptr(), kv_lens_out.data_ptr(),
+                                slots_out.data_ptr(), None if weights_out is None else weights_out.data_ptr(),
+                                workspace.data_ptr(), workspace.numel(), stream)
+    if rc:
+        _check(rc)
+    return kv_lens_out, slots_out
 
 
 def rpa_cross_workspace_size(params: rpa_params) -> int:

@@ -823,6 +823,173 @@ int rpa_g4_forward(const rpa_params* p, const void* q, const void* kv_pages, con
     return RPA_OK;
 }
 
+static int check_key_weights_params(const rpa_params* p) {
+    if (!p) return fail(RPA_ERR_NULL, "params is NULL");
+    const int rc = check_rpa_params(p, p->kv_dtype == RPA_DTYPE_G4);
+    if (rc) return rc;
+    if (p->kv_dtype != RPA_DTYPE_BF16 && p->kv_dtype != RPA_DTYPE_G4) return fail(RPA_ERR_DTYPE, "key weights take bf16 and 4-bit group caches");
+    if (p->head_dim != 64 && p->head_dim != 128 && p->head_dim != 256)
+        return fail(RPA_ERR_UNSUPPORTED, "key weights take head_dim 64, 128 or 256 (got %d)", p->head_dim);
+    if (p->k_scale != 0.f || p->v_scale != 0.f) return fail(RPA_ERR_VALUE, "key weights take no k_scale and v_scale");
+    if (!isnan(p->mask_value)) return fail(RPA_ERR_VALUE, "key weights: mask_value must be NaN");
+    return RPA_OK;
+}
+
+struct KwLayout {
+    size_t ends_a, ends_b, stats, total;
+    int max_items;
+};
+
+static KwLayout key_weights_layout(const rpa_params* p) {
+    KwLayout L;
+    const int hkv = p->num_combined_kv_heads / 2, G = p->num_q_heads / hkv;
+    // items: tiles of 16 rows, and about kKwTarget pieces more (a piece for every `work / kKwTarget` keys of a tile)
+    const size_t tiles = (size_t)hkv * ((size_t)p->max_num_tokens * G / 16 + p->max_num_seqs + 1);
+    size_t off = kWsHeaderBytes;
+    L.ends_a = off;
+    off = align_up(off + sizeof(int) * (size_t)p->max_num_seqs);
+    L.ends_b = off;
+    off = align_up(off + sizeof(int) * (size_t)p->max_num_seqs);
+    L.stats = off;
+    L.max_items = (int)(tiles + kKwTarget + 64);
+    off = align_up(off + sizeof(float2) * 16 * (size_t)L.max_items);
+    L.total = off;
+    return L;
+}
+
+int rpa_key_weights_workspace_size(const rpa_params* p, size_t* bytes) {
+    const int rc = check_key_weights_params(p);
+    if (rc) return rc;
+    if (!bytes) return fail(RPA_ERR_NULL, "bytes is NULL");
+    *bytes = key_weights_layout(p).total;
+    return RPA_OK;
+}
+
+int rpa_key_weights(const rpa_params* p, const void* q, const void* kv_pages, const int32_t* kv_lens, const int32_t* page_indices,
+                    const int32_t* cu_q_lens, const int32_t* num_seqs, const float* weights, float* weights_out, float keep,
+                    void* workspace, size_t workspace_bytes, rpa_stream_t stream) {
+    int rc = check_key_weights_params(p);
+    if (rc) return rc;
+    if (!q || !kv_pages || !kv_lens || !page_indices || !cu_q_lens || !num_seqs || !weights_out || (!weights && keep != 0.f))
+        return fail(RPA_ERR_NULL, "a tensor pointer is NULL");
+    if (!aligned16(q) || !aligned16(kv_pages)) return fail(RPA_ERR_VALUE, "q and kv_pages must be 16-byte aligned");
+    if (!isfinite(keep)) return fail(RPA_ERR_VALUE, "keep must be finite");
+    if (weights_out == q || weights_out == kv_pages) return fail(RPA_ERR_VALUE, "weights_out must not alias q or kv_pages");
+    const KwLayout L = key_weights_layout(p);
+    rc = check_workspace(workspace, workspace_bytes, L.total);
+    if (rc) return rc;
+    const int sms = num_sms_current();
+    if (!sms) return fail(RPA_ERR_CUDA, "no CUDA device");
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    KwArgs a;
+    memset(&a, 0, sizeof a);
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.kv_pages = kv_pages;
+    a.kv_lens = kv_lens;
+    a.page_indices = page_indices;
+    a.cu_q_lens = cu_q_lens;
+    a.num_seqs = num_seqs;
+    a.weights = weights;
+    a.weights_out = weights_out;
+    a.max_num_tokens = p->max_num_tokens;
+    a.num_q_heads = p->num_q_heads;
+    a.num_kv_heads = p->num_combined_kv_heads / 2;
+    a.total_num_pages = p->total_num_pages;
+    a.page_size = p->page_size;
+    a.max_num_seqs = p->max_num_seqs;
+    a.pages_per_seq = p->pages_per_seq;
+    a.sm_scale = p->sm_scale;
+    a.soft_cap = p->soft_cap;
+    a.keep = keep;
+    a.sliding_window = p->sliding_window;
+    a.hdr = reinterpret_cast<WsHeader*>(ws);
+    a.ends_a = reinterpret_cast<int*>(ws + L.ends_a);
+    a.ends_b = reinterpret_cast<int*>(ws + L.ends_b);
+    a.stats = reinterpret_cast<float2*>(ws + L.stats);
+    a.max_items = L.max_items;
+    cudaError_t e = launch_key_weights(a, p->head_dim, p->kv_dtype == RPA_DTYPE_G4, sms, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "rpa_key_weights launch");
+    return RPA_OK;
+}
+
+static int check_evict_params(const rpa_evict_params* p) {
+    if (!p) return fail(RPA_ERR_NULL, "params is NULL");
+    if (p->struct_size < sizeof(rpa_evict_params)) return fail(RPA_ERR_VALUE, "rpa_evict_params.struct_size too small");
+    if (p->version != RPA_ABI_VERSION) return fail(RPA_ERR_VALUE, "rpa_evict_params.version %u != %d", p->version, RPA_ABI_VERSION);
+    if (p->num_kv_heads <= 0 || p->row_bytes <= 0 || p->total_num_pages <= 0 || p->page_size <= 0 || p->max_num_seqs <= 0 ||
+        p->pages_per_seq <= 0 || p->max_keys <= 0)
+        return fail(RPA_ERR_SHAPE, "all sizes must be positive");
+    if (p->row_bytes % 16) return fail(RPA_ERR_SHAPE, "row_bytes %d must be a multiple of 16", p->row_bytes);
+    if (p->sinks < 0 || p->recent < 0 || (long long)p->sinks + p->recent > p->max_keys)
+        return fail(RPA_ERR_VALUE, "sinks and recent must be positive and together at most max_keys");
+    if ((long long)p->max_num_seqs * p->pages_per_seq > INT32_MAX || (long long)p->pages_per_seq * p->page_size > INT32_MAX ||
+        (long long)p->max_num_seqs * p->num_kv_heads * ((p->max_keys + 255) / 256) > INT32_MAX)
+        return fail(RPA_ERR_SHAPE, "page table or slots_out too large");
+    return RPA_OK;
+}
+
+struct EvictLayout {
+    size_t kept, holes, total;
+};
+
+static EvictLayout evict_layout(const rpa_evict_params* p) {
+    EvictLayout L;
+    L.kept = kWsHeaderBytes;
+    L.holes = align_up(L.kept + sizeof(int) * (size_t)p->max_num_seqs);
+    L.total = align_up(L.holes + sizeof(int) * (size_t)p->max_num_seqs * p->num_kv_heads * p->max_keys);
+    return L;
+}
+
+int rpa_evict_workspace_size(const rpa_evict_params* p, size_t* bytes) {
+    const int rc = check_evict_params(p);
+    if (rc) return rc;
+    if (!bytes) return fail(RPA_ERR_NULL, "bytes is NULL");
+    *bytes = evict_layout(p).total;
+    return RPA_OK;
+}
+
+int rpa_evict_kv_cache(const rpa_evict_params* p, void* kv_pages, const int32_t* kv_lens, const int32_t* page_indices,
+                       const int32_t* num_seqs, const float* weights, const int32_t* budgets, int32_t* kv_lens_out,
+                       int32_t* slots_out, float* weights_out, void* workspace, size_t workspace_bytes, rpa_stream_t stream) {
+    int rc = check_evict_params(p);
+    if (rc) return rc;
+    if (!kv_pages || !kv_lens || !page_indices || !num_seqs || !weights || !budgets || !slots_out)
+        return fail(RPA_ERR_NULL, "a tensor pointer is NULL");
+    if (!aligned16(kv_pages)) return fail(RPA_ERR_VALUE, "kv_pages must be 16-byte aligned");
+    if (slots_out == kv_lens || slots_out == page_indices || slots_out == budgets || slots_out == kv_lens_out || kv_lens_out == budgets)
+        return fail(RPA_ERR_VALUE, "slots_out and kv_lens_out must not alias page_indices or budgets, nor slots_out kv_lens");
+    const EvictLayout L = evict_layout(p);
+    rc = check_workspace(workspace, workspace_bytes, L.total);
+    if (rc) return rc;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    EvictArgs a;
+    memset(&a, 0, sizeof a);
+    a.kv_pages = static_cast<uint8_t*>(kv_pages);
+    a.kv_lens = kv_lens;
+    a.page_indices = page_indices;
+    a.num_seqs = num_seqs;
+    a.weights = weights;
+    a.budgets = budgets;
+    a.kv_lens_out = kv_lens_out;
+    a.slots_out = slots_out;
+    a.weights_out = weights_out;
+    a.num_kv_heads = p->num_kv_heads;
+    a.row_bytes = p->row_bytes;
+    a.total_num_pages = p->total_num_pages;
+    a.page_size = p->page_size;
+    a.max_num_seqs = p->max_num_seqs;
+    a.pages_per_seq = p->pages_per_seq;
+    a.max_keys = p->max_keys;
+    a.sinks = p->sinks;
+    a.recent = p->recent;
+    a.err = &reinterpret_cast<WsHeader*>(ws)->error_bits;
+    a.kept = reinterpret_cast<int*>(ws + L.kept);
+    a.holes = reinterpret_cast<int*>(ws + L.holes);
+    cudaError_t e = launch_evict(a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "rpa_evict_kv_cache launch");
+    return RPA_OK;
+}
+
 static int check_cross_params(const rpa_params* p) {
     const int rc = check_rpa_params(p);
     if (rc) return rc;

@@ -256,6 +256,50 @@ struct MlaUpdateArgs {
     int total_num_pages, page_size, max_num_seqs, pages_per_seq;
 };
 
+// Key weights: a warp's piece of a row tile's keys is at least kKwMinPiece keys, and about kKwTarget of them are made;
+// the second kernel's items are kKwChunk keys.
+constexpr int kKwMinPiece = 128, kKwTarget = 8192, kKwChunk = 128;
+
+struct KwArgs {
+    const __nv_bfloat16* q;
+    const void* kv_pages;
+    const int32_t* kv_lens;
+    const int32_t* page_indices;
+    const int32_t* cu_q_lens;
+    const int32_t* num_seqs;
+    const float* weights;           // [total_num_pages, num_kv_heads, page_size]
+    float* weights_out;             // may be weights
+    int max_num_tokens, num_q_heads, num_kv_heads;
+    int total_num_pages, page_size, max_num_seqs, pages_per_seq;
+    float sm_scale, soft_cap, keep;
+    int sliding_window;
+    // workspace
+    WsHeader* hdr;
+    int* ends_a;                    // [max_num_seqs] ends of the sequences' items of either kernel
+    int* ends_b;
+    float2* stats;                  // 16 rows' (maximum, sum) an item of the first
+    int max_items;                  // of the first
+};
+
+struct EvictArgs {
+    uint8_t* kv_pages;
+    const int32_t* kv_lens;
+    const int32_t* page_indices;
+    const int32_t* num_seqs;
+    const float* weights;           // [total_num_pages, num_kv_heads, page_size]
+    const int32_t* budgets;
+    int32_t* kv_lens_out;           // may be kv_lens, or null
+    int32_t* slots_out;             // [max_num_seqs, num_kv_heads, max_keys]
+    float* weights_out;             // may be weights, or null
+    int num_kv_heads, row_bytes;    // row_bytes: a key's K and V of one head
+    int total_num_pages, page_size, max_num_seqs, pages_per_seq, max_keys, sinks, recent;
+    int held;                       // set by the launch: keys whose order a block holds in shared memory
+    // workspace
+    uint32_t* err;
+    int* kept;                      // [max_num_seqs] keys that stay, -1: left alone
+    int* holes;                     // [max_num_seqs, num_kv_heads, max_keys]
+};
+
 // A rope_table as the kernels take it (by value, in the launch's parameters).
 struct RopeTab {
     uint64_t step[128];             // pair i's turn per position, as a fraction of 2^64
@@ -340,6 +384,8 @@ cudaError_t launch_g4_decode(const RpaArgs& a, int num_sms, cudaStream_t stream)
 int g4_decode_ctas_per_sm(const RpaArgs& a);
 cudaError_t launch_g4_prefill(const RpaArgs& a, int num_sms, cudaStream_t stream, int tail);
 int g4_prefill_rows(int head_dim);  // rows of an item
+cudaError_t launch_key_weights(const KwArgs& a, int head_dim, bool g4, int num_sms, cudaStream_t stream);
+cudaError_t launch_evict(EvictArgs& a, cudaStream_t stream);
 cudaError_t launch_g4_read(const RopeUpdateArgs& a, __nv_bfloat16* k_out, __nv_bfloat16* v_out, int num_sms, cudaStream_t stream);
 cudaError_t launch_rpa_decode(const RpaArgs& a, int num_sms, cudaStream_t stream);
 int rpa_decode_ctas_per_sm(const RpaArgs& a);  // resident CTAs per SM of the kernel launch_rpa_decode picks
