@@ -836,7 +836,8 @@ static int check_key_weights_params(const rpa_params* p) {
 }
 
 struct KwLayout {
-    size_t ends_a, ends_b, stats, total;
+    size_t ends_a, ends_b, ends_c, score_at, stats, scores, total;
+    long long max_scores;
     int max_items;
 };
 
@@ -850,9 +851,19 @@ static KwLayout key_weights_layout(const rpa_params* p) {
     off = align_up(off + sizeof(int) * (size_t)p->max_num_seqs);
     L.ends_b = off;
     off = align_up(off + sizeof(int) * (size_t)p->max_num_seqs);
+    L.ends_c = off;
+    off = align_up(off + sizeof(int) * (size_t)p->max_num_seqs);
+    L.score_at = off;
+    off = align_up(off + sizeof(int) * (size_t)p->max_num_seqs);
     L.stats = off;
     L.max_items = (int)(tiles + kKwTarget + 64);
     off = align_up(off + sizeof(float2) * 16 * (size_t)L.max_items);
+    // scores of the sequences of up to 16 rows: 4, 8 or 16 a key, less than twice a sequence's rows beyond 4
+    const long long rows = std::min(16ll * p->max_num_seqs, 4ll * p->max_num_seqs + 2ll * p->max_num_tokens * G);
+    const long long keys = ((long long)p->pages_per_seq * p->page_size + 15) / 16 * 16;
+    L.max_scores = keys > kKwScores / (hkv * rows) ? kKwScores : keys * hkv * rows;
+    L.scores = off;
+    off = align_up(off + sizeof(float) * (size_t)L.max_scores);
     L.total = off;
     return L;
 }
@@ -905,7 +916,12 @@ int rpa_key_weights(const rpa_params* p, const void* q, const void* kv_pages, co
     a.hdr = reinterpret_cast<WsHeader*>(ws);
     a.ends_a = reinterpret_cast<int*>(ws + L.ends_a);
     a.ends_b = reinterpret_cast<int*>(ws + L.ends_b);
+    a.ends_c = reinterpret_cast<int*>(ws + L.ends_c);
+    a.score_at = reinterpret_cast<int*>(ws + L.score_at);
     a.stats = reinterpret_cast<float2*>(ws + L.stats);
+    a.scores = reinterpret_cast<float*>(ws + L.scores);
+    a.max_scores = L.max_scores;
+    a.all_stored = (long long)p->max_num_tokens * (a.num_q_heads / a.num_kv_heads) <= 16 && L.max_scores < kKwScores;
     a.max_items = L.max_items;
     cudaError_t e = launch_key_weights(a, p->head_dim, p->kv_dtype == RPA_DTYPE_G4, sms, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "rpa_key_weights launch");

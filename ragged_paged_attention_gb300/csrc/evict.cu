@@ -16,6 +16,7 @@ namespace rpa {
 
 constexpr int kEvictThreads = 512;
 constexpr int kEvictBins = 2048;
+constexpr int kEvictAhead = 8;
 constexpr int kEvictHeld = 49152;      // most keys whose order a block holds in shared memory
 
 // Weights as integers of the same order: NaN below all, either zero alike; a kept key above all.
@@ -25,9 +26,17 @@ __device__ __forceinline__ uint32_t evict_order(float w) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// The place of sequence s's slot i: its page's first slot and the slot in the page.
-__device__ __forceinline__ size_t evict_slot(const EvictArgs& a, int s, int i) {
-    return (size_t)a.page_indices[(size_t)s * a.pages_per_seq + i / a.page_size] * a.page_size + i % a.page_size;
+// Where sequence s's slot i is: its page and the slot in it.
+struct EvictSlot {
+    size_t page;
+    int in_page;
+};
+__device__ __forceinline__ EvictSlot evict_slot(const EvictArgs& a, int s, int i) {
+    const int p = a.page_shift >= 0 ? i >> a.page_shift : i / a.page_size;
+    return {(size_t)a.page_indices[(size_t)s * a.pages_per_seq + p], i - p * a.page_size};
+}
+__device__ __forceinline__ size_t evict_weight(const EvictArgs& a, const EvictSlot& at, int h) {
+    return (at.page * a.num_kv_heads + h) * a.page_size + at.in_page;
 }
 
 // How many keys of sequence s stay, and its length; -1 where it is left alone (the error word then says why).
@@ -58,6 +67,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
     __shared__ long long scan[40];
     __shared__ int s_bad, s_digit, s_above;
     const int s = blockIdx.x / a.num_kv_heads, h = blockIdx.x % a.num_kv_heads, tid = threadIdx.x;
+    pdl_launch_dependents();  // (the moving kernel waits for this grid's end)
     int n = 0, keep = evict_keep(a, s, n);
     // every page of the sequence is one of the cache's, or the sequence is left alone
     if (tid == 0) s_bad = 0;
@@ -83,12 +93,19 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
     }
     auto order_of = [&](int i) -> uint32_t {
         if (i < a.sinks || i >= n - a.recent) return 0xffffffffu;
-        const size_t at = evict_slot(a, s, i), page = at / a.page_size;
-        return evict_order(a.weights[(page * a.num_kv_heads + h) * a.page_size + at % a.page_size]);
+        return evict_order(a.weights[evict_weight(a, evict_slot(a, s, i), h)]);
     };
     const bool fits = n <= a.held;
     if (fits) {
-        for (int i = tid; i < n; i += kEvictThreads) held[i] = order_of(i);
+        // (several keys' page and weight on their way at once)
+        for (int i0 = tid; i0 < n; i0 += kEvictAhead * kEvictThreads) {
+            uint32_t v[kEvictAhead];
+#pragma unroll
+            for (int u = 0; u < kEvictAhead; ++u) v[u] = order_of(min(i0 + u * kEvictThreads, n - 1));
+#pragma unroll
+            for (int u = 0; u < kEvictAhead; ++u)
+                if (i0 + u * kEvictThreads < n) held[i0 + u * kEvictThreads] = v[u];
+        }
         __syncthreads();
     }
     auto order = [&](int i) { return fits ? held[i] : order_of(i); };
@@ -128,7 +145,8 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
         width = shift;
     }
     // keys above `top` stay, and of those equal to it the first keep - above
-    const int ties = keep - above, per = cdiv(n, kEvictThreads), i0 = min(n, tid * per), i1 = min(n, i0 + per);
+    // (runs of an odd length: 32 threads' slots lie in 32 banks)
+    const int ties = keep - above, per = cdiv(n, kEvictThreads) | 1, i0 = min(n, tid * per), i1 = min(n, i0 + per);
     int equal = 0;
     for (int i = i0; i < i1; ++i) equal += order(i) == top;
     long long total;
@@ -170,6 +188,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     __shared__ uint4* to[kMoveThreads];
     const int head = blockIdx.x / blocks_per_head, s = head / a.num_kv_heads, h = head % a.num_kv_heads;
     const int block = blockIdx.x % blocks_per_head, lane = threadIdx.x & 31, w0 = threadIdx.x & ~31;
+    pdl_wait();
     const int keep = a.kept[s];
     if (keep < 0) return;
     if (a.kv_lens_out && h == 0 && block == 0 && threadIdx.x == 0) a.kv_lens_out[s] = keep;
@@ -177,19 +196,18 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     if (i - lane >= keep) return;
     const int src = i < keep ? a.slots_out[((size_t)s * a.num_kv_heads + h) * a.max_keys + i] : i;
     const bool moves = src != i;
-    size_t at = 0, at_src = 0;
+    EvictSlot at = {0, 0}, at_src = {0, 0};
     if (i < keep && (moves || a.weights_out)) {
         at = evict_slot(a, s, i);
         at_src = moves ? evict_slot(a, s, src) : at;
     }
-    if (i < keep && a.weights_out)
-        a.weights_out[(at / a.page_size * a.num_kv_heads + h) * a.page_size + at % a.page_size] =
-            a.weights[(at_src / a.page_size * a.num_kv_heads + h) * a.page_size + at_src % a.page_size];
+    if (i < keep && a.weights_out) a.weights_out[evict_weight(a, at, h)] = a.weights[evict_weight(a, at_src, h)];
     const uint32_t mask = __ballot_sync(0xffffffffu, moves);
     if (moves) {
         const int k = w0 + __popc(mask & ((1u << lane) - 1));
-        from[k] = reinterpret_cast<const uint4*>(a.kv_pages + (at_src * a.num_kv_heads + h) * a.row_bytes);
-        to[k] = reinterpret_cast<uint4*>(a.kv_pages + (at * a.num_kv_heads + h) * a.row_bytes);
+        auto row = [&](const EvictSlot& x) { return a.kv_pages + ((x.page * a.page_size + x.in_page) * a.num_kv_heads + h) * a.row_bytes; };
+        from[k] = reinterpret_cast<const uint4*>(row(at_src));
+        to[k] = reinterpret_cast<uint4*>(row(at));
     }
     __syncwarp();
     const int units = a.row_bytes / 16, all = __popc(mask) * units;
@@ -221,6 +239,7 @@ cudaError_t launch_evict(EvictArgs& a, cudaStream_t stream) {
         configured[dev] = true;
     }
     const long long most = (long long)a.pages_per_seq * a.page_size;
+    a.page_shift = (a.page_size & (a.page_size - 1)) == 0 ? __builtin_ctz(a.page_size) : -1;
     a.held = most <= kEvictHeld ? (int)most : 0;
     {
         ProfScope ps("rpa_evict_select", stream);
@@ -230,8 +249,8 @@ cudaError_t launch_evict(EvictArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     ProfScope ps("rpa_evict_move", stream);
     const int blocks = max(1, cdiv(a.max_keys, kMoveThreads));
-    evict_move_kernel<<<(unsigned)a.max_num_seqs * a.num_kv_heads * blocks, kMoveThreads, 0, stream>>>(a, blocks);
-    return cudaGetLastError();
+    return launch_pdl(evict_move_kernel, dim3((unsigned)a.max_num_seqs * a.num_kv_heads * blocks), dim3(kMoveThreads), 0, stream,
+                      !prof_enabled(), a, blocks);
 }
 
 }  // namespace rpa

@@ -28,14 +28,17 @@ namespace rpa {
 
 template <int D, int HG>
 struct G4Dec {
-    static constexpr int BK = kDecodeBK;
+    static constexpr int BK = 2 * kDecodeBK;             // keys a stage: two tiles of 16
+    // tiles at once: two, so that the chains of loads, products, maxima and exponentials of one run beside the other's (and
+    // the maximum's exchange and the barriers come once for both); head_dim 256 has no registers for that
+    static constexpr int NT = D == 256 ? 1 : 2;
     static constexpr int kSeg = HG * G4<D>::kRow;
     // rows 24 words apart modulo the 32 banks: K's 8-byte loads (four rows of 32 bytes a half-warp) and, with
     // the keys' order of key_of, V's 4-byte loads (four rows of 32 bytes) touch every bank once
     static constexpr int kPitch = kSeg + 32;
     static_assert(kPitch / 4 % 32 == 24 && kSeg % 16 == 0, "bank pattern");
     static constexpr int kStage = BK * kPitch;
-    static constexpr int STAGES = 4;
+    static constexpr int STAGES = 3;
     static constexpr int kBarOff = STAGES * kStage;
     static constexpr int kSmem = kBarOff + 2 * STAGES * 8;
     static constexpr int kThreads = (HG + 1) * 32;
@@ -80,7 +83,7 @@ __global__ void __launch_bounds__(G4Dec<D, HG>::kThreads) g4_decode_kernel(const
     fence_proxy_async_smem();
     __syncthreads();
     uint32_t pipe = 0;                                  // blocks this CTA has pushed through the ring so far
-    uint32_t issued_phase[STAGES] = {};                 // producer: last phase issued per stage (+ 1)
+    uint32_t issued = 0;                                // producer's first lane: blocks it has asked for
 
     // prefill first (the plan gave it every SM): start once it has ended (no-op on an ordinary launch)
     if (hdr->prefill_ctas >= a.num_sms && hdr->num_items[1] > 0) pdl_wait();
@@ -117,36 +120,41 @@ __global__ void __launch_bounds__(G4Dec<D, HG>::kThreads) g4_decode_kernel(const
         const uint32_t seg_bytes = seg_heads * F::kRow;
 
         if (producer) {
-            const size_t tbl = (size_t)s * a.pages_per_seq;
+            // lane t has key t of every stage; pages are looked up two stages ahead (one was not enough: a stage then
+            // took a load's latency)
+            const int* tbl = a.page_indices + (size_t)s * a.pages_per_seq;
+            const bool pow2 = (a.page_size & (a.page_size - 1)) == 0;
+            const int lps = __ffs(a.page_size) - 1;
             auto page_of = [&](int blk) -> int {
                 const int key = kb + blk * BK + lane;
-                return (lane < BK && blk < n_blocks && key < ke) ? __ldg(a.page_indices + tbl + key / a.page_size) : -1;
+                return blk < n_blocks && key < ke ? __ldg(tbl + (pow2 ? key >> lps : key / a.page_size)) : -1;
             };
-            int page_next = page_of(0);
+            int page_next = page_of(0), page_then = page_of(1);
             for (int blk = 0; blk < n_blocks; ++blk) {
                 const uint32_t q = pipe + blk, st = q % STAGES, ph = (q / STAGES) & 1;
                 const int page = page_next;
-                page_next = page_of(blk + 1);
+                page_next = page_then;
+                page_then = page_of(blk + 2);
                 const int key = kb + blk * BK + lane;
-                const bool want = lane < BK && key < ke;
-                const bool ok = want && (unsigned)page < (unsigned)a.total_num_pages;
-                if (want && !ok) set_error(err, RPA_DEV_ERR_PAGE);
+                const bool ok = key < ke && (unsigned)page < (unsigned)a.total_num_pages;
+                if (key < ke && !ok) set_error(err, RPA_DEV_ERR_PAGE);
                 const uint32_t mask = __ballot_sync(0xffffffffu, ok);
                 int go = 1;
                 if (lane == 0) {
                     go = mbar_wait(&empty[st], ph ^ 1, err);
                     if (go) {
                         mbar_arrive_expect_tx(&full[st], __popc(mask) * seg_bytes);
-                        issued_phase[st] = ph + 1;
+                        issued = q + 1;
                     } else {
                         s_abort = 1;
                     }
                 }
                 go = __shfl_sync(0xffffffffu, go, 0);
                 if (!go) break;
+                const int in_page = pow2 ? key & (a.page_size - 1) : key % a.page_size;
                 if (ok)
                     bulk_g2s(smem_u32(smem + st * T::kStage + lane * T::kPitch),
-                             kv + (((size_t)page * a.page_size + key % a.page_size) * Hkv + h0) * F::kRow, seg_bytes, &full[st]);
+                             kv + (((size_t)page * a.page_size + in_page) * Hkv + h0) * F::kRow, seg_bytes, &full[st]);
             }
         } else {
             // ---------------- consumer warp: KV head h0 + warp ----------------
@@ -169,7 +177,7 @@ __global__ void __launch_bounds__(G4Dec<D, HG>::kThreads) g4_decode_kernel(const
             // (kGroup / 4) + 8 wd on, and a k-step takes dims (0, 4 | 1, 5) or (2, 6 | 3, 7) of them, as K's masked
             // words come; the second pair of either lies 4 bits higher there, so it is a 16th here
             uint32_t qb[NG * KW * 2][2];
-            float qsum[NG][2], colmul[2];
+            float qsum[NG][2], to_log2[2];
             {
                 const int Rb = rb + g8;
                 const bool rvb = head_ok && Rb < n_rows;
@@ -193,8 +201,6 @@ __global__ void __launch_bounds__(G4Dec<D, HG>::kThreads) g4_decode_kernel(const
                     }
                     sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
                     sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) qsum[g][j] = __shfl_sync(0xffffffffu, sum[g], (2 * q4 + j) * 4);
                 }
                 mabs = fmaxf(mabs, __shfl_xor_sync(0xffffffffu, mabs, 1));
                 mabs = fmaxf(mabs, __shfl_xor_sync(0xffffffffu, mabs, 2));
@@ -214,8 +220,14 @@ __global__ void __launch_bounds__(G4Dec<D, HG>::kThreads) g4_decode_kernel(const
                     qb[2 * i + 1][0] = scaled(v.y << 16, v.w << 16, qs);                                // 2, 6
                     qb[2 * i + 1][1] = scaled(v.y & 0xffff0000u, v.w & 0xffff0000u, qs * 0.0625f);      // 3, 7
                 }
+                // scores are in units of the products, 2^(k - 133) of their size, until the factor to log2 units
+                const float unit = ldexpf(1.f, k - 133);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) colmul[j] = __shfl_sync(0xffffffffu, rowmul, (2 * q4 + j) * 4);
+                for (int j = 0; j < 2; ++j) {
+                    to_log2[j] = __shfl_sync(0xffffffffu, rowmul, (2 * q4 + j) * 4) * (a.soft_cap != 0.f ? a.sm_scale : a.sm_scale * kLog2e);
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) qsum[g][j] = __shfl_sync(0xffffffffu, sum[g] * unit, (2 * q4 + j) * 4);
+                }
             }
             // O^T tiles: tile t of group g has this lane's dims g * kGroup + g8 * (kGroup / 8) + 2 t (C rows g8) and
             // + 1 (rows g8 + 8, 4 bits higher), columns (query rows) 2 q4, 2 q4 + 1; psum: the sums of P s
@@ -226,7 +238,6 @@ __global__ void __launch_bounds__(G4Dec<D, HG>::kThreads) g4_decode_kernel(const
             for (int g = 0; g < NG; ++g) psum[g][0] = psum[g][1] = psum[g][2] = psum[g][3] = mid[g][0] = mid[g][1] = 0.f;
             float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
             const float cap = a.soft_cap, cap_k2 = cap != 0.f ? 2.f * kLog2e / cap : 0.f;
-            const float to_log2 = cap != 0.f ? a.sm_scale : a.sm_scale * kLog2e;
             const int kk = g4_key_of(g8);
 
             for (int blk = 0; blk < n_blocks; ++blk) {
@@ -236,145 +247,166 @@ __global__ void __launch_bounds__(G4Dec<D, HG>::kThreads) g4_decode_kernel(const
                     break;
                 }
                 if (head_ok) {
-                    const uint8_t* stg = smem + st * T::kStage + warp * F::kRow;
-                    const uint8_t* r0 = stg + kk * T::kPitch;  // this lane's keys
-                    const uint8_t* r1 = r0 + 8 * T::kPitch;
-                    const int key0 = kb + blk * BK + kk;
-                    uint32_t ks[2][NG], vs[2][NG];  // (s, m) of K's and V's groups
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint4* p = reinterpret_cast<const uint4*>((h ? r1 : r0) + F::kParams);
-                        if constexpr (NG == 2) {
-                            const uint4 v = p[0];
-                            ks[h][0] = v.x; ks[h][1] = v.y; vs[h][0] = v.z; vs[h][1] = v.w;
-                        } else {
-                            const uint4 u = p[0], v = p[1];
-                            ks[h][0] = u.x; ks[h][1] = u.y; ks[h][2] = u.z; ks[h][3] = u.w;
-                            vs[h][0] = v.x; vs[h][1] = v.y; vs[h][2] = v.z; vs[h][3] = v.w;
+                    for (int sub = 0; sub < 2; sub += T::NT) {
+                        constexpr int NT = T::NT;
+                        const int b0 = kb + blk * BK + 16 * sub;  // the tiles' first key
+                        if (NT == 1 && b0 >= ke) break;
+                        const uint8_t* stg = smem + st * T::kStage + 16 * sub * T::kPitch + warp * F::kRow;
+                        const uint8_t* r0 = stg + kk * T::kPitch;  // this lane's keys: kk and kk + 8 of a tile
+                        float sc[NT][4];
+                        uint32_t vs[NT][2][NG];  // (s, m) of V's groups
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            const uint8_t* rt = r0 + 16 * t * T::kPitch;
+                            uint32_t ks[2][NG];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const uint4* p = reinterpret_cast<const uint4*>(rt + 8 * h * T::kPitch + F::kParams);
+                                if constexpr (NG == 2) {
+                                    const uint4 v = p[0];
+                                    ks[h][0] = v.x; ks[h][1] = v.y; vs[t][h][0] = v.z; vs[t][h][1] = v.w;
+                                } else {
+                                    const uint4 u = p[0], v = p[1];
+                                    ks[h][0] = u.x; ks[h][1] = u.y; ks[h][2] = u.z; ks[h][3] = u.w;
+                                    vs[t][h][0] = v.x; vs[t][h][1] = v.y; vs[t][h][2] = v.z; vs[t][h][3] = v.w;
+                                }
+                            }
+                            // S^T [16 keys x 8 rows], a group at a time
+                            sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
+#pragma unroll
+                            for (int g = 0; g < NG; ++g) {
+                                uint32_t x0[KW], x1[KW];
+                                const uint8_t* at = rt + g * (F::kGroup / 2) + q4 * (F::kGroup / 8);
+                                if constexpr (KW == 2) {
+                                    const uint2 u = *reinterpret_cast<const uint2*>(at), v = *reinterpret_cast<const uint2*>(at + 8 * T::kPitch);
+                                    x0[0] = u.x; x0[1] = u.y; x1[0] = v.x; x1[1] = v.y;
+                                } else {
+                                    x0[0] = *reinterpret_cast<const uint32_t*>(at);
+                                    x1[0] = *reinterpret_cast<const uint32_t*>(at + 8 * T::kPitch);
+                                }
+                                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                                for (int wd = 0; wd < KW; ++wd) {
+                                    const uint32_t u = x0[wd], v = x1[wd], u8 = u >> 8, v8 = v >> 8;
+                                    const uint32_t f0[4] = {u & 0x000f000fu, v & 0x000f000fu, u & 0x00f000f0u, v & 0x00f000f0u};
+                                    const uint32_t f1[4] = {u8 & 0x000f000fu, v8 & 0x000f000fu, u8 & 0x00f000f0u, v8 & 0x00f000f0u};
+                                    mma_bf16(acc, f0, qb[2 * (g * KW + wd)][0], qb[2 * (g * KW + wd)][1]);
+                                    mma_bf16(acc, f1, qb[2 * (g * KW + wd) + 1][0], qb[2 * (g * KW + wd) + 1][1]);
+                                }
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    sc[t][e] = fmaf(bf16_lo(ks[e >> 1][g]), acc[e], fmaf(bf16_hi(ks[e >> 1][g]), qsum[g][e & 1], sc[t][e]));
+                            }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) sc[t][e] *= to_log2[e & 1];
                         }
-                    }
-                    // S^T [16 keys x 8 rows], a group at a time
-                    float sc[4] = {0.f, 0.f, 0.f, 0.f};
+                        if (cap != 0.f) {
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        uint32_t x0[KW], x1[KW];
-                        const int off = g * (F::kGroup / 2) + q4 * (F::kGroup / 8);
-                        if constexpr (KW == 2) {
-                            const uint2 u = *reinterpret_cast<const uint2*>(r0 + off), v = *reinterpret_cast<const uint2*>(r1 + off);
-                            x0[0] = u.x; x0[1] = u.y; x1[0] = v.x; x1[1] = v.y;
-                        } else {
-                            x0[0] = *reinterpret_cast<const uint32_t*>(r0 + off);
-                            x1[0] = *reinterpret_cast<const uint32_t*>(r1 + off);
+                            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) sc[t][e] = soft_cap(sc[t][e], cap, cap_k2) * kLog2e;
                         }
-                        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                        if (b0 < all_lo || b0 + 16 * NT - 1 > all_hi) {
 #pragma unroll
-                        for (int wd = 0; wd < KW; ++wd) {
-                            const uint32_t u = x0[wd], v = x1[wd], u8 = u >> 8, v8 = v >> 8;
-                            const uint32_t f0[4] = {u & 0x000f000fu, v & 0x000f000fu, u & 0x00f000f0u, v & 0x00f000f0u};
-                            const uint32_t f1[4] = {u8 & 0x000f000fu, v8 & 0x000f000fu, u8 & 0x00f000f0u, v8 & 0x00f000f0u};
-                            mma_bf16(acc, f0, qb[2 * (g * KW + wd)][0], qb[2 * (g * KW + wd)][1]);
-                            mma_bf16(acc, f1, qb[2 * (g * KW + wd) + 1][0], qb[2 * (g * KW + wd) + 1][1]);
+                            for (int t = 0; t < NT; ++t) {
+                                bool seen[2] = {false, false};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const int j = e & 1, key = b0 + 16 * t + kk + (e >> 1) * 8;
+                                    const bool ok = key <= qpos[j] && key >= wlo[j] && key < ke;
+                                    sc[t][e] = ok ? sc[t][e] : -INFINITY;
+                                    seen[e >> 1] |= ok;
+                                }
+                                // a key that neither of this lane's rows sees counts as zeros, whatever lies there
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                    for (int g = 0; g < NG; ++g) vs[t][h][g] = seen[h] ? vs[t][h][g] : 0u;
+                            }
                         }
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            sc[e] = fmaf(bf16_lo(ks[e >> 1][g]), acc[e] * colmul[e & 1], fmaf(bf16_hi(ks[e >> 1][g]), qsum[g][e & 1], sc[e]));
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        sc[e] *= to_log2;
-                        if (cap != 0.f) sc[e] = soft_cap(sc[e], cap, cap_k2) * kLog2e;
-                    }
-                    const int b0 = kb + blk * BK;
-                    if (b0 < all_lo || b0 + BK - 1 > all_hi) {
-                        bool seen[2] = {false, false};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int j = e & 1, key = key0 + (e >> 1) * 8;
-                            const bool ok = key <= qpos[j] && key >= wlo[j] && key < ke;
-                            sc[e] = ok ? sc[e] : -INFINITY;
-                            seen[e >> 1] |= ok;
-                        }
-                        // a key that neither of this lane's rows sees counts as zeros, whatever lies there
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int g = 0; g < NG; ++g) vs[h][g] = seen[h] ? vs[h][g] : 0u;
-                    }
-                    float mx[2] = {fmaxf(sc[0], sc[2]), fmaxf(sc[1], sc[3])};
-                    // the reference maximum moves only when a row's has grown by more than 2^8
-                    bool grown = false;
-                    float muse[2];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 4));
-                        mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 8));
-                        mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 16));
-                        grown |= mx[j] > m_run[j] + 8.f;
-                    }
-                    if (__any_sync(0xffffffffu, grown)) {
+                        // the reference maximum moves only when a row's has grown by more than 2^8
+                        float mx[2], muse[2];
+                        bool grown = false;
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            const bool g = mx[j] > m_run[j] + 8.f;
-                            const float f = g ? fast_exp2(m_run[j] - mx[j]) : 1.f;
-                            if (g) m_run[j] = mx[j];
-                            l_run[j] *= f;
+                            mx[j] = fmaxf(sc[0][j], sc[0][2 + j]);
+                            if (NT == 2) mx[j] = fmax3(mx[j], sc[NT - 1][j], sc[NT - 1][2 + j]);
+                            mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 4));
+                            mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 8));
+                            mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 16));
+                            grown |= mx[j] > m_run[j] + 8.f;
+                        }
+                        if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
-                            for (int i = 0; i < NG * TG; ++i) {
-                                o[i][j] *= f;
-                                o[i][2 + j] *= f;
+                            for (int j = 0; j < 2; ++j) {
+                                const bool g = mx[j] > m_run[j] + 8.f;
+                                const float f = g ? fast_exp2(m_run[j] - mx[j]) : 1.f;
+                                if (g) m_run[j] = mx[j];
+                                l_run[j] *= f;
+#pragma unroll
+                                for (int i = 0; i < NG * TG; ++i) {
+                                    o[i][j] *= f;
+                                    o[i][2 + j] *= f;
+                                }
+#pragma unroll
+                                for (int i = 0; i < NG; ++i) {
+                                    psum[i][j] *= f;
+                                    mid[i][j] *= f;
+                                }
                             }
+                        }
 #pragma unroll
-                            for (int i = 0; i < NG; ++i) {
-                                psum[i][j] *= f;
-                                mid[i][j] *= f;
+                        for (int j = 0; j < 2; ++j) muse[j] = m_run[j] == -INFINITY ? 0.f : m_run[j];
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                sc[t][e] = fast_exp2(sc[t][e] - muse[e & 1]);
+                                l_run[e & 1] += sc[t][e];
                             }
-                        }
-                    }
+                        // O^T [16 dims x 8 rows] += V^T (P s)^T, a group at a time; A = V^T from the keys of rows 2 q4,
+                        // 2 q4 + 1, 2 q4 + 8, 2 q4 + 9: a byte permute pairs two keys' numbers
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) muse[j] = m_run[j] == -INFINITY ? 0.f : m_run[j];
+                        for (int t = 0; t < NT; ++t) {
+                            const uint8_t* va = stg + (16 * t + g4_key_of(2 * q4)) * T::kPitch + F::kPart + g8 * (F::kGroup / 16);
+                            const uint8_t* vb = stg + (16 * t + g4_key_of(2 * q4 + 1)) * T::kPitch + F::kPart + g8 * (F::kGroup / 16);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        sc[e] = fast_exp2(sc[e] - muse[e & 1]);
-                        l_run[e & 1] += sc[e];
-                    }
-                    // O^T [16 dims x 8 rows] += V^T (P s)^T, a group at a time; A = V^T from the keys of rows 2 q4,
-                    // 2 q4 + 1, 2 q4 + 8, 2 q4 + 9: a byte permute pairs two keys' numbers
-                    const uint8_t* va = stg + g4_key_of(2 * q4) * T::kPitch + F::kPart;
-                    const uint8_t* vb = stg + g4_key_of(2 * q4 + 1) * T::kPitch + F::kPart;
+                            for (int g = 0; g < NG; ++g) {
+                                const int off = g * (F::kGroup / 2);
+                                uint32_t wa, wb, wc, wd;
+                                if constexpr (F::kGroup == 64) {
+                                    wa = *reinterpret_cast<const uint32_t*>(va + off);
+                                    wb = *reinterpret_cast<const uint32_t*>(vb + off);
+                                    wc = *reinterpret_cast<const uint32_t*>(va + 8 * T::kPitch + off);
+                                    wd = *reinterpret_cast<const uint32_t*>(vb + 8 * T::kPitch + off);
+                                } else {
+                                    wa = *reinterpret_cast<const uint16_t*>(va + off);
+                                    wb = *reinterpret_cast<const uint16_t*>(vb + off);
+                                    wc = *reinterpret_cast<const uint16_t*>(va + 8 * T::kPitch + off);
+                                    wd = *reinterpret_cast<const uint16_t*>(vb + 8 * T::kPitch + off);
+                                }
+                                float ps[4];
 #pragma unroll
-                    for (int g = 0; g < NG; ++g) {
-                        const int off = g * (F::kGroup / 2) + g8 * (F::kGroup / 16);
-                        uint32_t wa, wb, wc, wd;
-                        if constexpr (F::kGroup == 64) {
-                            wa = *reinterpret_cast<const uint32_t*>(va + off);
-                            wb = *reinterpret_cast<const uint32_t*>(vb + off);
-                            wc = *reinterpret_cast<const uint32_t*>(va + 8 * T::kPitch + off);
-                            wd = *reinterpret_cast<const uint32_t*>(vb + 8 * T::kPitch + off);
-                        } else {
-                            wa = *reinterpret_cast<const uint16_t*>(va + off);
-                            wb = *reinterpret_cast<const uint16_t*>(vb + off);
-                            wc = *reinterpret_cast<const uint16_t*>(va + 8 * T::kPitch + off);
-                            wd = *reinterpret_cast<const uint16_t*>(vb + 8 * T::kPitch + off);
-                        }
-                        float ps[4];
+                                for (int e = 0; e < 4; ++e) {
+                                    const float sv = bf16_lo(vs[t][e >> 1][g]);
+                                    ps[e] = sc[t][e] * (sv * 0x1p64f);
+                                    mid[g][e & 1] = fmaf(sc[t][e], fmaf(7.5f, sv, bf16_hi(vs[t][e >> 1][g])), mid[g][e & 1]);
+                                }
+                                const uint32_t pb0 = movmatrix_t(pack_bf16(ps[0], ps[1])), pb1 = movmatrix_t(pack_bf16(ps[2], ps[3]));
+                                const uint32_t ones[4] = {0x00010001u, 0x00010001u, 0x00010001u, 0x00010001u};
+                                mma_bf16(psum[g], ones, pb0, pb1);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float sv = bf16_lo(vs[e >> 1][g]);
-                            ps[e] = sc[e] * (sv * 0x1p64f);
-                            mid[g][e & 1] = fmaf(sc[e], fmaf(7.5f, sv, bf16_hi(vs[e >> 1][g])), mid[g][e & 1]);
-                        }
-                        const uint32_t b0 = movmatrix_t(pack_bf16(ps[0], ps[1])), b1 = movmatrix_t(pack_bf16(ps[2], ps[3]));
-                        const uint32_t ones[4] = {0x00010001u, 0x00010001u, 0x00010001u, 0x00010001u};
-                        mma_bf16(psum[g], ones, b0, b1);
-#pragma unroll
-                        for (int half = 0; half < TG / 2; ++half) {
-                            const uint32_t u = half ? __byte_perm(wa, wb, 0x7632) : __byte_perm(wa, wb, 0x5410);
-                            const uint32_t v = half ? __byte_perm(wc, wd, 0x7632) : __byte_perm(wc, wd, 0x5410);
-                            const uint32_t u8 = u >> 8, v8 = v >> 8;
-                            const uint32_t f0[4] = {u & 0x000f000fu, u & 0x00f000f0u, v & 0x000f000fu, v & 0x00f000f0u};
-                            const uint32_t f1[4] = {u8 & 0x000f000fu, u8 & 0x00f000f0u, v8 & 0x000f000fu, v8 & 0x00f000f0u};
-                            mma_bf16(o[g * TG + 2 * half], f0, b0, b1);
-                            mma_bf16(o[g * TG + 2 * half + 1], f1, b0, b1);
+                                for (int half = 0; half < TG / 2; ++half) {
+                                    const uint32_t u = half ? __byte_perm(wa, wb, 0x7632) : __byte_perm(wa, wb, 0x5410);
+                                    const uint32_t v = half ? __byte_perm(wc, wd, 0x7632) : __byte_perm(wc, wd, 0x5410);
+                                    const uint32_t u8 = u >> 8, v8 = v >> 8;
+                                    const uint32_t f0[4] = {u & 0x000f000fu, u & 0x00f000f0u, v & 0x000f000fu, v & 0x00f000f0u};
+                                    const uint32_t f1[4] = {u8 & 0x000f000fu, u8 & 0x00f000f0u, v8 & 0x000f000fu, v8 & 0x00f000f0u};
+                                    mma_bf16(o[g * TG + 2 * half], f0, pb0, pb1);
+                                    mma_bf16(o[g * TG + 2 * half + 1], f1, pb0, pb1);
+                                }
+                            }
                         }
                     }
                 }
@@ -459,8 +491,7 @@ __global__ void __launch_bounds__(G4Dec<D, HG>::kThreads) g4_decode_kernel(const
     }
     // after an abort, wait (bounded) until no bulk copy can still land in this CTA's memory
     if (producer && lane == 0 && s_abort) {
-        for (int st = 0; st < STAGES; ++st)
-            if (issued_phase[st]) mbar_wait(&full[st], issued_phase[st] - 1, err);
+        for (uint32_t i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i) mbar_wait(&full[i % STAGES], (i / STAGES) & 1, err);
     }
     if (tid == 0 && (int)blockIdx.x < n_static) atomicAdd(&hdr->next_item[0], 1);
     // started early beside the prefill grid: end after it, so that later launches see the plain order

@@ -259,6 +259,10 @@ struct MlaUpdateArgs {
 // Key weights: a warp's piece of a row tile's keys is at least kKwMinPiece keys, and about kKwTarget of them are made;
 // the second kernel's items are kKwChunk keys.
 constexpr int kKwMinPiece = 128, kKwTarget = 8192, kKwChunk = 128;
+// A sequence of one row tile leaves its scores in the workspace, as far as kKwScores floats of it go (half a GB), and
+// its items of the third kernel are kKwLong keys.
+constexpr long long kKwScores = 1ll << 27;
+constexpr int kKwLong = 512;
 
 struct KwArgs {
     const __nv_bfloat16* q;
@@ -277,8 +281,13 @@ struct KwArgs {
     WsHeader* hdr;
     int* ends_a;                    // [max_num_seqs] ends of the sequences' items of either kernel
     int* ends_b;
+    int* ends_c;
+    int* score_at;                  // [max_num_seqs] first place of a sequence's scores, in units of 64 floats; -1: none
+    float* scores;                  // [kv head][key][rows, 4, 8 or 16]
+    long long max_scores;
     float2* stats;                  // 16 rows' (maximum, sum) an item of the first
     int max_items;                  // of the first
+    int all_stored;                 // no sequence can be left for the recomputing kernel
 };
 
 struct EvictArgs {
@@ -293,7 +302,8 @@ struct EvictArgs {
     float* weights_out;             // may be weights, or null
     int num_kv_heads, row_bytes;    // row_bytes: a key's K and V of one head
     int total_num_pages, page_size, max_num_seqs, pages_per_seq, max_keys, sinks, recent;
-    int held;                       // set by the launch: keys whose order a block holds in shared memory
+    int held, page_shift;           // set by the launch: keys whose order a block holds in shared memory; log2 of a
+                                    // page size that is a power of two, or -1
     // workspace
     uint32_t* err;
     int* kept;                      // [max_num_seqs] keys that stay, -1: left alone

@@ -3,8 +3,9 @@
 //   w_out[key] = keep w_in[key] + sum over the sequence's queries and the group's q heads of 2^(c s - L),
 //   L = log2 of the row's sum of 2^(c s) over the keys it sees, c = sm_scale log2(e), s = q.k (its soft cap, too).
 //
-// Two kernels behind a plan: one finds each row's maximum and sum over pieces of its keys, one computes the
-// scores again, knowing L, and adds up each key's. Items are a warp's: 16 keys fill the M side of m16n8k16, 16
+// Behind a plan one kernel finds each row's maximum and sum over pieces of its keys. Sequences of up to 16 rows a KV head (decodes)
+// leave their scores there, 16 bytes a key for 4 rows beside K's 256 (bf16, D = 128), and a light kernel adds them up;
+// for the others a third computes the scores again, knowing L. Items are a warp's: 16 keys fill the M side of m16n8k16, 16
 // query rows (G heads x tokens) two N sides; a warp copies its K rows (no V) by cp.async a few stages ahead and
 // waits for nobody else. A row's running maximum and sum stay in each lane on the keys it holds, and meet once an item.
 // Scores are exact products in float32: bf16 operands, or the 4-bit numbers as bf16 subnormals with their groups'
@@ -222,27 +223,33 @@ __device__ __forceinline__ void kw_range(const KwArgs& a, const KwSeq& q, int G,
     lo = a.sliding_window > 0 ? max(0, p0 - a.sliding_window + 1) : 0;
 }
 
-// ends of the items of both kernels, a sequence after another, and the keys of a piece
+// Rows a key of stored scores.
+__device__ __forceinline__ int kw_row_slots(int n_rows) { return n_rows <= 4 ? 4 : n_rows <= 8 ? 8 : 16; }
+
+// Ends of the kernels' items, a sequence after another, the keys of a piece, and where sequences of one row tile leave
+// their scores.
 __global__ void __launch_bounds__(1024) kw_plan_kernel(const __grid_constant__ KwArgs a) {
     __shared__ long long scan[40];
     __shared__ float red[32];
-    __shared__ int s_num;
     const int tid = threadIdx.x, lane = tid & 31, G = a.num_q_heads / a.num_kv_heads;
-    pdl_wait();  // (the stream's earlier work may be writing the lengths)
-    if (tid == 0) {
-        int n = a.num_seqs[0];
-        if (n < 0 || n > a.max_num_seqs) {
-            set_error(&a.hdr->error_bits, RPA_DEV_ERR_NUM_SEQS);
-            n = 0;
-        }
-        s_num = n;
+    pdl_launch_dependents();  // (the next kernel waits for this one's end)
+    pdl_wait();               // (the stream's earlier work may be writing the lengths)
+    // the first sequences' numbers in the same round trip as their count
+    const int mine = min(tid, a.max_num_seqs - 1);
+    int c0 = a.cu_q_lens[mine], c1 = a.cu_q_lens[mine + 1], k = a.kv_lens[mine];
+    int num = a.num_seqs[0];
+    if (num < 0 || num > a.max_num_seqs) {
+        if (tid == 0) set_error(&a.hdr->error_bits, RPA_DEV_ERR_NUM_SEQS);
+        num = 0;
     }
-    __syncthreads();
-    const int num = s_num;
     auto shape = [&](int s, int& ql, int& kl) {
         ql = kl = 0;
         if (s >= num) return;
-        const int c0 = a.cu_q_lens[s], c1 = a.cu_q_lens[s + 1], k = a.kv_lens[s];
+        if (s != tid) {
+            c0 = a.cu_q_lens[s];
+            c1 = a.cu_q_lens[s + 1];
+            k = a.kv_lens[s];
+        }
         uint32_t bad = 0;
         if (c0 < 0 || c1 < c0 || c1 > a.max_num_tokens)
             bad = RPA_DEV_ERR_TOKENS;
@@ -259,7 +266,10 @@ __global__ void __launch_bounds__(1024) kw_plan_kernel(const __grid_constant__ K
     };
     // keys x tiles of the batch, cut into about as many pieces as keep the warps busy
     float work = 0.f;
-    for (int s = tid; s < num; s += blockDim.x) {
+    int ql0, kl0;
+    shape(tid, ql0, kl0);
+    work = (float)cdiv(ql0 * G, 16) * (float)kl0 * (float)a.num_kv_heads;
+    for (int s = tid + blockDim.x; s < num; s += blockDim.x) {
         int ql, kl;
         shape(s, ql, kl);
         work += (float)cdiv(ql * G, 16) * (float)kl * (float)a.num_kv_heads;
@@ -269,30 +279,44 @@ __global__ void __launch_bounds__(1024) kw_plan_kernel(const __grid_constant__ K
     __syncthreads();
     work = warp_sum(red[lane]);
     const int piece = max(kKwMinPiece, (int)min((double)work / kKwTarget, 1e9) / kKwBK * kKwBK + kKwBK);
-    int base_a = 0, base_b = 0;
+    int base_a = 0, base_b = 0, base_c = 0;
+    long long base_s = 0;  // scores, in units of 64
     for (int s0 = 0; s0 < num; s0 += blockDim.x) {
-        int ql, kl;
-        shape(s0 + tid, ql, kl);
-        const int na = cdiv(ql * G, 16) * a.num_kv_heads * cdiv(kl, piece), nb = ql ? a.num_kv_heads * cdiv(kl, kKwChunk) : 0;
+        int ql = ql0, kl = kl0;
+        if (s0) shape(s0 + tid, ql, kl);
+        const int rows = ql * G;
         long long total;
-        const long long before = block_exclusive_scan(((long long)na << 32) | nb, scan, &total);
+        const long long want = rows > 0 && rows <= 16 ? (long long)cdiv(kl, 16) * kw_row_slots(rows) / 4 * a.num_kv_heads : 0;
+        const long long at = base_s + block_exclusive_scan(want, scan, &total);
+        base_s += total;
+        const bool stored = want > 0 && (at + want) * 64 <= a.max_scores;
+        // (each count is far below 2^31; the first two share one scan)
+        const int na = cdiv(rows, 16) * a.num_kv_heads * cdiv(kl, piece);
+        const int nb = ql && !stored ? a.num_kv_heads * cdiv(kl, kKwChunk) : 0, nc = stored ? a.num_kv_heads * cdiv(kl, kKwLong) : 0;
+        const long long ab = block_exclusive_scan(((long long)na << 32) | nb, scan, &total);
+        const int total_a = (int)(total >> 32), total_b = (int)(total & 0xffffffffll);
+        const int c = (int)block_exclusive_scan((long long)nc, scan, &total);
         if (s0 + tid < num) {
-            a.ends_a[s0 + tid] = base_a + (int)(before >> 32) + na;
-            a.ends_b[s0 + tid] = base_b + (int)(before & 0xffffffffll) + nb;
+            a.ends_a[s0 + tid] = base_a + (int)(ab >> 32) + na;
+            a.ends_b[s0 + tid] = base_b + (int)(ab & 0xffffffffll) + nb;
+            a.ends_c[s0 + tid] = base_c + c + nc;
+            a.score_at[s0 + tid] = stored ? (int)at : -1;
         }
-        base_a += (int)(total >> 32);
-        base_b += (int)(total & 0xffffffffll);
+        base_a += total_a;
+        base_b += total_b;
+        base_c += (int)total;
     }
     if (tid == 0) {
         if (base_a > a.max_items) {  // (only sequences that claim the same tokens make so many)
             set_error(&a.hdr->error_bits, RPA_DEV_ERR_TOKENS);
-            base_a = base_b = 0;
+            base_a = base_b = base_c = 0;
         }
         a.hdr->num_items[0] = base_a;
         a.hdr->num_items[1] = base_b;
         a.hdr->num_items[2] = num;
+        a.hdr->num_items[3] = base_c;
         a.hdr->chunk_keys = piece;
-        a.hdr->next_item[0] = a.hdr->next_item[1] = 0;
+        a.hdr->next_item[0] = a.hdr->next_item[1] = a.hdr->next_item[2] = 0;
     }
 }
 
@@ -349,6 +373,7 @@ __global__ void __launch_bounds__(kKwWarps * 32) kw_stats_kernel(const __grid_co
     // rows that are never copied stay finite
     for (int i = threadIdx.x * 16; i < T::kSmem; i += blockDim.x * 16) *reinterpret_cast<uint4*>(smem + i) = make_uint4(0, 0, 0, 0);
     __syncthreads();
+    pdl_launch_dependents();  // (the kernels behind wait for this grid's end)
     pdl_wait();
     const int n_items = a.hdr->num_items[0], num = a.hdr->num_items[2], piece = a.hdr->chunk_keys;
     while (true) {
@@ -361,8 +386,11 @@ __global__ void __launch_bounds__(kKwWarps * 32) kw_stats_kernel(const __grid_co
         const int split = rel % splits, tile = rel / splits % q.tiles, head = rel / (splits * q.tiles), row0 = 16 * tile;
         int lo, hi;
         kw_range(a, q, G, row0, lo, hi);
-        const int k0 = max(split * piece, lo / kKwBK * kKwBK), ke = min(hi, (split + 1) * piece);
+        const int store = a.score_at[s], slots = kw_row_slots(q.n_rows);
+        // (stored scores are there for every key, also those that a window hides)
+        const int k0 = max(split * piece, store >= 0 ? 0 : lo / kKwBK * kKwBK), ke = min(hi, (split + 1) * piece);
         const bool two = q.n_rows - row0 > 8;
+        float* to = store >= 0 ? a.scores + (size_t)store * 64 + (size_t)head * cdiv(q.kv_len, 16) * 16 * slots + 2 * q4 : nullptr;
         float m[2][2], l[2][2];
         int at[2][2];
 #pragma unroll
@@ -389,6 +417,11 @@ __global__ void __launch_bounds__(kKwWarps * 32) kw_stats_kernel(const __grid_co
                         const bool seen = key <= p && key < ke && (a.sliding_window == 0 || key > p - a.sliding_window);
                         sc[nt][e] = seen ? kw_log2(a, sc[nt][e]) : -INFINITY;
                     }
+                    if (to && 8 * nt + 2 * q4 < slots) {
+                        float* at_key = to + (size_t)(k0 + j * kKwBK + g8) * slots + 8 * nt;
+                        *reinterpret_cast<float2*>(at_key) = make_float2(sc[nt][0], sc[nt][1]);
+                        *reinterpret_cast<float2*>(at_key + 8 * slots) = make_float2(sc[nt][2], sc[nt][3]);
+                    }
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         const float mx = fmaxf(sc[nt][c], sc[nt][2 + c]);
@@ -414,6 +447,70 @@ __global__ void __launch_bounds__(kKwWarps * 32) kw_stats_kernel(const __grid_co
                 for (int o = 4; o < 32; o *= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
                 if (g8 == 0) a.stats[(size_t)item * 16 + 8 * nt + 2 * q4 + j] = make_float2(M, v);
             }
+    }
+}
+
+// L of row lane of a tile (lanes below 16), from its pieces; infinity for a row that is not there.
+__device__ __forceinline__ float kw_norm(const KwArgs& a, int first_a, int head, int tile, const KwSeq& q, int splits) {
+    const int lane = threadIdx.x & 31;
+    if (lane >= 16 || 16 * tile + lane >= q.n_rows) return INFINITY;
+    const float2* st = a.stats + ((size_t)first_a + ((size_t)head * q.tiles + tile) * splits) * 16 + lane;
+    float M = -INFINITY, sum = 0.f;
+#pragma unroll 8
+    for (int i = 0; i < splits; ++i) {
+        const float2 v = st[(size_t)i * 16];
+        const float n = fmaxf(M, v.x), u = n == -INFINITY ? 0.f : n;
+        sum = sum * fast_exp2(M - u) + v.y * fast_exp2(v.x - u);
+        M = n;
+    }
+    return M + log2f(sum);
+}
+
+// The keys of sequences whose scores are stored: a warp takes kKwLong keys of a head, a key a lane.
+template <int R>
+__device__ __forceinline__ void kw_finish(const KwArgs& a, float L, const float* scores, const int* tbl, int head, int c0, int c1) {
+    const int lane = threadIdx.x & 31;
+    float Lr[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) Lr[r] = __shfl_sync(0xffffffffu, L, r);
+#pragma unroll 4
+    for (int key = c0 + lane; key < c1; key += 32) {
+        const float4* p = reinterpret_cast<const float4*>(scores + (size_t)key * R);
+        float v = 0.f;
+#pragma unroll
+        for (int r = 0; r < R / 4; ++r) {
+            const float4 x = __ldcs(p + r);
+            v += (fast_exp2(x.x - Lr[4 * r]) + fast_exp2(x.y - Lr[4 * r + 1])) + (fast_exp2(x.z - Lr[4 * r + 2]) + fast_exp2(x.w - Lr[4 * r + 3]));
+        }
+        const int p_at = key / a.page_size, page = __ldg(tbl + p_at);
+        if ((unsigned)page < (unsigned)a.total_num_pages) {
+            const size_t o = ((size_t)page * a.num_kv_heads + head) * a.page_size + (key - p_at * a.page_size);
+            a.weights_out[o] = a.keep == 0.f ? v : fmaf(a.keep, a.weights[o], v);
+        }
+    }
+}
+__global__ void __launch_bounds__(kKwWarps * 32) kw_finish_kernel(const __grid_constant__ KwArgs a) {
+    const int G = a.num_q_heads / a.num_kv_heads;
+    pdl_launch_dependents();  // (the kernel behind works on other sequences' keys, and waits for this one's end)
+    pdl_wait();
+    const int n_items = a.hdr->num_items[3], num = a.hdr->num_items[2], piece = a.hdr->chunk_keys;
+    while (true) {
+        const int item = kw_take(&a.hdr->next_item[2]);
+        if (item >= n_items) break;
+        int first;
+        const int s = kw_find(a.ends_c, num, item, first), first_a = s > 0 ? a.ends_a[s - 1] : 0, store = a.score_at[s];
+        const KwSeq q = kw_seq(a, s, G);
+        const int chunks = cdiv(q.kv_len, kKwLong), rel = item - first, head = rel / chunks, c0 = rel % chunks * kKwLong;
+        const int c1 = min(q.kv_len, c0 + kKwLong), slots = kw_row_slots(q.n_rows);
+        const float L = kw_norm(a, first_a, head, 0, q, cdiv(q.kv_len, piece));
+        const float* scores = a.scores + (size_t)store * 64 + (size_t)head * cdiv(q.kv_len, 16) * 16 * slots;
+        const int* tbl = a.page_indices + (size_t)s * a.pages_per_seq;
+        if (slots == 4)
+            kw_finish<4>(a, L, scores, tbl, head, c0, c1);
+        else if (slots == 8)
+            kw_finish<8>(a, L, scores, tbl, head, c0, c1);
+        else
+            kw_finish<16>(a, L, scores, tbl, head, c0, c1);
     }
 }
 
@@ -447,21 +544,7 @@ __global__ void __launch_bounds__(kKwWarps * 32) kw_sum_kernel(const __grid_cons
             kw_range(a, q, G, row0, lo, hi);
             if (hi <= c0 || lo >= c1) continue;
             const bool two = q.n_rows - row0 > 8;
-            // L of this lane's rows: lane r < 16 joins row r's pieces
-            float L = INFINITY;
-            if (lane < 16 && row0 + lane < q.n_rows) {
-                const float2* st = a.stats + ((size_t)first_a + ((size_t)head * q.tiles + tile) * splits) * 16 + lane;
-                float M = -INFINITY, sum = 0.f;
-                for (int i = 0; i < splits; ++i) {
-                    const float2 v = st[(size_t)i * 16];
-                    const float n = fmaxf(M, v.x);
-                    if (n > -INFINITY) {
-                        sum = sum * fast_exp2(M - n) + v.y * fast_exp2(v.x - n);
-                        M = n;
-                    }
-                }
-                L = M + log2f(sum);
-            }
+            const float L = kw_norm(a, first_a, head, tile, q, splits);
             float Lc[2][2];
             int at[2][2];
 #pragma unroll
@@ -533,19 +616,26 @@ static cudaError_t launch_kw(const KwArgs& a, int num_sms, cudaStream_t stream) 
         if (e != cudaSuccess) return e;
         per_sm[dev][i] = n > 0 ? n : 1;
     }
+    const bool pdl = !prof_enabled();
     {
         ProfScope ps("rpa_kw_stats", stream);
-        e = launch_pdl(kern[0], dim3(num_sms * per_sm[dev][0]), dim3(kKwWarps * 32), T::kSmem, stream, false, a);
+        e = launch_pdl(kern[0], dim3(num_sms * per_sm[dev][0]), dim3(kKwWarps * 32), T::kSmem, stream, pdl, a);
     }
     if (e != cudaSuccess) return e;
+    {
+        ProfScope ps("rpa_kw_finish", stream);
+        e = launch_pdl(kw_finish_kernel, dim3(num_sms * 8), dim3(kKwWarps * 32), 0, stream, pdl, a);
+    }
+    // (so few query rows that every sequence has one tile, and the workspace room for all their scores: nothing is left)
+    if (e != cudaSuccess || a.all_stored) return e;
     ProfScope ps("rpa_kw_sum", stream);
-    return launch_pdl(kern[1], dim3(num_sms * per_sm[dev][1]), dim3(kKwWarps * 32), T::kSmem, stream, false, a);
+    return launch_pdl(kern[1], dim3(num_sms * per_sm[dev][1]), dim3(kKwWarps * 32), T::kSmem, stream, pdl, a);
 }
 
 cudaError_t launch_key_weights(const KwArgs& a, int head_dim, bool g4, int num_sms, cudaStream_t stream) {
     {
         ProfScope ps("rpa_kw_plan", stream);
-        const cudaError_t e = launch_pdl(kw_plan_kernel, dim3(1), dim3(1024), 0, stream, false, a);
+        const cudaError_t e = launch_pdl(kw_plan_kernel, dim3(1), dim3(1024), 0, stream, !prof_enabled(), a);
         if (e != cudaSuccess) return e;
     }
     switch (head_dim) {
