@@ -3,14 +3,15 @@
 //
 //   S = Q K^T, P = 2^(c S - m), O += P V, l += sum P, out = O / l, K = s n + m and V = s n + m rounded to bf16.
 //
-// Tiles of 128 rows (token, q head of the group; a row a thread), blocks of 128 keys (64 at head_dim 256). Four warps
+// Tiles of 128 rows (token, q head of the group; a row a thread), blocks of 128 keys (64 at head_dim 256). Eight warps
 // turn the 4-bit rows into the bf16 panels that the products read: a thread a row, which it has brought to shared
 // memory itself by cp.async (any page size, no barrier on the way), 8 numbers in some 20 instructions (a permute and a
 // mask put two numbers into the halves as 128 + n, one subtraction and one fused multiply-add give both values, the
 // latter rounding once). Two tiles of a KV head (head_dim 64 and 128) share each converted block, and while
 // one's softmax runs the tensor pipe works for the other; at head_dim 256 tensor memory holds one tile.
 // The rounding of K and V to bf16 (2^-9 of a value) is what a bf16 cache has too.
-// Warps: 4 softmax warps a tile; an MMA issuer a tile; one that takes items and loads Q; one idle; 4 converters.
+// Warps: 4 softmax warps a tile; an MMA issuer a tile; one that takes items and loads Q; the rest of a warpgroup idle; 4
+// converters for K and 4 for V.
 // Barriers, all waits bounded: k/v_full, k/v_empty (panels), q_full, q_empty, item_full/empty; per tile s_full (QK
 // done), s_free (scores loaded), p_full (P written, O rescaled), pv_done, o_empty.
 #include <cuda.h>
@@ -39,7 +40,13 @@ struct G4Pre {
     static constexpr bool ONE_S = D == 128;                // the two tiles take turns with one S buffer
     static constexpr int NK = 2, NV = D == 64 ? 2 : 1;
     static constexpr int NR = 3;                           // raw blocks on their way
-    static constexpr int kRaw = BK * G4<D>::kRow;
+    // converters: 4 warps for K and 4 for V, a row (head_dim 256: half a row) a thread, which has a place of its own for
+    // each raw block: its numbers and 16 bytes with their scales
+    static constexpr int TPR = D == 256 ? 2 : 1;           // threads a row
+    static constexpr int DT = D / TPR;                     // dims a thread
+    static constexpr int kOwn = DT / 2 + 16;
+    static constexpr int kRaw = 256 * kOwn;
+    static_assert(BK * TPR == 128 && kOwn / 16 % 2 == 1, "a thread's share; 8 threads' loads touch every bank once");
     static constexpr int kOffK = TILES * kQTile;
     static constexpr int kOffV = kOffK + NK * kTile;
     static constexpr int kOffRaw = kOffV + NV * kTile;
@@ -48,14 +55,14 @@ struct G4Pre {
     static constexpr int kOffItem = (kOffBar + kBars * 8 + 15) / 16 * 16;  // [2] G4Item, abort, TMEM base, exit
     static constexpr int kSmem = kOffItem + 2 * (int)sizeof(G4Item) + 16;
     static constexpr int kSoft = 4 * TILES;
-    static constexpr int kThreads = (kSoft + 8) * 32;
+    static constexpr int kThreads = (kSoft + 12) * 32;
     static constexpr int kColS = 0, kColSStep = ONE_S ? 0 : BK;
     static constexpr int kColP = ONE_S ? BK : TILES * BK, kColO = kColP + TILES * (BK / 2);
     static constexpr int kTmemCols = 512;
     // registers: the launch's share of the SM, dealt out again by warpgroup (setmaxnreg)
-    static constexpr int kRegsLaunch = TILES == 2 ? 128 : 168;
-    static constexpr int kRegsSoft = 192, kRegsRest = 64;
-    static_assert(TILES == 1 || 256 * kRegsSoft + 256 * kRegsRest <= kThreads * kRegsLaunch, "register split");
+    static constexpr int kRegsLaunch = TILES == 2 ? 96 : 128;
+    static constexpr int kRegsSoft = 160, kRegsMma = 56, kRegsConv = 48;
+    static_assert(TILES == 1 || 256 * kRegsSoft + 128 * kRegsMma + 256 * kRegsConv <= kThreads * kRegsLaunch, "register split");
     static_assert(kSmem <= 232448 && kOffK % 1024 == 0 && kOffV % 1024 == 0 && kOffRaw % 16 == 0 && kOffBar % 8 == 0, "shared memory");
     static_assert(kColO + TILES * D <= kTmemCols, "tensor memory");
 };
@@ -123,7 +130,7 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
 
     if (tid == 0) {
         for (int i = 0; i < NK; ++i) {
-            mbar_init(&k_full[i], 4);
+            mbar_init(&k_full[i], 4);  // (converter warps)
             mbar_init(&k_empty[i], TILES);
         }
         for (int i = 0; i < NV; ++i) {
@@ -299,8 +306,8 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
             }
             if (!ok) s_abort = 1;
         }
-    } else {
-        if constexpr (TILES == 2) g4_regs_dec<T::kRegsRest>();
+    } else if (warp < kConv0) {
+        if constexpr (TILES == 2) g4_regs_dec<T::kRegsMma>();
         if (warp >= kMma0 && warp < kMma0 + TILES) {
             // ---------------- MMA issuer of tile t (a constant in either branch) ----------------
             // One lane, elected once, does all of it: the ring positions and phases are its registers, and a commit
@@ -463,96 +470,99 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
                 if (items > 0) mbar_wait(q_full, (items - 1) & 1, err);
             }
             __syncwarp();
-        } else if (warp >= kConv0) {
-            // ---------------- converters: a thread a row, or (head_dim 256) half of one ----------------
-            constexpr int TPR = D == 256 ? 2 : 1;        // threads a row
-            constexpr int DT = D / TPR;                  // dims of K (and V) a thread
-            constexpr int CH = DT / 32;                  // 16-byte chunks of them
-            static_assert(BK * TPR == 128, "a thread's share");
-            const int ct = tid - kConv0 * 32, row = ct / TPR, half = ct % TPR;
-            // this thread's bytes of a raw block: its K, its V, the row's parameters
-            uint8_t* const mine = smem + T::kOffRaw + row * F::kRow;
-            const uint8_t* kv = static_cast<const uint8_t*>(a.kv_pages);
-            const size_t slot_bytes = (size_t)a.num_kv_heads * F::kRow;
-            uint32_t jb = 0, jr = 0;  // blocks converted, and raw blocks asked for
-            bool ok = true;
-            while (ok && next_item(it)) {
-                const int* tbl = a.page_indices + (size_t)it.seq * a.pages_per_seq;
-                const int ke = min(it.kv_len, it.kv_len - it.q_len + (min(it.row + 128 * TILES, it.q_len * G) - 1) / G + 1);
-                // (a window leaves out the first block's keys before its first row's)
-                const int k0 = a.sliding_window > 0 ? it.kv_len - it.q_len + it.row / G - a.sliding_window + 1 : 0;
-                const int key_first = it.block0 * BK + row;
-                auto page_of = [&](int j) -> int {
-                    const int key = key_first + j * BK;
-                    return j < it.blocks && key < ke ? __ldg(tbl + key / a.page_size) : -1;
-                };
-                auto ask = [&](int j, int page) {  // block j's row on its way (an empty group where there is none)
-                    const int key = key_first + j * BK;
-                    if (j < it.blocks && key < ke) {
-                        if ((unsigned)page >= (unsigned)a.total_num_pages) {
-                            set_error(err, RPA_DEV_ERR_PAGE);
-                            page = 0;
-                        }
-                        const uint8_t* src = kv + ((size_t)page * a.page_size + key % a.page_size) * slot_bytes + (size_t)it.head * F::kRow;
-                        const uint32_t dst = smem_u32(mine + (jr % NR) * T::kRaw);
-#pragma unroll
-                        for (int part = 0; part < 2; ++part)
-#pragma unroll
-                            for (int c = 0; c < CH; ++c) {
-                                const int off = part * F::kPart + half * (DT / 2) + c * 16;
-                                cp_async16(dst + off, src + off, true);
-                            }
-                        // (both threads of a row bring its parameters: the same bytes)
-#pragma unroll
-                        for (int c = 0; c < F::NG / 2; ++c) cp_async16(dst + F::kParams + c * 16, src + F::kParams + c * 16, true);
-                    }
-                    cp_async_commit();
-                    ++jr;
-                };
-#pragma unroll
-                for (int j = 0; j < NR - 1; ++j) ask(j, page_of(j));
-                int page_next = page_of(NR - 1);
-                for (int j = 0; j < it.blocks; ++j, ++jb) {
-                    const int page = page_next;
-                    page_next = page_of(j + NR);
-                    ask(j + NR - 1, page);
-                    cp_async_wait<NR - 1>();
-                    const uint8_t* src = mine + ((jr - NR) % NR) * T::kRaw;
-                    const bool in = key_first + j * BK < ke && key_first + j * BK >= k0;
-#pragma unroll
-                    for (int part = 0; part < 2; ++part) {
-                        const uint32_t slot = part ? jb % NV : jb % NK, ph = (part ? jb / NV : jb / NK) & 1;
-                        if (!mbar_wait(part ? &v_empty[slot] : &k_empty[slot], ph ^ 1, err)) {
-                            ok = false;
-                            break;
-                        }
-                        uint8_t* stage = smem + (part ? T::kOffV + slot * T::kTile : T::kOffK + slot * T::kTile) + row * 128;
-#pragma unroll
-                        for (int c = 0; c < CH; ++c) {
-                            const int d0 = half * DT + c * 32;
-                            uint32_t sm = *reinterpret_cast<const uint32_t*>(src + F::kParams + 4 * (part * F::NG + d0 / F::kGroup));
-                            if (!in) sm = 0;  // rows that no query sees: zeros, whatever lies there
-                            const uint4 w = *reinterpret_cast<const uint4*>(src + part * F::kPart + d0 / 2);
-                            const uint32_t s2 = __byte_perm(sm, sm, 0x1010), m2 = __byte_perm(sm, sm, 0x3232);
-                            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int chunk = d0 / 8 + e;
-                                *reinterpret_cast<uint4*>(stage + (chunk >> 3) * T::kPanel + (((chunk & 7) ^ (row & 7)) << 4)) = g4_panel8(ww[e], s2, m2);
-                            }
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(part ? &v_full[slot] : &k_full[slot]);
-                    }
-                    if (!ok) break;
-                }
-                cp_async_wait<0>();
-                if (!ok) s_abort = 1;
-            }
         } else {
             while (next_item(it)) {
             }
+        }
+    } else {
+        // ---------------- converters ----------------
+        if constexpr (TILES == 2) g4_regs_dec<T::kRegsConv>();
+        constexpr int CH = T::DT / 32;               // 16-byte chunks of numbers a thread
+        const int ct = (tid - kConv0 * 32) & 127, part = warp >= kConv0 + 4, row = ct / T::TPR, d0 = ct % T::TPR * T::DT;
+        uint8_t* const mine = smem + T::kOffRaw + (part * 128 + ct) * T::kOwn;
+        const uint8_t* kv = static_cast<const uint8_t*>(a.kv_pages);
+        const size_t slot_bytes = (size_t)a.num_kv_heads * F::kRow;
+        const bool pow2 = (a.page_size & (a.page_size - 1)) == 0;
+        const int lps = __ffs(a.page_size) - 1;
+        // offsets in a row of this thread's numbers and of the 16 bytes with its part's scales, whose first word here is
+        // that of group `g0`
+        const int off = part * F::kPart + d0 / 2, off_sm = F::kParams + (F::NG == 4 ? part * 16 : 0);
+        const int word0 = F::NG == 4 ? d0 / F::kGroup : part * F::NG;
+        uint64_t* const full = part ? v_full : k_full;
+        uint64_t* const empty = part ? v_empty : k_empty;
+        const uint32_t ring = part ? NV : NK;
+        uint8_t* const panel = smem + (part ? T::kOffV : T::kOffK) + row * 128;
+        uint32_t slot = 0, ph = 1;                   // panel ring
+        uint32_t ask_slot = 0, get_slot = 0;         // raw ring
+        bool ok = true;
+        while (ok && next_item(it)) {
+            const int* tbl = a.page_indices + (size_t)it.seq * a.pages_per_seq;
+            // keys that some row of the item sees: [k0, ke)
+            const int ke = min(it.kv_len, it.kv_len - it.q_len + (min(it.row + 128 * TILES, it.q_len * G) - 1) / G + 1);
+            const int k0 = a.sliding_window > 0 ? it.kv_len - it.q_len + it.row / G - a.sliding_window + 1 : 0;
+            const int key_end = min(ke, (it.block0 + it.blocks) * BK);
+            int key_ask = it.block0 * BK + row, key = key_ask;
+            auto page_of = [&](int k) -> int { return k < key_end ? __ldg(tbl + (pow2 ? k >> lps : k / a.page_size)) : -1; };
+            auto ask = [&](int page) {  // the row of key_ask on its way (an empty group where there is none)
+                if (key_ask < key_end) {
+                    if ((unsigned)page >= (unsigned)a.total_num_pages) {
+                        set_error(err, RPA_DEV_ERR_PAGE);
+                        page = 0;
+                    }
+                    const int in_page = pow2 ? key_ask & (a.page_size - 1) : key_ask % a.page_size;
+                    const uint8_t* src = kv + ((size_t)page * a.page_size + in_page) * slot_bytes + (size_t)it.head * F::kRow;
+                    const uint32_t dst = smem_u32(mine + ask_slot * T::kRaw);
+#pragma unroll
+                    for (int c = 0; c < CH; ++c) cp_async16(dst + c * 16, src + off + c * 16, true);
+                    cp_async16(dst + T::DT / 2, src + off_sm, true);
+                }
+                cp_async_commit();
+                key_ask += BK;
+                ask_slot = ask_slot + 1 == NR ? 0 : ask_slot + 1;
+            };
+#pragma unroll
+            for (int j = 0; j < NR - 1; ++j) ask(page_of(key_ask));
+            int page_next = page_of(key_ask);
+#pragma unroll 1
+            for (int j = 0; j < it.blocks; ++j) {
+                const int page = page_next;
+                page_next = page_of(key_ask + BK);
+                ask(page);
+                cp_async_wait<NR - 1>();
+                const uint8_t* src = mine + get_slot * T::kRaw;
+                get_slot = get_slot + 1 == NR ? 0 : get_slot + 1;
+                const bool in = key < ke && key >= k0;  // rows that no query sees: zeros, whatever lies there
+                key += BK;
+                if (!mbar_wait(&empty[slot], ph, err)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t* stage = panel + slot * T::kTile;
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    uint32_t sm = *reinterpret_cast<const uint32_t*>(src + T::DT / 2 + 4 * (word0 + c * 32 / F::kGroup));
+                    if (!in) sm = 0;
+                    const uint4 w = *reinterpret_cast<const uint4*>(src + c * 16);
+                    const uint32_t s2 = __byte_perm(sm, sm, 0x1010), m2 = __byte_perm(sm, sm, 0x3232);
+                    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int chunk = d0 / 8 + 4 * c + e;
+                        *reinterpret_cast<uint4*>(stage + (chunk >> 3) * T::kPanel + (((chunk & 7) ^ (row & 7)) << 4)) = g4_panel8(ww[e], s2, m2);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[slot]);
+                if (++slot == ring) {
+                    slot = 0;
+                    ph ^= 1;
+                }
+            }
+            cp_async_wait<0>();
+            // the raw ring starts over with the next item's first block
+            ask_slot = get_slot;
+            if (!ok) s_abort = 1;
         }
     }
     // every role has left its loop
