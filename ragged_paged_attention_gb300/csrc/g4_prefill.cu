@@ -33,18 +33,18 @@ struct __align__(16) G4Item {
 template <int D>
 struct G4Pre {
     static constexpr int TILES = D == 256 ? 1 : 2;
-    static constexpr int BK = D == 256 ? 64 : 128;
+    static constexpr int BK = 64;
     static constexpr int DP = D / 64;                      // 64-wide panels
     static constexpr int kQPanel = 128 * 128, kQTile = DP * kQPanel;
     static constexpr int kPanel = BK * 128, kTile = DP * kPanel;
-    static constexpr bool ONE_S = D == 128;                // the two tiles take turns with one S buffer
-    static constexpr int NK = 2, NV = D == 64 ? 2 : 1;
+    static constexpr bool ONE_S = false;                   // the two tiles take turns with one S buffer
+    static constexpr int NK = D == 256 ? 2 : 3, NV = D == 256 ? 1 : 3;
     static constexpr int NR = 3;                           // raw blocks on their way
     // converters: 4 warps for K and 4 for V, a row (head_dim 256: half a row) a thread, which has a place of its own for
     // each raw block: its numbers and 16 bytes with their scales
-    static constexpr int TPR = D == 256 ? 2 : 1;           // threads a row
+    static constexpr int TPR = 2;                          // threads a row
     static constexpr int DT = D / TPR;                     // dims a thread
-    static constexpr int kOwn = DT / 2 + 16;
+    static constexpr int kOwn = (DT / 2 + 16) / 16 % 2 ? DT / 2 + 16 : DT / 2 + 32;
     static constexpr int kRaw = 256 * kOwn;
     static_assert(BK * TPR == 128 && kOwn / 16 % 2 == 1, "a thread's share; 8 threads' loads touch every bank once");
     static constexpr int kOffK = TILES * kQTile;
@@ -487,7 +487,7 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
         // offsets in a row of this thread's numbers and of the 16 bytes with its part's scales, whose first word here is
         // that of group `g0`
         const int off = part * F::kPart + d0 / 2, off_sm = F::kParams + (F::NG == 4 ? part * 16 : 0);
-        const int word0 = F::NG == 4 ? d0 / F::kGroup : part * F::NG;
+        const int word0 = (F::NG == 4 ? 0 : part * F::NG) + d0 / F::kGroup;
         uint64_t* const full = part ? v_full : k_full;
         uint64_t* const empty = part ? v_empty : k_empty;
         const uint32_t ring = part ? NV : NK;
