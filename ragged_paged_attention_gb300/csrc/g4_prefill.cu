@@ -3,17 +3,18 @@
 //
 //   S = Q K^T, P = 2^(c S - m), O += P V, l += sum P, out = O / l, K = s n + m and V = s n + m rounded to bf16.
 //
-// Tiles of 128 rows (token, q head of the group; a row a thread), blocks of 128 keys (64 at head_dim 256). Eight warps
+// Tiles of 128 rows (token, q head of the group; a row a thread), blocks of 128 keys (64 at head_dim 256). Four warps
 // turn the 4-bit rows into the bf16 panels that the products read: a thread a row, which it has brought to shared
 // memory itself by cp.async (any page size, no barrier on the way), 8 numbers in some 20 instructions (a permute and a
 // mask put two numbers into the halves as 128 + n, one subtraction and one fused multiply-add give both values, the
 // latter rounding once). Two tiles of a KV head (head_dim 64 and 128) share each converted block, and while
 // one's softmax runs the tensor pipe works for the other; at head_dim 256 tensor memory holds one tile.
 // The rounding of K and V to bf16 (2^-9 of a value) is what a bf16 cache has too.
-// Warps: 4 softmax warps a tile; an MMA issuer a tile; one that takes items and loads Q; the rest of a warpgroup idle; 4
-// converters for K and 4 for V.
+// Warps: 4 softmax warps a tile; an MMA issuer a tile; one that takes items and loads Q; the rest of a warpgroup idle; 2
+// converters for K and 2 for V.
 // Barriers, all waits bounded: k/v_full, k/v_empty (panels), q_full, q_empty, item_full/empty; per tile s_full (QK
-// done), s_free (scores loaded), p_full (P written, O rescaled), pv_done, o_empty.
+// done), s_free (scores loaded), and P buffer p_full (P written, O rescaled) and pv_done;
+// per tile o_empty.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -40,29 +41,27 @@ struct G4Pre {
     static constexpr bool ONE_S = false;                   // the two tiles take turns with one S buffer
     static constexpr int NK = D == 256 ? 2 : 3, NV = D == 256 ? 1 : 3;
     static constexpr int NR = 3;                           // raw blocks on their way
-    // converters: 4 warps for K and 4 for V, a row (head_dim 256: half a row) a thread, which has a place of its own for
-    // each raw block: its numbers and 16 bytes with their scales
-    static constexpr int TPR = 2;                          // threads a row
-    static constexpr int DT = D / TPR;                     // dims a thread
-    static constexpr int kOwn = (DT / 2 + 16) / 16 % 2 ? DT / 2 + 16 : DT / 2 + 32;
-    static constexpr int kRaw = 256 * kOwn;
-    static_assert(BK * TPR == 128 && kOwn / 16 % 2 == 1, "a thread's share; 8 threads' loads touch every bank once");
+    // converters: 2 warps for K and 2 for V, a row a thread, which has a place of its own for each raw block: its
+    // numbers and 16 bytes with their scales
+    static constexpr int kOwn = D / 2 + 16;
+    static constexpr int kRaw = 128 * kOwn;
+    static_assert(BK == 64 && kOwn / 16 % 2 == 1, "a thread's share; 8 threads' loads touch every bank once");
     static constexpr int kOffK = TILES * kQTile;
     static constexpr int kOffV = kOffK + NK * kTile;
     static constexpr int kOffRaw = kOffV + NV * kTile;
     static constexpr int kOffBar = kOffRaw + NR * kRaw;
-    static constexpr int kBars = 2 * (NK + NV) + 7 + 5 * TILES;
+    static constexpr int kBars = 2 * (NK + NV) + 7 + 7 * TILES;
     static constexpr int kOffItem = (kOffBar + kBars * 8 + 15) / 16 * 16;  // [2] G4Item, abort, TMEM base, exit
     static constexpr int kSmem = kOffItem + 2 * (int)sizeof(G4Item) + 16;
     static constexpr int kSoft = 4 * TILES;
-    static constexpr int kThreads = (kSoft + 12) * 32;
+    static constexpr int kThreads = (kSoft + 8) * 32;
     static constexpr int kColS = 0, kColSStep = ONE_S ? 0 : BK;
-    static constexpr int kColP = ONE_S ? BK : TILES * BK, kColO = kColP + TILES * (BK / 2);
+    static constexpr int kColP = ONE_S ? BK : TILES * BK, kColO = kColP + TILES * BK;  // (two P buffers a tile)
     static constexpr int kTmemCols = 512;
     // registers: the launch's share of the SM, dealt out again by warpgroup (setmaxnreg)
-    static constexpr int kRegsLaunch = TILES == 2 ? 96 : 128;
-    static constexpr int kRegsSoft = 160, kRegsMma = 56, kRegsConv = 48;
-    static_assert(TILES == 1 || 256 * kRegsSoft + 128 * kRegsMma + 256 * kRegsConv <= kThreads * kRegsLaunch, "register split");
+    static constexpr int kRegsLaunch = TILES == 2 ? 128 : 168;
+    static constexpr int kRegsSoft = 184, kRegsRest = 72;
+    static_assert(TILES == 1 || 256 * kRegsSoft + 256 * kRegsRest <= kThreads * kRegsLaunch, "register split");
     static_assert(kSmem <= 232448 && kOffK % 1024 == 0 && kOffV % 1024 == 0 && kOffRaw % 16 == 0 && kOffBar % 8 == 0, "shared memory");
     static_assert(kColO + TILES * D <= kTmemCols, "tensor memory");
 };
@@ -121,8 +120,8 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
     uint64_t* s_full = q_full + 7;      // [TILES] each
     uint64_t* s_free = s_full + TILES;
     uint64_t* o_empty = s_full + 2 * TILES;
-    uint64_t* p_full = s_full + 3 * TILES;
-    uint64_t* pv_done = s_full + 4 * TILES;
+    uint64_t* p_full = s_full + 3 * TILES;   // [TILES][2 P buffers] each
+    uint64_t* pv_done = s_full + 5 * TILES;
     G4Item* s_items = reinterpret_cast<G4Item*>(smem + T::kOffItem);
     uint32_t* err = &hdr->error_bits;
     const int G = a.num_q_heads / a.num_kv_heads;
@@ -130,11 +129,11 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
 
     if (tid == 0) {
         for (int i = 0; i < NK; ++i) {
-            mbar_init(&k_full[i], 4);  // (converter warps)
+            mbar_init(&k_full[i], 2);  // (converter warps)
             mbar_init(&k_empty[i], TILES);
         }
         for (int i = 0; i < NV; ++i) {
-            mbar_init(&v_full[i], 4);
+            mbar_init(&v_full[i], 2);
             mbar_init(&v_empty[i], TILES);
         }
         mbar_init(q_full, 1);
@@ -147,9 +146,11 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
         for (int t = 0; t < TILES; ++t) {
             mbar_init(&s_full[t], 1);
             mbar_init(&s_free[t], 4);
-            mbar_init(&p_full[t], 4);
             mbar_init(&o_empty[t], 4);
-            mbar_init(&pv_done[t], 1);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&p_full[2 * t + b], 4);
+                mbar_init(&pv_done[2 * t + b], 1);
+            }
         }
         s_abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -180,14 +181,15 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
         if constexpr (TILES == 2) g4_regs_inc<T::kRegsSoft>();
         const int t = warp >> 2, quarter = warp & 3;
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-        const uint32_t col_s = tmem + lane_off + T::kColS + t * T::kColSStep, col_p = tmem + lane_off + T::kColP + t * (BK / 2),
+        const uint32_t col_s = tmem + lane_off + T::kColS + t * T::kColSStep, col_p = tmem + lane_off + T::kColP + t * BK,
                        col_o = tmem + lane_off + T::kColO + t * D;
         const float cap = a.soft_cap, cap_k2 = cap != 0.f ? 2.f * kLog2e / cap : 0.f, c_log2 = a.sm_scale * kLog2e;
         // without a soft cap (and with a positive scale) the maximum is taken on the raw scores and the scale goes into
         // the exponent's multiply-add
         const bool fold = cap == 0.f && c_log2 > 0.f;
         const float cs = fold ? c_log2 : 1.f;
-        uint32_t nblk = 0;  // blocks this tile has processed
+        uint32_t nblk = 0;  // blocks this tile has processed; block n's P lies in buffer n & 1
+        auto pv_of = [&](uint32_t n) { return mbar_wait(&pv_done[2 * t + (n & 1)], (n >> 1) & 1, err); };
         bool ok = true;
         while (ok && next_item(it)) {
             const int n_rows = it.q_len * G;
@@ -239,7 +241,7 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
                 const float nmu = m_use == -INFINITY ? 0.f : -m_use;
                 const bool row_rescale = rescale && had;
                 if (__any_sync(0xffffffffu, row_rescale)) {
-                    if (!mbar_wait(&pv_done[t], par ^ 1, err)) {  // the previous block's PV has written O
+                    if (!pv_of(nblk - 1)) {  // the previous block's PV has written O
                         ok = false;
                         break;
                     }
@@ -256,8 +258,8 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
                 }
                 float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                 const float2 cs2 = make_float2(cs, cs), nmu2 = make_float2(nmu, nmu);
-                // the previous block's PV has read P
-                if (nblk > 0 && !mbar_wait(&pv_done[t], par ^ 1, err)) {
+                // the PV of the block before the last has read this buffer
+                if (nblk > 1 && !pv_of(nblk - 2)) {
                     ok = false;
                     break;
                 }
@@ -273,16 +275,16 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
                         sum2[e & 1] = fadd2(sum2[e & 1], p);
                         pk[e] = pack_bf16(p.x, p.y);
                     }
-                    tmem_st16_nowait(col_p + c * 16, pk);
+                    tmem_st16_nowait(col_p + (nblk & 1) * (BK / 2) + c * 16, pk);
                 }
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[t]);
+                if (lane == 0) mbar_arrive(&p_full[2 * t + (nblk & 1)]);
                 l = l * alpha + ((sum2[0].x + sum2[1].x) + (sum2[0].y + sum2[1].y));
             }
             // epilogue: O of the last PV
-            if (ok && mbar_wait(&pv_done[t], (nblk - 1) & 1, err)) {
+            if (ok && pv_of(nblk - 1)) {
                 tc_fence_after();
                 const float inv = l > 0.f ? 1.f / l : 0.f;
                 __nv_bfloat16* dst = a.out + ((size_t)(it.q_start + (rv ? R / G : 0)) * a.num_q_heads + it.head * G + (rv ? R % G : 0)) * D;
@@ -307,7 +309,7 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
             if (!ok) s_abort = 1;
         }
     } else if (warp < kConv0) {
-        if constexpr (TILES == 2) g4_regs_dec<T::kRegsMma>();
+        if constexpr (TILES == 2) g4_regs_dec<T::kRegsRest>();
         if (warp >= kMma0 && warp < kMma0 + TILES) {
             // ---------------- MMA issuer of tile t (a constant in either branch) ----------------
             // One lane, elected once, does all of it: the ring positions and phases are its registers, and a commit
@@ -319,7 +321,7 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
                 const uint64_t qdesc = umma_desc_sw128(smem_u32(smem + t * T::kQTile), 16, 1024);
                 const uint64_t kdesc = umma_desc_sw128(smem_u32(smem + T::kOffK), 16, 1024);
                 const uint64_t vdesc = umma_desc_sw128(smem_u32(smem + T::kOffV), T::kPanel, 1024);
-                const uint32_t col_s = tmem + T::kColS + t * T::kColSStep, col_p = tmem + T::kColP + t * (BK / 2), col_o = tmem + T::kColO + t * D;
+                const uint32_t col_s = tmem + T::kColS + t * T::kColSStep, col_p = tmem + T::kColP + t * BK, col_o = tmem + T::kColO + t * D;
                 uint32_t jk = 0, jv = 0;          // ring positions
                 uint32_t n_own = 0, n_other = 0;  // QKs of this tile, and of the other one before the next of these
                 uint32_t npv = 0, no = 0;         // PVs, and items this tile has had
@@ -371,13 +373,14 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
                             if (active) {
                                 if (j == 1 && no > 0) ok = ok && mbar_wait(&o_empty[t], (no - 1) & 1, err);
                                 const uint64_t vb = vdesc + (uint64_t)((slot * T::kTile) >> 4);
-                                ok = ok && mbar_wait(&p_full[t], npv & 1, err);
+                                const uint32_t pb = npv & 1;
+                                ok = ok && mbar_wait(&p_full[2 * t + pb], (npv >> 1) & 1, err);
                                 if (!ok) break;
                                 tc_fence_after();
 #pragma unroll
                                 for (int kk = 0; kk < BK / 16; ++kk)
-                                    umma_bf16_ta(col_o, col_p + kk * 8, vb + ((kk * 16 * 128) >> 4), idesc_pv, (j > 1 || kk > 0) ? 1u : 0u);
-                                umma_commit(&pv_done[t]);
+                                    umma_bf16_ta(col_o, col_p + pb * (BK / 2) + kk * 8, vb + ((kk * 16 * 128) >> 4), idesc_pv, (j > 1 || kk > 0) ? 1u : 0u);
+                                umma_commit(&pv_done[2 * t + pb]);
                                 umma_commit(&v_empty[slot]);
                                 ++npv;
                             } else {
@@ -476,22 +479,20 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
         }
     } else {
         // ---------------- converters ----------------
-        if constexpr (TILES == 2) g4_regs_dec<T::kRegsConv>();
-        constexpr int CH = T::DT / 32;               // 16-byte chunks of numbers a thread
-        const int ct = (tid - kConv0 * 32) & 127, part = warp >= kConv0 + 4, row = ct / T::TPR, d0 = ct % T::TPR * T::DT;
-        uint8_t* const mine = smem + T::kOffRaw + (part * 128 + ct) * T::kOwn;
+        if constexpr (TILES == 2) g4_regs_dec<T::kRegsRest>();
+        constexpr int CH = D / 32, kLoad = CH < 4 ? CH : 4;  // 16-byte chunks of numbers a thread
+        const int row = (tid - kConv0 * 32) & 63, part = warp >= kConv0 + 2;
+        const uint32_t mine = smem_u32(smem + T::kOffRaw + (part * 64 + row) * T::kOwn);
         const uint8_t* kv = static_cast<const uint8_t*>(a.kv_pages);
         const size_t slot_bytes = (size_t)a.num_kv_heads * F::kRow;
         const bool pow2 = (a.page_size & (a.page_size - 1)) == 0;
         const int lps = __ffs(a.page_size) - 1;
-        // offsets in a row of this thread's numbers and of the 16 bytes with its part's scales, whose first word here is
-        // that of group `g0`
-        const int off = part * F::kPart + d0 / 2, off_sm = F::kParams + (F::NG == 4 ? part * 16 : 0);
-        const int word0 = (F::NG == 4 ? 0 : part * F::NG) + d0 / F::kGroup;
+        // offsets in a row of this thread's numbers and of the 16 bytes with its part's scales, the first of them word0
+        const int off = part * F::kPart, off_sm = F::kParams + (F::NG == 4 ? part * 16 : 0), word0 = F::NG == 4 ? 0 : part * F::NG;
         uint64_t* const full = part ? v_full : k_full;
         uint64_t* const empty = part ? v_empty : k_empty;
         const uint32_t ring = part ? NV : NK;
-        uint8_t* const panel = smem + (part ? T::kOffV : T::kOffK) + row * 128;
+        const uint32_t panel = smem_u32(smem + (part ? T::kOffV : T::kOffK) + row * 128);
         uint32_t slot = 0, ph = 1;                   // panel ring
         uint32_t ask_slot = 0, get_slot = 0;         // raw ring
         bool ok = true;
@@ -511,10 +512,10 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
                     }
                     const int in_page = pow2 ? key_ask & (a.page_size - 1) : key_ask % a.page_size;
                     const uint8_t* src = kv + ((size_t)page * a.page_size + in_page) * slot_bytes + (size_t)it.head * F::kRow;
-                    const uint32_t dst = smem_u32(mine + ask_slot * T::kRaw);
+                    const uint32_t dst = mine + ask_slot * T::kRaw;
 #pragma unroll
                     for (int c = 0; c < CH; ++c) cp_async16(dst + c * 16, src + off + c * 16, true);
-                    cp_async16(dst + T::DT / 2, src + off_sm, true);
+                    cp_async16(dst + D / 2, src + off_sm, true);
                 }
                 cp_async_commit();
                 key_ask += BK;
@@ -529,7 +530,7 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
                 page_next = page_of(key_ask + BK);
                 ask(page);
                 cp_async_wait<NR - 1>();
-                const uint8_t* src = mine + get_slot * T::kRaw;
+                const uint32_t src = mine + get_slot * T::kRaw;
                 get_slot = get_slot + 1 == NR ? 0 : get_slot + 1;
                 const bool in = key < ke && key >= k0;  // rows that no query sees: zeros, whatever lies there
                 key += BK;
@@ -537,18 +538,28 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
                     ok = false;
                     break;
                 }
-                uint8_t* stage = panel + slot * T::kTile;
+                const uint32_t stage = panel + slot * T::kTile;
+                // (four chunks loaded before any is stored: the compiler cannot tell raw rows from panels, and would keep
+                // every load behind the store before it)
 #pragma unroll
-                for (int c = 0; c < CH; ++c) {
-                    uint32_t sm = *reinterpret_cast<const uint32_t*>(src + T::DT / 2 + 4 * (word0 + c * 32 / F::kGroup));
-                    if (!in) sm = 0;
-                    const uint4 w = *reinterpret_cast<const uint4*>(src + c * 16);
-                    const uint32_t s2 = __byte_perm(sm, sm, 0x1010), m2 = __byte_perm(sm, sm, 0x3232);
-                    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+                for (int c0 = 0; c0 < CH; c0 += kLoad) {
+                    uint4 w[kLoad];
+                    uint32_t sm[kLoad];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int chunk = d0 / 8 + 4 * c + e;
-                        *reinterpret_cast<uint4*>(stage + (chunk >> 3) * T::kPanel + (((chunk & 7) ^ (row & 7)) << 4)) = g4_panel8(ww[e], s2, m2);
+                    for (int c = 0; c < kLoad; ++c) {
+                        w[c] = lds128(src + (c0 + c) * 16);
+                        sm[c] = lds32(src + D / 2 + 4 * (word0 + (c0 + c) * 32 / F::kGroup));
+                        if (!in) sm[c] = 0;
+                    }
+#pragma unroll
+                    for (int c = 0; c < kLoad; ++c) {
+                        const uint32_t s2 = __byte_perm(sm[c], sm[c], 0x1010), m2 = __byte_perm(sm[c], sm[c], 0x3232);
+                        const uint32_t ww[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int chunk = 4 * (c0 + c) + e;
+                            sts128(stage + (chunk >> 3) * T::kPanel + (((chunk & 7) ^ (row & 7)) << 4), g4_panel8(ww[e], s2, m2));
+                        }
                     }
                 }
                 fence_proxy_async_smem();
