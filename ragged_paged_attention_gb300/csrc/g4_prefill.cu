@@ -39,59 +39,81 @@ struct G4Pre {
     static constexpr int kQPanel = 128 * 128, kQTile = DP * kQPanel;
     static constexpr int kPanel = BK * 128, kTile = DP * kPanel;
     static constexpr bool ONE_S = false;                   // the two tiles take turns with one S buffer
-    static constexpr int NK = D == 256 ? 2 : 3, NV = D == 256 ? 1 : 3;
+    // K's ring of blocks and V's of half ones (64 keys), so that one is turned while the products read the others
+    static constexpr int NK = D == 256 ? 2 : 4, HV = BK / 64, NV = D == 256 ? 1 : 4;
+    static constexpr int kHalf = DP * 64 * 128;            // half a block of V
+    static constexpr int PB = 2;            // P buffers a tile
     static constexpr int NR = 3;                           // raw blocks on their way
-    // converters: 2 warps for K and 2 for V, a row a thread, which has a place of its own for each raw block: its
-    // numbers and 16 bytes with their scales
-    static constexpr int kOwn = D / 2 + 16;
-    static constexpr int kRaw = 128 * kOwn;
-    static_assert(BK == 64 && kOwn / 16 % 2 == 1, "a thread's share; 8 threads' loads touch every bank once");
+    static constexpr int kRaw = BK * G4<D>::kRow;
     static constexpr int kOffK = TILES * kQTile;
     static constexpr int kOffV = kOffK + NK * kTile;
-    static constexpr int kOffRaw = kOffV + NV * kTile;
+    static constexpr int kOffRaw = kOffV + NV * kHalf;
     static constexpr int kOffBar = kOffRaw + NR * kRaw;
-    static constexpr int kBars = 2 * (NK + NV) + 7 + 7 * TILES;
+    static constexpr int kBars = 2 * (NK + NV + NR) + 7 + (3 + 2 * PB) * TILES;
     static constexpr int kOffItem = (kOffBar + kBars * 8 + 15) / 16 * 16;  // [2] G4Item, abort, TMEM base, exit
     static constexpr int kSmem = kOffItem + 2 * (int)sizeof(G4Item) + 16;
     static constexpr int kSoft = 4 * TILES;
     static constexpr int kThreads = (kSoft + 8) * 32;
     static constexpr int kColS = 0, kColSStep = ONE_S ? 0 : BK;
-    static constexpr int kColP = ONE_S ? BK : TILES * BK, kColO = kColP + TILES * BK;  // (two P buffers a tile)
+    static constexpr int kColP = ONE_S ? BK : TILES * BK, kColO = kColP + TILES * PB * (BK / 2);
     static constexpr int kTmemCols = 512;
     // registers: the launch's share of the SM, dealt out again by warpgroup (setmaxnreg)
     static constexpr int kRegsLaunch = TILES == 2 ? 128 : 168;
     static constexpr int kRegsSoft = 184, kRegsRest = 72;
     static_assert(TILES == 1 || 256 * kRegsSoft + 256 * kRegsRest <= kThreads * kRegsLaunch, "register split");
-    static_assert(kSmem <= 232448 && kOffK % 1024 == 0 && kOffV % 1024 == 0 && kOffRaw % 16 == 0 && kOffBar % 8 == 0, "shared memory");
+    static_assert(kSmem <= 232448 && kOffK % 1024 == 0 && kOffV % 1024 == 0 && kOffRaw % 128 == 0 && kRaw % 128 == 0 && kOffBar % 8 == 0, "shared memory");
     static_assert(kColO + TILES * D <= kTmemCols, "tensor memory");
 };
+
+// Behind the last key that a row of the item sees.
+__device__ __forceinline__ int g4_key_end(const G4Item& it, int G, int tiles) {
+    return it.kv_len - it.q_len + (min(it.row + 128 * tiles, it.q_len * G) - 1) / G + 1;
+}
 
 template <int R>
 __device__ __forceinline__ void g4_regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R>
 __device__ __forceinline__ void g4_regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 
-// 8 numbers of a word -> 8 bf16 of s n + m, in order: byte i's two numbers to the low bits of two halves, which are then
-// 128 + n; the difference is exact and the fused multiply-add rounds once.
+// Panels hold values times kDown. A number with all other bits of its half masked away is the bf16 subnormal n 2^-133 (or n
+// 2^-129 in bits 4-7), so that one fused multiply-add with (s 2^80, m 2^-53) gives (s n + m) 2^-53, rounded once, with
+// bf16's exponents: scores and outputs take the 2^53 back. (Numbers as 128 + n, and a subtraction before the multiply-add:
+// 34 cycles of a quarter of the SM for 8 of them, where K's take 26 and V's 18.)
+constexpr float kDown = 0x1p-53f;
+__device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// 8 numbers in order (K, whose dims lie as Q's do): byte e's two go to the low bits of two halves.
 __device__ __forceinline__ uint4 g4_panel8(uint32_t w, uint32_t s2, uint32_t m2) {
     const uint32_t h = w >> 4;
     uint32_t r[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        uint32_t t = __byte_perm(w, h, e | (e << 4) | ((4 + e) << 8) | ((4 + e) << 12));
-        t = (t & 0x000f000fu) | 0x43004300u;
-        asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(t) : "r"(0x43004300u));
-        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r[e]) : "r"(t), "r"(s2), "r"(m2));
-    }
+    for (int e = 0; e < 4; ++e) r[e] = __byte_perm(w, h, e | (e << 4) | ((4 + e) << 8) | ((4 + e) << 12)) & 0x000f000fu;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = bf16x2_fma(r[e], s2, m2);
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
+// In the order 0, 4, 1, 5, 2, 6, 3, 7 (V, whose dims are O's columns: the epilogue puts them in order).
+__device__ __forceinline__ uint4 g4_panel8_v(uint32_t w, uint32_t s2, uint32_t s2_16, uint32_t m2) {
+    const uint32_t h = w >> 8;
+    return make_uint4(bf16x2_fma(w & 0x000f000fu, s2, m2), bf16x2_fma(w & 0x00f000f0u, s2_16, m2), bf16x2_fma(h & 0x000f000fu, s2, m2),
+                      bf16x2_fma(h & 0x00f000f0u, s2_16, m2));
+}
 
-template <int D>
+template <int D, bool CAP>
 __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
-    g4_prefill_kernel(const __grid_constant__ RpaArgs a, const __grid_constant__ CUtensorMap tm_q, int q_tma, int tail) {
+    g4_prefill_kernel(const __grid_constant__ RpaArgs a, const __grid_constant__ CUtensorMap tm_q,
+                      const __grid_constant__ CUtensorMap tm_kv, int q_tma, int box_rows, int tail) {
     using T = G4Pre<D>;
     using F = G4<D>;
-    constexpr int BK = T::BK, NK = T::NK, NV = T::NV, TILES = T::TILES, NR = T::NR;
+    constexpr int BK = T::BK, NK = T::NK, NV = T::NV, TILES = T::TILES, NR = T::NR, PB = T::PB;
     // first launch (tail == 0): started early behind the plan, it waits for it, then lets the decode grid behind
     // start; only the plan's share of its CTAs works. Either launch leaves at once when the list is empty.
     if (!tail) {
@@ -112,7 +134,9 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
     uint64_t* k_empty = k_full + NK;
     uint64_t* v_full = k_empty + NK;
     uint64_t* v_empty = v_full + NV;
-    uint64_t* q_full = v_empty + NV;
+    uint64_t* raw_full = v_empty + NV;
+    uint64_t* raw_empty = raw_full + NR;
+    uint64_t* q_full = raw_empty + NR;
     uint64_t* q_empty = q_full + 1;
     uint64_t* item_full = q_full + 2;   // [2]
     uint64_t* item_empty = q_full + 4;  // [2]
@@ -120,12 +144,12 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
     uint64_t* s_full = q_full + 7;      // [TILES] each
     uint64_t* s_free = s_full + TILES;
     uint64_t* o_empty = s_full + 2 * TILES;
-    uint64_t* p_full = s_full + 3 * TILES;   // [TILES][2 P buffers] each
-    uint64_t* pv_done = s_full + 5 * TILES;
+    uint64_t* p_full = s_full + 3 * TILES;   // [TILES][P buffers] each
+    uint64_t* pv_done = p_full + PB * TILES;
     G4Item* s_items = reinterpret_cast<G4Item*>(smem + T::kOffItem);
     uint32_t* err = &hdr->error_bits;
     const int G = a.num_q_heads / a.num_kv_heads;
-    constexpr int kMma0 = T::kSoft, kQw = T::kSoft + 2, kConv0 = T::kSoft + 4;
+    constexpr int kMma0 = T::kSoft, kQw = T::kSoft + 2, kRawW = T::kSoft + 3, kConv0 = T::kSoft + 4;
 
     if (tid == 0) {
         for (int i = 0; i < NK; ++i) {
@@ -135,6 +159,10 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
         for (int i = 0; i < NV; ++i) {
             mbar_init(&v_full[i], 2);
             mbar_init(&v_empty[i], TILES);
+        }
+        for (int i = 0; i < NR; ++i) {
+            mbar_init(&raw_full[i], 1);
+            mbar_init(&raw_empty[i], 4);
         }
         mbar_init(q_full, 1);
         mbar_init(q_empty, TILES);
@@ -147,9 +175,9 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
             mbar_init(&s_full[t], 1);
             mbar_init(&s_free[t], 4);
             mbar_init(&o_empty[t], 4);
-            for (int b = 0; b < 2; ++b) {
-                mbar_init(&p_full[2 * t + b], 4);
-                mbar_init(&pv_done[2 * t + b], 1);
+            for (int b = 0; b < PB; ++b) {
+                mbar_init(&p_full[PB * t + b], 4);
+                mbar_init(&pv_done[PB * t + b], 1);
             }
         }
         s_abort = 0;
@@ -181,15 +209,15 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
         if constexpr (TILES == 2) g4_regs_inc<T::kRegsSoft>();
         const int t = warp >> 2, quarter = warp & 3;
         const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-        const uint32_t col_s = tmem + lane_off + T::kColS + t * T::kColSStep, col_p = tmem + lane_off + T::kColP + t * BK,
+        const uint32_t col_s = tmem + lane_off + T::kColS + t * T::kColSStep, col_p = tmem + lane_off + T::kColP + t * PB * (BK / 2),
                        col_o = tmem + lane_off + T::kColO + t * D;
-        const float cap = a.soft_cap, cap_k2 = cap != 0.f ? 2.f * kLog2e / cap : 0.f, c_log2 = a.sm_scale * kLog2e;
+        const float cap = a.soft_cap, cap_k2 = cap != 0.f ? 2.f * kLog2e / cap : 0.f, scale = a.sm_scale / kDown, c_log2 = scale * kLog2e;
         // without a soft cap (and with a positive scale) the maximum is taken on the raw scores and the scale goes into
         // the exponent's multiply-add
-        const bool fold = cap == 0.f && c_log2 > 0.f;
+        const bool fold = !CAP && c_log2 > 0.f;
         const float cs = fold ? c_log2 : 1.f;
-        uint32_t nblk = 0;  // blocks this tile has processed; block n's P lies in buffer n & 1
-        auto pv_of = [&](uint32_t n) { return mbar_wait(&pv_done[2 * t + (n & 1)], (n >> 1) & 1, err); };
+        uint32_t nblk = 0;  // blocks this tile has processed; block n's P lies in buffer n % PB
+        auto pv_of = [&](uint32_t n) { return mbar_wait(&pv_done[PB * t + n % PB], (n / PB) & 1, err); };
         bool ok = true;
         while (ok && next_item(it)) {
             const int n_rows = it.q_len * G;
@@ -215,9 +243,23 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s_free[t]);
-                if (cap != 0.f) {
+                if constexpr (CAP) {
+                    // small logits (the warp's every |x * scale| <= |cap| / 4): the series form, on the FMA pipe
+                    float am = 0.f;
 #pragma unroll
-                    for (int i = 0; i < BK; ++i) x[i] = soft_cap(x[i] * a.sm_scale, cap, cap_k2) * kLog2e;
+                    for (int i = 0; i < BK; i += 2) am = fmax3(am, fabsf(x[i]), fabsf(x[i + 1]));
+                    if (__all_sync(0xffffffffu, am * fabsf(scale) <= 0.25f * fabsf(cap))) {
+                        const float ic = 1.f / (cap * kLog2e);
+#pragma unroll
+                        for (int i = 0; i < BK; i += 2) {
+                            const float2 y = soft_cap_small2(fmul2(make_float2(x[i], x[i + 1]), make_float2(c_log2, c_log2)), ic);
+                            x[i] = y.x;
+                            x[i + 1] = y.y;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < BK; ++i) x[i] = soft_cap(x[i] * scale, cap, cap_k2) * kLog2e;
+                    }
                 } else if (!fold) {
 #pragma unroll
                     for (int i = 0; i < BK; ++i) x[i] *= c_log2;
@@ -258,8 +300,8 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
                 }
                 float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                 const float2 cs2 = make_float2(cs, cs), nmu2 = make_float2(nmu, nmu);
-                // the PV of the block before the last has read this buffer
-                if (nblk > 1 && !pv_of(nblk - 2)) {
+                // the last PV of this buffer has read it
+                if (nblk >= PB && !pv_of(nblk - PB)) {
                     ok = false;
                     break;
                 }
@@ -275,18 +317,18 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
                         sum2[e & 1] = fadd2(sum2[e & 1], p);
                         pk[e] = pack_bf16(p.x, p.y);
                     }
-                    tmem_st16_nowait(col_p + (nblk & 1) * (BK / 2) + c * 16, pk);
+                    tmem_st16_nowait(col_p + nblk % PB * (BK / 2) + c * 16, pk);
                 }
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[2 * t + (nblk & 1)]);
+                if (lane == 0) mbar_arrive(&p_full[PB * t + nblk % PB]);
                 l = l * alpha + ((sum2[0].x + sum2[1].x) + (sum2[0].y + sum2[1].y));
             }
             // epilogue: O of the last PV
             if (ok && pv_of(nblk - 1)) {
                 tc_fence_after();
-                const float inv = l > 0.f ? 1.f / l : 0.f;
+                const float inv = l > 0.f ? 1.f / (l * kDown) : 0.f;
                 __nv_bfloat16* dst = a.out + ((size_t)(it.q_start + (rv ? R / G : 0)) * a.num_q_heads + it.head * G + (rv ? R % G : 0)) * D;
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
@@ -296,8 +338,8 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
                         uint4* d4 = reinterpret_cast<uint4*>(dst + c * 32);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            d4[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 1] * inv), pack_bf16(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                                               pack_bf16(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack_bf16(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+                            d4[i] = make_uint4(pack_bf16(o[8 * i] * inv, o[8 * i + 2] * inv), pack_bf16(o[8 * i + 4] * inv, o[8 * i + 6] * inv),
+                                               pack_bf16(o[8 * i + 1] * inv, o[8 * i + 3] * inv), pack_bf16(o[8 * i + 5] * inv, o[8 * i + 7] * inv));
                     }
                 }
                 tc_fence_before();
@@ -320,8 +362,8 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
                 constexpr uint32_t idesc_pv = umma_idesc_bf16(128, D, false, true);
                 const uint64_t qdesc = umma_desc_sw128(smem_u32(smem + t * T::kQTile), 16, 1024);
                 const uint64_t kdesc = umma_desc_sw128(smem_u32(smem + T::kOffK), 16, 1024);
-                const uint64_t vdesc = umma_desc_sw128(smem_u32(smem + T::kOffV), T::kPanel, 1024);
-                const uint32_t col_s = tmem + T::kColS + t * T::kColSStep, col_p = tmem + T::kColP + t * BK, col_o = tmem + T::kColO + t * D;
+                const uint64_t vdesc = umma_desc_sw128(smem_u32(smem + T::kOffV), 64 * 128, 1024);
+                const uint32_t col_s = tmem + T::kColS + t * T::kColSStep, col_p = tmem + T::kColP + t * PB * (BK / 2), col_o = tmem + T::kColO + t * D;
                 uint32_t jk = 0, jv = 0;          // ring positions
                 uint32_t n_own = 0, n_other = 0;  // QKs of this tile, and of the other one before the next of these
                 uint32_t npv = 0, no = 0;         // PVs, and items this tile has had
@@ -366,26 +408,33 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
                             if (!ok) break;
                             mbar_arrive(q_empty);
                         }
-                        if (j > 0) {  // PV of block j - 1
-                            const uint32_t slot = jv % NV;
-                            ok = mbar_wait(&v_full[slot], (jv / NV) & 1, err);
-                            ++jv;
+                        if (j > 0) {  // PV of block j - 1, half a block of V after another
+                            const uint32_t pb = npv % PB;
                             if (active) {
                                 if (j == 1 && no > 0) ok = ok && mbar_wait(&o_empty[t], (no - 1) & 1, err);
-                                const uint64_t vb = vdesc + (uint64_t)((slot * T::kTile) >> 4);
-                                const uint32_t pb = npv & 1;
-                                ok = ok && mbar_wait(&p_full[2 * t + pb], (npv >> 1) & 1, err);
-                                if (!ok) break;
-                                tc_fence_after();
+                                ok = ok && mbar_wait(&p_full[PB * t + pb], (npv / PB) & 1, err);
+                            }
 #pragma unroll
-                                for (int kk = 0; kk < BK / 16; ++kk)
-                                    umma_bf16_ta(col_o, col_p + pb * (BK / 2) + kk * 8, vb + ((kk * 16 * 128) >> 4), idesc_pv, (j > 1 || kk > 0) ? 1u : 0u);
-                                umma_commit(&pv_done[2 * t + pb]);
-                                umma_commit(&v_empty[slot]);
-                                ++npv;
-                            } else {
+                            for (int h = 0; h < T::HV; ++h, ++jv) {
+                                const uint32_t slot = jv % NV;
+                                ok = ok && mbar_wait(&v_full[slot], (jv / NV) & 1, err);
                                 if (!ok) break;
-                                mbar_arrive(&v_empty[slot]);
+                                if (active) {
+                                    const uint64_t vb = vdesc + (uint64_t)((slot * T::kHalf) >> 4);
+                                    tc_fence_after();
+#pragma unroll
+                                    for (int kk = 0; kk < 4; ++kk)
+                                        umma_bf16_ta(col_o, col_p + pb * (BK / 2) + (4 * h + kk) * 8, vb + ((kk * 16 * 128) >> 4), idesc_pv,
+                                                     (j > 1 || h > 0 || kk > 0) ? 1u : 0u);
+                                    umma_commit(&v_empty[slot]);
+                                } else {
+                                    mbar_arrive(&v_empty[slot]);
+                                }
+                            }
+                            if (!ok) break;
+                            if (active) {
+                                umma_commit(&pv_done[PB * t + pb]);
+                                ++npv;
                             }
                         }
                     }
@@ -473,106 +522,132 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
                 if (items > 0) mbar_wait(q_full, (items - 1) & 1, err);
             }
             __syncwarp();
+        } else if (warp == kRawW) {
+            // ---------------- raw rows: a tensor copy a page (or a block's part of one) of this head's rows ----------------
+            // (page sizes no box tiles a block with: 16 bytes at a time)
+            const uint8_t* kv = static_cast<const uint8_t*>(a.kv_pages);
+            const size_t slot_bytes = (size_t)a.num_kv_heads * F::kRow;
+            const int lbr = __ffs(box_rows) - 1, lps = __ffs(a.page_size) - 1;
+            uint32_t jr = 0;
+            bool ok = true;
+            while (ok && next_item(it)) {
+                const int* tbl = a.page_indices + (size_t)it.seq * a.pages_per_seq;
+                const int ke = g4_key_end(it, G, TILES);
+                auto page_of = [&](int j) -> int {
+                    const int key = (it.block0 + j) * BK + lane * box_rows;
+                    return box_rows && lane * box_rows < BK && j < it.blocks && key < ke ? __ldg(tbl + (key >> lps)) : 0;
+                };
+                int page_next = page_of(0);
+                for (int j = 0; ok && j < it.blocks; ++j, ++jr) {
+                    int page = page_next;
+                    page_next = page_of(j + 1);
+                    const int key0 = (it.block0 + j) * BK, valid = min(BK, ke - key0);
+                    const uint32_t slot = jr % NR, ph = (jr / NR) & 1, dst = smem_u32(smem + T::kOffRaw + slot * T::kRaw);
+                    ok = mbar_wait(&raw_empty[slot], ph ^ 1, err);
+                    if (!ok) break;  // (every lane has waited)
+                    if (box_rows) {
+                        const int boxes = (valid + box_rows - 1) >> lbr;
+                        if (lane < boxes && (unsigned)page >= (unsigned)a.total_num_pages) {
+                            set_error(err, RPA_DEV_ERR_PAGE);
+                            page = 0;  // an in-bounds page keeps the barrier's byte count; the error is recorded
+                        }
+                        if (lane == 0) mbar_arrive_expect_tx(&raw_full[slot], (uint32_t)(boxes * box_rows * F::kRow));
+                        __syncwarp();
+                        if (lane < boxes)
+                            tma_load_3d(dst + lane * box_rows * F::kRow, &tm_kv, 0, it.head, (page << lps) + ((key0 + lane * box_rows) & (a.page_size - 1)),
+                                        &raw_full[slot]);
+                    } else {
+                        for (int i = lane; i < valid * (F::kRow / 16); i += 32) {
+                            const int r = i / (F::kRow / 16), c = i % (F::kRow / 16), key = key0 + r;
+                            int p = __ldg(tbl + key / a.page_size);
+                            if ((unsigned)p >= (unsigned)a.total_num_pages) {
+                                set_error(err, RPA_DEV_ERR_PAGE);
+                                p = 0;
+                            }
+                            cp_async16(dst + r * F::kRow + c * 16,
+                                       kv + ((size_t)p * a.page_size + key % a.page_size) * slot_bytes + (size_t)it.head * F::kRow + c * 16, true);
+                        }
+                        cp_async_commit();
+                        cp_async_wait<0>();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&raw_full[slot]);
+                    }
+                }
+                if (!ok) s_abort = 1;
+            }
+            if (lane == 0 && s_abort)  // copies under way land (bounded) before shared memory goes
+                for (uint32_t i = jr > NR ? jr - NR : 0; i < jr; ++i) mbar_wait(&raw_full[i % NR], (i / NR) & 1, err);
+            __syncwarp();
         } else {
             while (next_item(it)) {
             }
         }
     } else {
-        // ---------------- converters ----------------
+        // ---------------- converters: a row of a half block a thread ----------------
         if constexpr (TILES == 2) g4_regs_dec<T::kRegsRest>();
-        constexpr int CH = D / 32, kLoad = CH < 4 ? CH : 4;  // 16-byte chunks of numbers a thread
+        constexpr int CH = D / 32;  // 16-byte chunks of numbers a row
         const int row = (tid - kConv0 * 32) & 63, part = warp >= kConv0 + 2;
-        const uint32_t mine = smem_u32(smem + T::kOffRaw + (part * 64 + row) * T::kOwn);
-        const uint8_t* kv = static_cast<const uint8_t*>(a.kv_pages);
-        const size_t slot_bytes = (size_t)a.num_kv_heads * F::kRow;
-        const bool pow2 = (a.page_size & (a.page_size - 1)) == 0;
-        const int lps = __ffs(a.page_size) - 1;
-        // offsets in a row of this thread's numbers and of the 16 bytes with its part's scales, the first of them word0
-        const int off = part * F::kPart, off_sm = F::kParams + (F::NG == 4 ? part * 16 : 0), word0 = F::NG == 4 ? 0 : part * F::NG;
-        uint64_t* const full = part ? v_full : k_full;
-        uint64_t* const empty = part ? v_empty : k_empty;
-        const uint32_t ring = part ? NV : NK;
+        const uint32_t off = smem_u32(smem + T::kOffRaw) + row * F::kRow + part * F::kPart;
+        const uint32_t off_sm = smem_u32(smem + T::kOffRaw) + row * F::kRow + F::kParams + part * 4 * F::NG;
         const uint32_t panel = smem_u32(smem + (part ? T::kOffV : T::kOffK) + row * 128);
-        uint32_t slot = 0, ph = 1;                   // panel ring
-        uint32_t ask_slot = 0, get_slot = 0;         // raw ring
+        uint32_t jb = 0, jh = 0;  // blocks, and half blocks of V
         bool ok = true;
         while (ok && next_item(it)) {
-            const int* tbl = a.page_indices + (size_t)it.seq * a.pages_per_seq;
-            // keys that some row of the item sees: [k0, ke)
-            const int ke = min(it.kv_len, it.kv_len - it.q_len + (min(it.row + 128 * TILES, it.q_len * G) - 1) / G + 1);
+            // keys that some row of the item sees: [k0, ke); the others are zeros, whatever lies there
+            const int ke = g4_key_end(it, G, TILES);
             const int k0 = a.sliding_window > 0 ? it.kv_len - it.q_len + it.row / G - a.sliding_window + 1 : 0;
-            const int key_end = min(ke, (it.block0 + it.blocks) * BK);
-            int key_ask = it.block0 * BK + row, key = key_ask;
-            auto page_of = [&](int k) -> int { return k < key_end ? __ldg(tbl + (pow2 ? k >> lps : k / a.page_size)) : -1; };
-            auto ask = [&](int page) {  // the row of key_ask on its way (an empty group where there is none)
-                if (key_ask < key_end) {
-                    if ((unsigned)page >= (unsigned)a.total_num_pages) {
-                        set_error(err, RPA_DEV_ERR_PAGE);
-                        page = 0;
-                    }
-                    const int in_page = pow2 ? key_ask & (a.page_size - 1) : key_ask % a.page_size;
-                    const uint8_t* src = kv + ((size_t)page * a.page_size + in_page) * slot_bytes + (size_t)it.head * F::kRow;
-                    const uint32_t dst = mine + ask_slot * T::kRaw;
-#pragma unroll
-                    for (int c = 0; c < CH; ++c) cp_async16(dst + c * 16, src + off + c * 16, true);
-                    cp_async16(dst + D / 2, src + off_sm, true);
-                }
-                cp_async_commit();
-                key_ask += BK;
-                ask_slot = ask_slot + 1 == NR ? 0 : ask_slot + 1;
-            };
-#pragma unroll
-            for (int j = 0; j < NR - 1; ++j) ask(page_of(key_ask));
-            int page_next = page_of(key_ask);
+            int key = it.block0 * BK + row;
 #pragma unroll 1
-            for (int j = 0; j < it.blocks; ++j) {
-                const int page = page_next;
-                page_next = page_of(key_ask + BK);
-                ask(page);
-                cp_async_wait<NR - 1>();
-                const uint32_t src = mine + get_slot * T::kRaw;
-                get_slot = get_slot + 1 == NR ? 0 : get_slot + 1;
-                const bool in = key < ke && key >= k0;  // rows that no query sees: zeros, whatever lies there
-                key += BK;
-                if (!mbar_wait(&empty[slot], ph, err)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t stage = panel + slot * T::kTile;
-                // (four chunks loaded before any is stored: the compiler cannot tell raw rows from panels, and would keep
-                // every load behind the store before it)
-#pragma unroll
-                for (int c0 = 0; c0 < CH; c0 += kLoad) {
-                    uint4 w[kLoad];
-                    uint32_t sm[kLoad];
-#pragma unroll
-                    for (int c = 0; c < kLoad; ++c) {
-                        w[c] = lds128(src + (c0 + c) * 16);
-                        sm[c] = lds32(src + D / 2 + 4 * (word0 + (c0 + c) * 32 / F::kGroup));
-                        if (!in) sm[c] = 0;
+            for (int j = 0; ok && j < it.blocks; ++j, ++jb) {
+                const uint32_t raw = jb % NR;
+                ok = mbar_wait(&raw_full[raw], (jb / NR) & 1, err);
+                if (!part) ok = ok && mbar_wait(&k_empty[jb % NK], ((jb / NK) & 1) ^ 1, err);
+#pragma unroll 1
+                for (int h = 0; h < T::HV; ++h, key += 64) {
+                    if (part) {
+                        ok = ok && mbar_wait(&v_empty[jh % NV], ((jh / NV) & 1) ^ 1, err);
                     }
+                    if (!ok) break;
+                    // K's block has its rows 128 bytes apart in 64-wide panels, V's halves have theirs the same way each
+                    const uint32_t stage = panel + (part ? jh % NV * T::kHalf : jb % NK * T::kTile + h * 64 * 128);
+                    const uint32_t pitch = part ? 64 * 128 : T::kPanel, src = raw * T::kRaw + h * 64 * F::kRow;
+                    const bool in = key < ke && key >= k0;
+                    // A chunk's numbers and scales are loaded while the one before is turned. The loop stays rolled: unrolled
+                    // over a block, this code and the softmax's, each run through once a block, come too slowly from the
+                    // instruction caches (4 x 4096 prompts 878 us).
+                    uint4 w = lds128(off + src);
+                    uint32_t sm = lds32(off_sm + src);
+#pragma unroll 1
+                    for (int c = 0; c < CH; ++c) {
+                        const uint32_t p = bf16x2_mul(in ? sm : 0u, 0x25006780u);  // (s 2^80, m 2^-53)
+                        const uint32_t s2 = __byte_perm(p, p, 0x1010), m2 = __byte_perm(p, p, 0x3232);
+                        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+                        const int next = c + 1 < CH ? c + 1 : 0;
+                        w = lds128(off + src + next * 16);
+                        sm = lds32(off_sm + src + 4 * (next * 32 / F::kGroup));
+                        uint4 x[4];
+                        if (part) {
+                            const uint32_t s2_16 = bf16x2_mul(s2, 0x3d803d80u);  // a 16th
 #pragma unroll
-                    for (int c = 0; c < kLoad; ++c) {
-                        const uint32_t s2 = __byte_perm(sm[c], sm[c], 0x1010), m2 = __byte_perm(sm[c], sm[c], 0x3232);
-                        const uint32_t ww[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+                            for (int e = 0; e < 4; ++e) x[e] = g4_panel8_v(ww[e], s2, s2_16, m2);
+                        } else {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int chunk = 4 * (c0 + c) + e;
-                            sts128(stage + (chunk >> 3) * T::kPanel + (((chunk & 7) ^ (row & 7)) << 4), g4_panel8(ww[e], s2, m2));
+                            for (int e = 0; e < 4; ++e) x[e] = g4_panel8(ww[e], s2, m2);
                         }
+                        // 16-byte chunks 4 c .. 4 c + 3 of the row: half of a panel's 128 bytes
+                        const uint32_t to = stage + (c >> 1) * pitch, low = (c & 1) << 2;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sts128(to + (((low + e) ^ (row & 7)) << 4), x[e]);
                     }
+                    if (part || h + 1 == T::HV) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(part ? &v_full[jh % NV] : &k_full[jb % NK]);
+                    }
+                    jh += part;
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&full[slot]);
-                if (++slot == ring) {
-                    slot = 0;
-                    ph ^= 1;
-                }
+                if (ok && lane == 0) mbar_arrive(&raw_empty[raw]);
             }
-            cp_async_wait<0>();
-            // the raw ring starts over with the next item's first block
-            ask_slot = get_slot;
             if (!ok) s_abort = 1;
         }
     }
@@ -583,10 +658,10 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
     if (warp == kMma0) tmem_dealloc(tmem, T::kTmemCols);
 }
 
-template <int D>
+template <int D, bool CAP>
 static cudaError_t launch_pre(const RpaArgs& a, int num_sms, cudaStream_t stream, int tail) {
     using T = G4Pre<D>;
-    auto kern = g4_prefill_kernel<D>;
+    auto kern = g4_prefill_kernel<D, CAP>;
     static bool configured[64] = {};  // (by device: the attribute is the device's)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -602,19 +677,25 @@ static cudaError_t launch_pre(const RpaArgs& a, int num_sms, cudaStream_t stream
         if (T::TILES == 2 && fa.numRegs != T::kRegsLaunch) return cudaErrorLaunchOutOfResources;
         configured[dev] = true;
     }
-    CUtensorMap tq;
+    CUtensorMap tq, tkv;
     memset(&tq, 0, sizeof tq);
-    const int G = a.num_q_heads / a.num_kv_heads;
+    memset(&tkv, 0, sizeof tkv);
+    const int G = a.num_q_heads / a.num_kv_heads, ps = a.page_size;
     const int q_tma = 128 % G == 0 && make_tmap_bf16(&tq, a.q, D, a.num_q_heads, a.max_num_tokens, G, 128 / G);
-    ProfScope ps(tail == 1 ? "rpa_g4_prefill_tail" : "rpa_g4_prefill", stream);
-    return launch_pdl(kern, dim3(num_sms), dim3(T::kThreads), T::kSmem, stream, a.overlap && !tail, a, tq, q_tma, tail);
+    // boxes of a page's rows, or a block's part of them: at least 8, so that each starts on 128 bytes
+    int box_rows = (ps & (ps - 1)) == 0 && ps >= 8 ? (ps < T::BK ? ps : T::BK) : 0;
+    if ((long long)a.total_num_pages * ps > INT32_MAX) box_rows = 0;
+    if (box_rows && !make_tmap_rows(&tkv, a.kv_pages, G4<D>::kRow, a.num_kv_heads, (uint64_t)a.total_num_pages * ps, box_rows)) box_rows = 0;
+    ProfScope prof(tail == 1 ? "rpa_g4_prefill_tail" : "rpa_g4_prefill", stream);
+    return launch_pdl(kern, dim3(num_sms), dim3(T::kThreads), T::kSmem, stream, a.overlap && !tail, a, tq, tkv, q_tma, box_rows, tail);
 }
 
 cudaError_t launch_g4_prefill(const RpaArgs& a, int num_sms, cudaStream_t stream, int tail) {
+    const bool cap = a.soft_cap != 0.f;
     switch (a.head_dim) {
-        case 64: return launch_pre<64>(a, num_sms, stream, tail);
-        case 128: return launch_pre<128>(a, num_sms, stream, tail);
-        case 256: return launch_pre<256>(a, num_sms, stream, tail);
+        case 64: return cap ? launch_pre<64, true>(a, num_sms, stream, tail) : launch_pre<64, false>(a, num_sms, stream, tail);
+        case 128: return cap ? launch_pre<128, true>(a, num_sms, stream, tail) : launch_pre<128, false>(a, num_sms, stream, tail);
+        case 256: return cap ? launch_pre<256, true>(a, num_sms, stream, tail) : launch_pre<256, false>(a, num_sms, stream, tail);
         default: return cudaErrorInvalidValue;
     }
 }
