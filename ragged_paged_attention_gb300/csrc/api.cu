@@ -836,9 +836,9 @@ static int check_key_weights_params(const rpa_params* p) {
 }
 
 struct KwLayout {
-    size_t ends_a, ends_b, ends_c, score_at, stats, scores, total;
+    size_t ends_a, ends_b, ends_c, ends_d, ends_e, tc, score_at, stats, tc_stats, scores, total;
     long long max_scores;
-    int max_items;
+    int max_items, max_tc_items;
 };
 
 static KwLayout key_weights_layout(const rpa_params* p) {
@@ -853,8 +853,17 @@ static KwLayout key_weights_layout(const rpa_params* p) {
     off = align_up(off + sizeof(int) * (size_t)p->max_num_seqs);
     L.ends_c = off;
     off = align_up(off + sizeof(int) * (size_t)p->max_num_seqs);
+    L.ends_d = off;
+    off = align_up(off + sizeof(int) * (size_t)p->max_num_seqs);
+    L.ends_e = off;
+    off = align_up(off + sizeof(int) * (size_t)p->max_num_seqs);
+    L.tc = off;
+    off = align_up(off + sizeof(int) * 8);
     L.score_at = off;
     off = align_up(off + sizeof(int) * (size_t)p->max_num_seqs);
+    L.max_tc_items = hkv * (int)((long long)p->max_num_tokens * G / 128 + p->max_num_seqs + 1) + kKwTcTarget + 64;
+    L.tc_stats = off;
+    off = align_up(off + sizeof(float2) * 256 * (size_t)L.max_tc_items);
     L.stats = off;
     L.max_items = (int)(tiles + kKwTarget + 64);
     off = align_up(off + sizeof(float2) * 16 * (size_t)L.max_items);
@@ -921,7 +930,14 @@ int rpa_key_weights(const rpa_params* p, const void* q, const void* kv_pages, co
     a.stats = reinterpret_cast<float2*>(ws + L.stats);
     a.scores = reinterpret_cast<float*>(ws + L.scores);
     a.max_scores = L.max_scores;
-    a.all_stored = (long long)p->max_num_tokens * (a.num_q_heads / a.num_kv_heads) <= 16 && L.max_scores < kKwScores;
+    a.scores_fit = L.max_scores < kKwScores;
+    a.all_stored = (long long)p->max_num_tokens * (a.num_q_heads / a.num_kv_heads) <= 16 && a.scores_fit;
+    a.ends_d = reinterpret_cast<int*>(ws + L.ends_d);
+    a.ends_e = reinterpret_cast<int*>(ws + L.ends_e);
+    a.tc = reinterpret_cast<int*>(ws + L.tc);
+    a.tc_stats = reinterpret_cast<float2*>(ws + L.tc_stats);
+    a.max_tc_items = L.max_tc_items;
+    a.use_tc = kw_tc_takes(a, p->head_dim, p->kv_dtype == RPA_DTYPE_G4);
     a.max_items = L.max_items;
     cudaError_t e = launch_key_weights(a, p->head_dim, p->kv_dtype == RPA_DTYPE_G4, sms, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "rpa_key_weights launch");

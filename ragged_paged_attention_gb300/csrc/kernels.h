@@ -263,6 +263,9 @@ constexpr int kKwMinPiece = 128, kKwTarget = 8192, kKwChunk = 128;
 // its items of the third kernel are kKwLong keys.
 constexpr long long kKwScores = 1ll << 27;
 constexpr int kKwLong = 512;
+// The tensor-core kernels' pieces: about kKwTcTarget of them in all, of blocks of 128 keys; at most kKwTcChunk blocks an item
+// of the second.
+constexpr int kKwTcTarget = 1200, kKwTcChunk = 8;
 
 struct KwArgs {
     const __nv_bfloat16* q;
@@ -287,7 +290,16 @@ struct KwArgs {
     long long max_scores;
     float2* stats;                  // 16 rows' (maximum, sum) an item of the first
     int max_items;                  // of the first
-    int all_stored;                 // no sequence can be left for the recomputing kernel
+    int scores_fit;                 // the workspace has room for the scores of every sequence of one tile, so that
+    int all_stored;                 // with tensor cores' kernels, or where every sequence has one, none is left to recompute
+    // sequences of more than 16 rows on the tensor cores' kernels (use_tc): ends of their items, both kernels' item
+    // counts, blocks of a piece and of a chunk and the counters of items taken ([6]), and the results of the first,
+    // 2 x 128 rows' (maximum, sum) an item
+    int use_tc, max_tc_items;
+    int* ends_d;
+    int* ends_e;
+    int* tc;
+    float2* tc_stats;
 };
 
 struct EvictArgs {
@@ -395,6 +407,8 @@ cudaError_t launch_g4_decode(const RpaArgs& a, int num_sms, cudaStream_t stream)
 int g4_decode_ctas_per_sm(const RpaArgs& a);
 cudaError_t launch_g4_prefill(const RpaArgs& a, int num_sms, cudaStream_t stream, int tail);
 int g4_prefill_rows(int head_dim);  // rows of an item
+bool kw_tc_takes(const KwArgs& a, int head_dim, bool g4);
+cudaError_t launch_kw_tc(const KwArgs& a, int head_dim, bool sum, int num_sms, cudaStream_t stream);
 cudaError_t launch_key_weights(const KwArgs& a, int head_dim, bool g4, int num_sms, cudaStream_t stream);
 cudaError_t launch_evict(EvictArgs& a, cudaStream_t stream);
 cudaError_t launch_g4_read(const RopeUpdateArgs& a, __nv_bfloat16* k_out, __nv_bfloat16* v_out, int num_sms, cudaStream_t stream);
@@ -455,6 +469,27 @@ __device__ __forceinline__ int seq_of_token(const int32_t* cu, int num, int t) {
         if (cu[mid] <= t) lo = mid; else hi = mid - 1;
     }
     return lo;
+}
+
+// Item `i`'s sequence: the first whose end (ascending) lies beyond i, found 32 at a time by the warp; `first`: the end
+// before it.
+__device__ __forceinline__ int kw_find(const int* ends, int num, int i, int& first) {
+    const int lane = threadIdx.x & 31;
+    int s = 0, left = num;
+    first = 0;
+    while (left > 0) {
+        const int stride = cdiv(left, 32), at = s + min(left, (lane + 1) * stride) - 1;
+        const bool before = lane * stride < left && ends[at] <= i;
+        const int upto = __popc(__ballot_sync(0xffffffffu, before));
+        if (stride == 1) {
+            s += upto;
+            break;
+        }
+        left = min(stride, left - upto * stride);
+        s += upto * stride;
+    }
+    if (s > 0) first = ends[s - 1];
+    return s;
 }
 
 // Whether the caller's batch_kind admits a sequence of this class (decode: q_len * G <= 16).

@@ -183,27 +183,6 @@ __device__ __forceinline__ float kw_log2(const KwArgs& a, float s) {
     return s * kLog2e;
 }
 
-// Item `i`'s sequence: the first whose end (ascending) lies beyond i, found 32 at a time by the warp; `first`: the end
-// before it.
-__device__ __forceinline__ int kw_find(const int* ends, int num, int i, int& first) {
-    const int lane = threadIdx.x & 31;
-    int s = 0, left = num;
-    first = 0;
-    while (left > 0) {
-        const int stride = cdiv(left, 32), at = s + min(left, (lane + 1) * stride) - 1;
-        const bool before = lane * stride < left && ends[at] <= i;
-        const int upto = __popc(__ballot_sync(0xffffffffu, before));
-        if (stride == 1) {
-            s += upto;
-            break;
-        }
-        left = min(stride, left - upto * stride);
-        s += upto * stride;
-    }
-    if (s > 0) first = ends[s - 1];
-    return s;
-}
-
 struct KwSeq {
     int q_start, q_len, kv_len, n_rows, tiles;
 };
@@ -230,7 +209,7 @@ __device__ __forceinline__ int kw_row_slots(int n_rows) { return n_rows <= 4 ? 4
 // their scores.
 __global__ void __launch_bounds__(1024) kw_plan_kernel(const __grid_constant__ KwArgs a) {
     __shared__ long long scan[40];
-    __shared__ float red[32];
+    __shared__ float red[3][32];
     const int tid = threadIdx.x, lane = tid & 31, G = a.num_q_heads / a.num_kv_heads;
     pdl_launch_dependents();  // (the next kernel waits for this one's end)
     pdl_wait();               // (the stream's earlier work may be writing the lengths)
@@ -264,22 +243,38 @@ __global__ void __launch_bounds__(1024) kw_plan_kernel(const __grid_constant__ K
         ql = c1 - c0;
         kl = ql ? k : 0;
     };
-    // keys x tiles of the batch, cut into about as many pieces as keep the warps busy
-    float work = 0.f;
+    // keys x tiles of the batch, cut into about as many pieces as keep the warps (and, for the tensor cores' kernels, the
+    // CTAs) busy
+    float work[3] = {0.f, 0.f, 0.f};  // keys x tiles of 16 rows; blocks x tiles of 128; blocks
+    auto count = [&](int ql, int kl) {
+        const float heads = (float)a.num_kv_heads;
+        if (a.use_tc && ql * G > 16) {
+            work[1] += (float)cdiv(ql * G, 128) * (float)cdiv(kl, 128) * heads;
+            work[2] += (float)cdiv(kl, 128) * heads;
+        } else {
+            work[0] += (float)cdiv(ql * G, 16) * (float)kl * heads;
+        }
+    };
     int ql0, kl0;
     shape(tid, ql0, kl0);
-    work = (float)cdiv(ql0 * G, 16) * (float)kl0 * (float)a.num_kv_heads;
+    count(ql0, kl0);
     for (int s = tid + blockDim.x; s < num; s += blockDim.x) {
         int ql, kl;
         shape(s, ql, kl);
-        work += (float)cdiv(ql * G, 16) * (float)kl * (float)a.num_kv_heads;
+        count(ql, kl);
     }
-    work = warp_sum(work);
-    if (lane == 0) red[tid >> 5] = work;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        work[i] = warp_sum(work[i]);
+        if (lane == 0) red[i][tid >> 5] = work[i];
+    }
     __syncthreads();
-    work = warp_sum(red[lane]);
-    const int piece = max(kKwMinPiece, (int)min((double)work / kKwTarget, 1e9) / kKwBK * kKwBK + kKwBK);
-    int base_a = 0, base_b = 0, base_c = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) work[i] = warp_sum(red[i][lane]);
+    const int piece = max(kKwMinPiece, (int)min((double)work[0] / kKwTarget, 1e9) / kKwBK * kKwBK + kKwBK);
+    const int tc_piece = 1 + (int)min((double)work[1] / kKwTcTarget, 1e9);
+    const int tc_chunk = max(1, min(kKwTcChunk, (int)(work[2] / (kKwTcTarget / 2))));
+    int base_a = 0, base_b = 0, base_c = 0, base_d = 0, base_e = 0;
     long long base_s = 0;  // scores, in units of 64
     for (int s0 = 0; s0 < num; s0 += blockDim.x) {
         int ql = ql0, kl = kl0;
@@ -291,26 +286,40 @@ __global__ void __launch_bounds__(1024) kw_plan_kernel(const __grid_constant__ K
         base_s += total;
         const bool stored = want > 0 && (at + want) * 64 <= a.max_scores;
         // (each count is far below 2^31; the first two share one scan)
-        const int na = cdiv(rows, 16) * a.num_kv_heads * cdiv(kl, piece);
-        const int nb = ql && !stored ? a.num_kv_heads * cdiv(kl, kKwChunk) : 0, nc = stored ? a.num_kv_heads * cdiv(kl, kKwLong) : 0;
+        const bool tc = a.use_tc && rows > 16;
+        const int na = tc ? 0 : cdiv(rows, 16) * a.num_kv_heads * cdiv(kl, piece);
+        const int nb = ql && !stored && !tc ? a.num_kv_heads * cdiv(kl, kKwChunk) : 0, nc = stored ? a.num_kv_heads * cdiv(kl, kKwLong) : 0;
         const long long ab = block_exclusive_scan(((long long)na << 32) | nb, scan, &total);
         const int total_a = (int)(total >> 32), total_b = (int)(total & 0xffffffffll);
+        long long total_de = 0, de = 0;
+        const int blocks = cdiv(kl, 128), nd = tc ? cdiv(rows, 128) * a.num_kv_heads * cdiv(blocks, tc_piece) : 0;
+        const int ne = tc ? a.num_kv_heads * cdiv(blocks, tc_chunk) : 0;
+        if (a.use_tc) de = block_exclusive_scan(((long long)nd << 32) | ne, scan, &total_de);
         const int c = (int)block_exclusive_scan((long long)nc, scan, &total);
         if (s0 + tid < num) {
             a.ends_a[s0 + tid] = base_a + (int)(ab >> 32) + na;
             a.ends_b[s0 + tid] = base_b + (int)(ab & 0xffffffffll) + nb;
             a.ends_c[s0 + tid] = base_c + c + nc;
             a.score_at[s0 + tid] = stored ? (int)at : -1;
+            a.ends_d[s0 + tid] = base_d + (int)(de >> 32) + nd;
+            a.ends_e[s0 + tid] = base_e + (int)(de & 0xffffffffll) + ne;
         }
+        base_d += (int)(total_de >> 32);
+        base_e += (int)(total_de & 0xffffffffll);
         base_a += total_a;
         base_b += total_b;
         base_c += (int)total;
     }
     if (tid == 0) {
-        if (base_a > a.max_items) {  // (only sequences that claim the same tokens make so many)
+        if (base_a > a.max_items || base_d > a.max_tc_items) {  // (only sequences that claim the same tokens make so many)
             set_error(&a.hdr->error_bits, RPA_DEV_ERR_TOKENS);
-            base_a = base_b = base_c = 0;
+            base_a = base_b = base_c = base_d = base_e = 0;
         }
+        a.tc[0] = base_d;
+        a.tc[1] = base_e;
+        a.tc[2] = tc_piece;
+        a.tc[3] = tc_chunk;
+        a.tc[4] = a.tc[5] = 0;
         a.hdr->num_items[0] = base_a;
         a.hdr->num_items[1] = base_b;
         a.hdr->num_items[2] = num;
@@ -628,6 +637,11 @@ static cudaError_t launch_kw(const KwArgs& a, int num_sms, cudaStream_t stream) 
     }
     // (so few query rows that every sequence has one tile, and the workspace room for all their scores: nothing is left)
     if (e != cudaSuccess || a.all_stored) return e;
+    if (a.use_tc) {
+        e = launch_kw_tc(a, D, false, num_sms, stream);
+        if (e == cudaSuccess) e = launch_kw_tc(a, D, true, num_sms, stream);
+        if (e != cudaSuccess || a.scores_fit) return e;
+    }
     ProfScope ps("rpa_kw_sum", stream);
     return launch_pdl(kern[1], dim3(num_sms * per_sm[dev][1]), dim3(kKwWarps * 32), T::kSmem, stream, pdl, a);
 }
