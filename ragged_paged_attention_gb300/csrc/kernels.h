@@ -260,7 +260,7 @@ struct MlaUpdateArgs {
 // the second kernel's items are kKwChunk keys.
 constexpr int kKwMinPiece = 128, kKwTarget = 8192, kKwChunk = 128;
 // A sequence of one row tile leaves its scores in the workspace, as far as kKwScores floats of it go (half a GB), and
-// its items of the third kernel are kKwLong keys.
+// the kernel that adds them up takes up to kKwLong keys an item.
 constexpr long long kKwScores = 1ll << 27;
 constexpr int kKwLong = 512;
 // The tensor-core kernels' pieces: about kKwTcTarget of them in all, of blocks of 128 keys; at most kKwTcChunk blocks an item
@@ -293,7 +293,8 @@ struct KwArgs {
     int scores_fit;                 // the workspace has room for the scores of every sequence of one tile, so that
     int all_stored;                 // with tensor cores' kernels, or where every sequence has one, none is left to recompute
     // sequences of more than 16 rows on the tensor cores' kernels (use_tc): ends of their items, both kernels' item
-    // counts, blocks of a piece and of a chunk and the counters of items taken ([6]), and the results of the first,
+    // counts, blocks of a piece and of a chunk, the counters of items taken (and, [6], the keys of an item of the kernel
+    // that adds stored scores up), and the results of the first,
     // 2 x 128 rows' (maximum, sum) an item
     int use_tc, max_tc_items;
     int* ends_d;

@@ -206,14 +206,15 @@ __device__ __forceinline__ void kw_range(const KwArgs& a, const KwSeq& q, int G,
 __device__ __forceinline__ int kw_row_slots(int n_rows) { return n_rows <= 4 ? 4 : n_rows <= 8 ? 8 : 16; }
 
 // Ends of the kernels' items, a sequence after another, the keys of a piece, and where sequences of one row tile leave
-// their scores.
-__global__ void __launch_bounds__(1024) kw_plan_kernel(const __grid_constant__ KwArgs a) {
+// their scores.  A chain of latencies: few threads, whose barriers are short (1024 of them: 16 us), the lengths in the same
+// round trip as their count, and two numbers a scan.
+constexpr int kKwPlan = 256;
+__global__ void __launch_bounds__(kKwPlan) kw_plan_kernel(const __grid_constant__ KwArgs a) {
     __shared__ long long scan[40];
-    __shared__ float red[3][32];
+    __shared__ float red[4][8];
     const int tid = threadIdx.x, lane = tid & 31, G = a.num_q_heads / a.num_kv_heads;
     pdl_launch_dependents();  // (the next kernel waits for this one's end)
     pdl_wait();               // (the stream's earlier work may be writing the lengths)
-    // the first sequences' numbers in the same round trip as their count
     const int mine = min(tid, a.max_num_seqs - 1);
     int c0 = a.cu_q_lens[mine], c1 = a.cu_q_lens[mine + 1], k = a.kv_lens[mine];
     int num = a.num_seqs[0];
@@ -243,72 +244,80 @@ __global__ void __launch_bounds__(1024) kw_plan_kernel(const __grid_constant__ K
         ql = c1 - c0;
         kl = ql ? k : 0;
     };
-    // keys x tiles of the batch, cut into about as many pieces as keep the warps (and, for the tensor cores' kernels, the
-    // CTAs) busy
-    float work[3] = {0.f, 0.f, 0.f};  // keys x tiles of 16 rows; blocks x tiles of 128; blocks
+    // the batch's work, cut into about as many pieces as keep the warps (and, for the tensor cores' kernels, the CTAs)
+    // busy: keys x tiles of 16 rows; keys of sequences of one tile; blocks x tiles of 128; blocks
+    float work[4] = {0.f, 0.f, 0.f, 0.f};
     auto count = [&](int ql, int kl) {
-        const float heads = (float)a.num_kv_heads;
         if (a.use_tc && ql * G > 16) {
-            work[1] += (float)cdiv(ql * G, 128) * (float)cdiv(kl, 128) * heads;
-            work[2] += (float)cdiv(kl, 128) * heads;
+            work[2] += (float)cdiv(ql * G, 128) * (float)cdiv(kl, 128);
+            work[3] += (float)cdiv(kl, 128);
         } else {
-            work[0] += (float)cdiv(ql * G, 16) * (float)kl * heads;
+            work[0] += (float)cdiv(ql * G, 16) * (float)kl;
+            if (ql * G <= 16) work[1] += (float)kl;
         }
     };
     int ql0, kl0;
     shape(tid, ql0, kl0);
     count(ql0, kl0);
-    for (int s = tid + blockDim.x; s < num; s += blockDim.x) {
+    for (int s = tid + kKwPlan; s < num; s += kKwPlan) {
         int ql, kl;
         shape(s, ql, kl);
         count(ql, kl);
     }
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < 4; ++i) {
         work[i] = warp_sum(work[i]);
         if (lane == 0) red[i][tid >> 5] = work[i];
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 3; ++i) work[i] = warp_sum(red[i][lane]);
+    for (int i = 0; i < 4; ++i) {
+        float v = 0.f;
+#pragma unroll
+        for (int j = 0; j < kKwPlan / 32; ++j) v += red[i][j];
+        work[i] = v * (float)a.num_kv_heads;
+    }
     const int piece = max(kKwMinPiece, (int)min((double)work[0] / kKwTarget, 1e9) / kKwBK * kKwBK + kKwBK);
-    const int tc_piece = 1 + (int)min((double)work[1] / kKwTcTarget, 1e9);
-    const int tc_chunk = max(1, min(kKwTcChunk, (int)(work[2] / (kKwTcTarget / 2))));
+    const int longest = min(kKwLong, max(64, ((int)min((double)work[1] / kKwTarget, 1e9) / 32 + 1) * 32));
+    const int tc_piece = 1 + (int)min((double)work[2] / kKwTcTarget, 1e9);
+    const int tc_chunk = max(1, min(kKwTcChunk, (int)(work[3] / (kKwTcTarget / 2))));
     int base_a = 0, base_b = 0, base_c = 0, base_d = 0, base_e = 0;
     long long base_s = 0;  // scores, in units of 64
-    for (int s0 = 0; s0 < num; s0 += blockDim.x) {
+    for (int s0 = 0; s0 < num; s0 += kKwPlan) {
         int ql = ql0, kl = kl0;
         if (s0) shape(s0 + tid, ql, kl);
         const int rows = ql * G;
-        long long total;
-        const long long want = rows > 0 && rows <= 16 ? (long long)cdiv(kl, 16) * kw_row_slots(rows) / 4 * a.num_kv_heads : 0;
-        const long long at = base_s + block_exclusive_scan(want, scan, &total);
-        base_s += total;
-        const bool stored = want > 0 && (at + want) * 64 <= a.max_scores;
-        // (each count is far below 2^31; the first two share one scan)
         const bool tc = a.use_tc && rows > 16;
+        // (scores: 32 bits are enough for what fits the workspace; a sequence with more has none)
+        const long long units = rows > 0 && rows <= 16 ? (long long)cdiv(kl, 16) * kw_row_slots(rows) / 4 * a.num_kv_heads : 0;
+        const long long want = units * 64 <= a.max_scores ? units : 0;
+        long long total;
         const int na = tc ? 0 : cdiv(rows, 16) * a.num_kv_heads * cdiv(kl, piece);
-        const int nb = ql && !stored && !tc ? a.num_kv_heads * cdiv(kl, kKwChunk) : 0, nc = stored ? a.num_kv_heads * cdiv(kl, kKwLong) : 0;
-        const long long ab = block_exclusive_scan(((long long)na << 32) | nb, scan, &total);
-        const int total_a = (int)(total >> 32), total_b = (int)(total & 0xffffffffll);
+        const long long sa = block_exclusive_scan((want << 32) | na, scan, &total);
+        const long long at = base_s + (sa >> 32);
+        const bool stored = want > 0 && (at + want) * 64 <= a.max_scores;
+        base_s += total >> 32;
+        const int total_a = (int)(total & 0xffffffffll);
+        const int nb = ql && !stored && !tc ? a.num_kv_heads * cdiv(kl, kKwChunk) : 0, nc = stored ? a.num_kv_heads * cdiv(kl, longest) : 0;
+        const long long bc = block_exclusive_scan(((long long)nb << 32) | nc, scan, &total);
+        const int total_b = (int)(total >> 32), total_c = (int)(total & 0xffffffffll);
         long long total_de = 0, de = 0;
         const int blocks = cdiv(kl, 128), nd = tc ? cdiv(rows, 128) * a.num_kv_heads * cdiv(blocks, tc_piece) : 0;
         const int ne = tc ? a.num_kv_heads * cdiv(blocks, tc_chunk) : 0;
-        if (a.use_tc) de = block_exclusive_scan(((long long)nd << 32) | ne, scan, &total_de);
-        const int c = (int)block_exclusive_scan((long long)nc, scan, &total);
+        if (work[3] > 0.f) de = block_exclusive_scan(((long long)nd << 32) | ne, scan, &total_de);
         if (s0 + tid < num) {
-            a.ends_a[s0 + tid] = base_a + (int)(ab >> 32) + na;
-            a.ends_b[s0 + tid] = base_b + (int)(ab & 0xffffffffll) + nb;
-            a.ends_c[s0 + tid] = base_c + c + nc;
+            a.ends_a[s0 + tid] = base_a + (int)(sa & 0xffffffffll) + na;
+            a.ends_b[s0 + tid] = base_b + (int)(bc >> 32) + nb;
+            a.ends_c[s0 + tid] = base_c + (int)(bc & 0xffffffffll) + nc;
             a.score_at[s0 + tid] = stored ? (int)at : -1;
             a.ends_d[s0 + tid] = base_d + (int)(de >> 32) + nd;
             a.ends_e[s0 + tid] = base_e + (int)(de & 0xffffffffll) + ne;
         }
-        base_d += (int)(total_de >> 32);
-        base_e += (int)(total_de & 0xffffffffll);
         base_a += total_a;
         base_b += total_b;
-        base_c += (int)total;
+        base_c += total_c;
+        base_d += (int)(total_de >> 32);
+        base_e += (int)(total_de & 0xffffffffll);
     }
     if (tid == 0) {
         if (base_a > a.max_items || base_d > a.max_tc_items) {  // (only sequences that claim the same tokens make so many)
@@ -320,6 +329,7 @@ __global__ void __launch_bounds__(1024) kw_plan_kernel(const __grid_constant__ K
         a.tc[2] = tc_piece;
         a.tc[3] = tc_chunk;
         a.tc[4] = a.tc[5] = 0;
+        a.tc[6] = longest;
         a.hdr->num_items[0] = base_a;
         a.hdr->num_items[1] = base_b;
         a.hdr->num_items[2] = num;
@@ -475,7 +485,7 @@ __device__ __forceinline__ float kw_norm(const KwArgs& a, int first_a, int head,
     return M + log2f(sum);
 }
 
-// The keys of sequences whose scores are stored: a warp takes kKwLong keys of a head, a key a lane.
+// The keys of sequences whose scores are stored: a warp takes up to kKwLong keys of a head, a key a lane.
 template <int R>
 __device__ __forceinline__ void kw_finish(const KwArgs& a, float L, const float* scores, const int* tbl, int head, int c0, int c1) {
     const int lane = threadIdx.x & 31;
@@ -502,15 +512,15 @@ __global__ void __launch_bounds__(kKwWarps * 32) kw_finish_kernel(const __grid_c
     const int G = a.num_q_heads / a.num_kv_heads;
     pdl_launch_dependents();  // (the kernel behind works on other sequences' keys, and waits for this one's end)
     pdl_wait();
-    const int n_items = a.hdr->num_items[3], num = a.hdr->num_items[2], piece = a.hdr->chunk_keys;
+    const int n_items = a.hdr->num_items[3], num = a.hdr->num_items[2], piece = a.hdr->chunk_keys, longest = a.tc[6];
     while (true) {
         const int item = kw_take(&a.hdr->next_item[2]);
         if (item >= n_items) break;
         int first;
         const int s = kw_find(a.ends_c, num, item, first), first_a = s > 0 ? a.ends_a[s - 1] : 0, store = a.score_at[s];
         const KwSeq q = kw_seq(a, s, G);
-        const int chunks = cdiv(q.kv_len, kKwLong), rel = item - first, head = rel / chunks, c0 = rel % chunks * kKwLong;
-        const int c1 = min(q.kv_len, c0 + kKwLong), slots = kw_row_slots(q.n_rows);
+        const int chunks = cdiv(q.kv_len, longest), rel = item - first, head = rel / chunks, c0 = rel % chunks * longest;
+        const int c1 = min(q.kv_len, c0 + longest), slots = kw_row_slots(q.n_rows);
         const float L = kw_norm(a, first_a, head, 0, q, cdiv(q.kv_len, piece));
         const float* scores = a.scores + (size_t)store * 64 + (size_t)head * cdiv(q.kv_len, 16) * 16 * slots;
         const int* tbl = a.page_indices + (size_t)s * a.pages_per_seq;
@@ -649,7 +659,7 @@ static cudaError_t launch_kw(const KwArgs& a, int num_sms, cudaStream_t stream) 
 cudaError_t launch_key_weights(const KwArgs& a, int head_dim, bool g4, int num_sms, cudaStream_t stream) {
     {
         ProfScope ps("rpa_kw_plan", stream);
-        const cudaError_t e = launch_pdl(kw_plan_kernel, dim3(1), dim3(1024), 0, stream, !prof_enabled(), a);
+        const cudaError_t e = launch_pdl(kw_plan_kernel, dim3(1), dim3(kKwPlan), 0, stream, !prof_enabled(), a);
         if (e != cudaSuccess) return e;
     }
     switch (head_dim) {

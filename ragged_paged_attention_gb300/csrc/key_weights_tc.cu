@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(KwTc<D>::kThreads, 1)
                         M[k] = -INFINITY;
                         sum[k] = 0.f;
                     }
-#pragma unroll 2
+#pragma unroll 8
                     for (int i = 0; i < 2 * it.pieces; ++i) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
