@@ -325,24 +325,24 @@ __global__ void __launch_bounds__(G4Dec<D, HG>::kThreads) g4_decode_kernel(const
                                     for (int g = 0; g < NG; ++g) vs[t][h][g] = seen[h] ? vs[t][h][g] : 0u;
                             }
                         }
-                        // the reference maximum moves only when a row's has grown by more than 2^8
-                        float mx[2], muse[2];
+                        // The reference maximum moves only when some score of a row is more than 2^8 above it: until then no
+                        // lane asks another
                         bool grown = false;
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            mx[j] = fmaxf(sc[0][j], sc[0][2 + j]);
-                            if (NT == 2) mx[j] = fmax3(mx[j], sc[NT - 1][j], sc[NT - 1][2 + j]);
-                            mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 4));
-                            mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 8));
-                            mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 16));
-                            grown |= mx[j] > m_run[j] + 8.f;
-                        }
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) grown |= sc[t][e] > m_run[e & 1] + 8.f;
                         if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
-                                const bool g = mx[j] > m_run[j] + 8.f;
-                                const float f = g ? fast_exp2(m_run[j] - mx[j]) : 1.f;
-                                if (g) m_run[j] = mx[j];
+                                float mx = fmaxf(sc[0][j], sc[0][2 + j]);
+                                if (NT == 2) mx = fmax3(mx, sc[NT - 1][j], sc[NT - 1][2 + j]);
+                                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                                const bool g = mx > m_run[j] + 8.f;
+                                const float f = g ? fast_exp2(m_run[j] - mx) : 1.f;
+                                if (g) m_run[j] = mx;
                                 l_run[j] *= f;
 #pragma unroll
                                 for (int i = 0; i < NG * TG; ++i) {
@@ -356,6 +356,7 @@ __global__ void __launch_bounds__(G4Dec<D, HG>::kThreads) g4_decode_kernel(const
                                 }
                             }
                         }
+                        float muse[2];
 #pragma unroll
                         for (int j = 0; j < 2; ++j) muse[j] = m_run[j] == -INFINITY ? 0.f : m_run[j];
 #pragma unroll

@@ -643,7 +643,7 @@ static cudaError_t launch_kw(const KwArgs& a, int num_sms, cudaStream_t stream) 
     if (e != cudaSuccess) return e;
     {
         ProfScope ps("rpa_kw_finish", stream);
-        e = launch_pdl(kw_finish_kernel, dim3(num_sms * 8), dim3(kKwWarps * 32), 0, stream, pdl, a);
+        e = launch_pdl(kw_finish_kernel, dim3(num_sms * 16), dim3(kKwWarps * 32), 0, stream, pdl, a);
     }
     // (so few query rows that every sequence has one tile, and the workspace room for all their scores: nothing is left)
     if (e != cudaSuccess || a.all_stored) return e;
