@@ -19,6 +19,9 @@
 // rows of HG heads in one bulk copy; a consumer warp a KV head, keys on the M side of m16n8k16, up to 8 query
 // rows on its N side; items split the keys (flash-decoding) along the plan's equal shares, and a group's last CTA
 // joins its pieces.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "common.cuh"
 #include "g4.cuh"
 #include "kernels.h"
@@ -32,12 +35,11 @@ struct G4Dec {
     // tiles at once: two, so that the chains of loads, products, maxima and exponentials of one run beside the other's (and
     // the maximum's exchange and the barriers come once for both); head_dim 256 has no registers for that
     static constexpr int NT = D == 256 ? 1 : 2;
-    static constexpr int kSeg = HG * G4<D>::kRow;
-    // rows 24 words apart modulo the 32 banks: K's 8-byte loads (four rows of 32 bytes a half-warp) and, with
-    // the keys' order of key_of, V's 4-byte loads (four rows of 32 bytes) touch every bank once
-    static constexpr int kPitch = kSeg + 32;
-    static_assert(kPitch / 4 % 32 == 24 && kSeg % 16 == 0, "bank pattern");
-    static constexpr int kStage = BK * kPitch;
+    // A stage is two tiles, a tile its heads one behind another, each 16 rows of kPitch bytes. Rows 8 or 24 words apart modulo the 32 banks
+    // let K's 8-byte loads (four rows of 32 bytes a half-warp) and, with the keys' order of key_of, V's 4-byte loads
+    // touch every bank once; at head_dim 64 (4- and 2-byte loads) 20 words do. A box copies the padding with its rows.
+    static constexpr int kPitch = D == 128 ? 160 : G4<D>::kRow;
+    static constexpr int kHead = 16 * kPitch, kTile = HG * kHead, kStage = 2 * kTile;
     static constexpr int STAGES = 3;
     static constexpr int kBarOff = STAGES * kStage;
     static constexpr int kSmem = kBarOff + 2 * STAGES * 8;
@@ -49,7 +51,8 @@ struct G4Dec {
 __device__ __forceinline__ int g4_key_of(int r) { return r ^ ((r >> 2) & 1); }
 
 template <int D, int HG>
-__global__ void __launch_bounds__(G4Dec<D, HG>::kThreads) g4_decode_kernel(const __grid_constant__ RpaArgs a) {
+__global__ void __launch_bounds__(G4Dec<D, HG>::kThreads)
+    g4_decode_kernel(const __grid_constant__ RpaArgs a, const __grid_constant__ CUtensorMap tm_kv, int boxes) {
     using T = G4Dec<D, HG>;
     using F = G4<D>;
     constexpr int BK = T::BK, STAGES = T::STAGES, NG = F::NG;
@@ -57,7 +60,7 @@ __global__ void __launch_bounds__(G4Dec<D, HG>::kThreads) g4_decode_kernel(const
     constexpr int TG = F::kGroup / 16;       // V tiles of 16 dims a group: 2 or 4
     constexpr int kRowO = HG * kDecodeRows;  // rows of an item's partial result
     constexpr float kUp = 0x1p69f;           // 2^(133 - 64): P s goes in times 2^64
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + T::kBarOff);
     uint64_t* empty = full + STAGES;
     __shared__ WorkItem s_item;
@@ -120,14 +123,14 @@ __global__ void __launch_bounds__(G4Dec<D, HG>::kThreads) g4_decode_kernel(const
         const uint32_t seg_bytes = seg_heads * F::kRow;
 
         if (producer) {
-            // lane t has key t of every stage; pages are looked up two stages ahead (one was not enough: a stage then
-            // took a load's latency)
+            // Pages are looked up two stages ahead (one was not enough: a stage then took a load's latency).
             const int* tbl = a.page_indices + (size_t)s * a.pages_per_seq;
-            const bool pow2 = (a.page_size & (a.page_size - 1)) == 0;
-            const int lps = __ffs(a.page_size) - 1;
+            // A lane asks for a tile's keys of all its heads with one box (page sizes that are whole tiles; the keys begin at a
+            // multiple of 16, so that a tile lies in one page), or for one key, head by head.
+            const int rows = boxes ? 16 : 1, lps = __ffs(a.page_size) - 1;
             auto page_of = [&](int blk) -> int {
-                const int key = kb + blk * BK + lane;
-                return blk < n_blocks && key < ke ? __ldg(tbl + (pow2 ? key >> lps : key / a.page_size)) : -1;
+                const int key = kb + blk * BK + lane * rows;
+                return blk < n_blocks && lane * rows < BK && key < ke ? __ldg(tbl + (boxes ? key >> lps : key / a.page_size)) : -1;
             };
             int page_next = page_of(0), page_then = page_of(1);
             for (int blk = 0; blk < n_blocks; ++blk) {
@@ -135,15 +138,15 @@ __global__ void __launch_bounds__(G4Dec<D, HG>::kThreads) g4_decode_kernel(const
                 const int page = page_next;
                 page_next = page_then;
                 page_then = page_of(blk + 2);
-                const int key = kb + blk * BK + lane;
-                const bool ok = key < ke && (unsigned)page < (unsigned)a.total_num_pages;
-                if (key < ke && !ok) set_error(err, RPA_DEV_ERR_PAGE);
+                const int key = kb + blk * BK + lane * rows;
+                const bool want = lane * rows < BK && key < ke, ok = want && (unsigned)page < (unsigned)a.total_num_pages;
+                if (want && !ok) set_error(err, RPA_DEV_ERR_PAGE);
                 const uint32_t mask = __ballot_sync(0xffffffffu, ok);
                 int go = 1;
                 if (lane == 0) {
                     go = mbar_wait(&empty[st], ph ^ 1, err);
                     if (go) {
-                        mbar_arrive_expect_tx(&full[st], __popc(mask) * seg_bytes);
+                        mbar_arrive_expect_tx(&full[st], __popc(mask) * (boxes ? (uint32_t)T::kTile : (uint32_t)(seg_heads * F::kRow)));
                         issued = q + 1;
                     } else {
                         s_abort = 1;
@@ -151,10 +154,16 @@ __global__ void __launch_bounds__(G4Dec<D, HG>::kThreads) g4_decode_kernel(const
                 }
                 go = __shfl_sync(0xffffffffu, go, 0);
                 if (!go) break;
-                const int in_page = pow2 ? key & (a.page_size - 1) : key % a.page_size;
-                if (ok)
-                    bulk_g2s(smem_u32(smem + st * T::kStage + lane * T::kPitch),
-                             kv + (((size_t)page * a.page_size + in_page) * Hkv + h0) * F::kRow, seg_bytes, &full[st]);
+                if (ok) {
+                    const uint32_t dst = smem_u32(smem + st * T::kStage);
+                    if (boxes) {
+                        tma_load_3d(dst + lane * T::kTile, &tm_kv, 0, (page << lps) + (key & (a.page_size - 1)), h0, &full[st]);
+                    } else {
+                        const uint8_t* src = kv + (((size_t)page * a.page_size + key % a.page_size) * Hkv + h0) * F::kRow;
+                        for (int h = 0; h < seg_heads; ++h)
+                            bulk_g2s(dst + (lane >> 4) * T::kTile + h * T::kHead + (lane & 15) * T::kPitch, src + h * F::kRow, F::kRow, &full[st]);
+                    }
+                }
             }
         } else {
             // ---------------- consumer warp: KV head h0 + warp ----------------
@@ -252,13 +261,13 @@ __global__ void __launch_bounds__(G4Dec<D, HG>::kThreads) g4_decode_kernel(const
                         constexpr int NT = T::NT;
                         const int b0 = kb + blk * BK + 16 * sub;  // the tiles' first key
                         if (NT == 1 && b0 >= ke) break;
-                        const uint8_t* stg = smem + st * T::kStage + 16 * sub * T::kPitch + warp * F::kRow;
+                        const uint8_t* stg = smem + st * T::kStage + sub * T::kTile + warp * T::kHead;
                         const uint8_t* r0 = stg + kk * T::kPitch;  // this lane's keys: kk and kk + 8 of a tile
                         float sc[NT][4];
                         uint32_t vs[NT][2][NG];  // (s, m) of V's groups
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
-                            const uint8_t* rt = r0 + 16 * t * T::kPitch;
+                            const uint8_t* rt = r0 + t * T::kTile;
                             uint32_t ks[2][NG];
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
@@ -370,8 +379,8 @@ __global__ void __launch_bounds__(G4Dec<D, HG>::kThreads) g4_decode_kernel(const
                         // 2 q4 + 1, 2 q4 + 8, 2 q4 + 9: a byte permute pairs two keys' numbers
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
-                            const uint8_t* va = stg + (16 * t + g4_key_of(2 * q4)) * T::kPitch + F::kPart + g8 * (F::kGroup / 16);
-                            const uint8_t* vb = stg + (16 * t + g4_key_of(2 * q4 + 1)) * T::kPitch + F::kPart + g8 * (F::kGroup / 16);
+                            const uint8_t* va = stg + t * T::kTile + g4_key_of(2 * q4) * T::kPitch + F::kPart + g8 * (F::kGroup / 16);
+                            const uint8_t* vb = stg + t * T::kTile + g4_key_of(2 * q4 + 1) * T::kPitch + F::kPart + g8 * (F::kGroup / 16);
 #pragma unroll
                             for (int g = 0; g < NG; ++g) {
                                 const int off = g * (F::kGroup / 2);
@@ -520,8 +529,14 @@ static cudaError_t launch_dec(const RpaArgs& a, int num_sms, cudaStream_t stream
         *per_sm_out = per_sm[dev];
         return cudaSuccess;
     }
-    ProfScope ps("rpa_g4_decode", stream);
-    return launch_pdl(kern, dim3(num_sms * per_sm[dev]), dim3(T::kThreads), T::kSmem, stream, a.overlap != 0, a);
+    CUtensorMap tkv;
+    memset(&tkv, 0, sizeof tkv);
+    const int ps = a.page_size;
+    const long long tokens = (long long)a.total_num_pages * ps;
+    const int boxes = (ps & (ps - 1)) == 0 && ps >= 16 && tokens <= INT32_MAX &&
+                      make_tmap_heads(&tkv, a.kv_pages, G4<D>::kRow, a.num_kv_heads, (uint64_t)tokens, T::kPitch, 16, HG);
+    ProfScope prof("rpa_g4_decode", stream);
+    return launch_pdl(kern, dim3(num_sms * per_sm[dev]), dim3(T::kThreads), T::kSmem, stream, a.overlap != 0, a, tkv, boxes);
 }
 
 static cudaError_t dispatch(const RpaArgs& a, int num_sms, cudaStream_t stream, int* per_sm_out) {

@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
                         if (lane == 0) mbar_arrive_expect_tx(&raw_full[slot], (uint32_t)(boxes * box_rows * F::kRow));
                         __syncwarp();
                         if (lane < boxes)
-                            tma_load_3d(dst + lane * box_rows * F::kRow, &tm_kv, 0, it.head, (page << lps) + ((key0 + lane * box_rows) & (a.page_size - 1)),
+                            tma_load_3d(dst + lane * box_rows * F::kRow, &tm_kv, 0, (page << lps) + ((key0 + lane * box_rows) & (a.page_size - 1)), it.head,
                                         &raw_full[slot]);
                     } else {
                         for (int i = lane; i < valid * (F::kRow / 16); i += 32) {
@@ -685,7 +685,7 @@ static cudaError_t launch_pre(const RpaArgs& a, int num_sms, cudaStream_t stream
     // boxes of a page's rows, or a block's part of them: at least 8, so that each starts on 128 bytes
     int box_rows = (ps & (ps - 1)) == 0 && ps >= 8 ? (ps < T::BK ? ps : T::BK) : 0;
     if ((long long)a.total_num_pages * ps > INT32_MAX) box_rows = 0;
-    if (box_rows && !make_tmap_rows(&tkv, a.kv_pages, G4<D>::kRow, a.num_kv_heads, (uint64_t)a.total_num_pages * ps, box_rows)) box_rows = 0;
+    if (box_rows && !make_tmap_heads(&tkv, a.kv_pages, G4<D>::kRow, a.num_kv_heads, (uint64_t)a.total_num_pages * ps, G4<D>::kRow, box_rows, 1)) box_rows = 0;
     ProfScope prof(tail == 1 ? "rpa_g4_prefill_tail" : "rpa_g4_prefill", stream);
     return launch_pdl(kern, dim3(num_sms), dim3(T::kThreads), T::kSmem, stream, a.overlap && !tail, a, tq, tkv, q_tma, box_rows, tail);
 }

@@ -397,7 +397,8 @@ cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, c
 // 3-D bf16 tensor [d2][d1][d0] (d0 contiguous) with a box of {64, b1, b2}, 128-byte swizzle.
 bool make_tmap_bf16(struct CUtensorMap_st* tm, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b1,
                     uint32_t b2);
-bool make_tmap_rows(struct CUtensorMap_st* tm, const void* base, uint64_t bytes, uint64_t d1, uint64_t d2, uint32_t b2);
+bool make_tmap_heads(struct CUtensorMap_st* tm, const void* base, uint64_t bytes, uint64_t heads, uint64_t tokens, uint32_t pitch,
+                     uint32_t b_tokens, uint32_t b_heads);
 // Cross attention with two tiles in flight an SM: every sequence, decode's too, of the batches it takes.
 bool rpa_cross_tc_takes(const RpaArgs& a);
 int rpa_cross_tile_rows(const RpaArgs& a);  // 256 or 128: the rows of an item
