@@ -103,7 +103,8 @@ RpaLayout rpa_layout(const rpa_params* p) {
     RpaLayout L;
     const int hkv = p->num_combined_kv_heads / 2;
     const int G = p->num_q_heads / hkv;
-    const int dh = decode_heads_for(p->head_dim, p->kv_dtype != RPA_DTYPE_BF16);
+    const int dh = p->kv_dtype == RPA_DTYPE_G4 ? g4_decode_heads(p->head_dim, hkv)
+                                               : decode_heads_for(p->head_dim, p->kv_dtype != RPA_DTYPE_BF16);
     const int groups = cdiv(hkv, dh);
     // pieces: one per CTA share plus one more per group a share boundary cuts (groups: up to two
     // 8-row halves per sequence and KV-head group)
@@ -443,6 +444,7 @@ static int rpa_prepare(const rpa_params* p, const void* q, const void* kv_pages,
     a.prefill_rows = kPrefillRows;
     if (g4) {
         a.prefill_rows = g4_prefill_rows(p->head_dim);
+        a.decode_heads = g4_decode_heads(p->head_dim, a.num_kv_heads);
         g4_rates(p->head_dim, &a.pre_flops_per_ns_sm, &a.dec_bytes_per_ns_sm, &a.dec_hbm_bytes_per_ns);
     }
     a.decode_per_sm = g4 ? g4_decode_ctas_per_sm(a) : rpa_decode_ctas_per_sm(a);

@@ -44,6 +44,7 @@ struct G4Dec {
     static constexpr int kBarOff = STAGES * kStage;
     static constexpr int kSmem = kBarOff + 2 * STAGES * 8;
     static constexpr int kThreads = (HG + 1) * 32;
+    static constexpr int kCtas = D == 256 ? 2 : 3;  // an SM's: as many as the stages let in
 };
 
 // The stage's key in row r of the M side (and r + 8 the one 8 further on): the order in which both K's and V's rows
@@ -51,7 +52,7 @@ struct G4Dec {
 __device__ __forceinline__ int g4_key_of(int r) { return r ^ ((r >> 2) & 1); }
 
 template <int D, int HG>
-__global__ void __launch_bounds__(G4Dec<D, HG>::kThreads)
+__global__ void __launch_bounds__(G4Dec<D, HG>::kThreads, G4Dec<D, HG>::kCtas)
     g4_decode_kernel(const __grid_constant__ RpaArgs a, const __grid_constant__ CUtensorMap tm_kv, int boxes) {
     using T = G4Dec<D, HG>;
     using F = G4<D>;
@@ -543,7 +544,9 @@ static cudaError_t dispatch(const RpaArgs& a, int num_sms, cudaStream_t stream, 
     switch (a.head_dim) {
         case 64: return launch_dec<64, 4>(a, num_sms, stream, per_sm_out);
         case 128: return launch_dec<128, 4>(a, num_sms, stream, per_sm_out);
-        case 256: return launch_dec<256, 2>(a, num_sms, stream, per_sm_out);
+        // Two heads a CTA leave four warps an SM that compute (64 decodes that see 1024 to 4096 keys of 8 heads, with a
+        // soft cap: 180 us; four heads a CTA 128), but half of four would idle where a cache has two heads.
+        case 256: return a.decode_heads == 4 ? launch_dec<256, 4>(a, num_sms, stream, per_sm_out) : launch_dec<256, 2>(a, num_sms, stream, per_sm_out);
         default: return cudaErrorInvalidValue;
     }
 }

@@ -407,6 +407,8 @@ cudaError_t launch_rpa_cross_tc(const RpaArgs& a, int num_sms, cudaStream_t stre
 cudaError_t launch_g4_forward(const RpaArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_g4_decode(const RpaArgs& a, int num_sms, cudaStream_t stream);
 int g4_decode_ctas_per_sm(const RpaArgs& a);
+// KV heads of a decode item over a 4-bit cache: 4, or 2 at head_dim 256 where the cache's are not a multiple of 4.
+inline int g4_decode_heads(int head_dim, int num_kv_heads) { return head_dim >= 256 && num_kv_heads % 4 != 0 ? 2 : 4; }
 cudaError_t launch_g4_prefill(const RpaArgs& a, int num_sms, cudaStream_t stream, int tail);
 int g4_prefill_rows(int head_dim);  // rows of an item
 bool kw_tc_takes(const KwArgs& a, int head_dim, bool g4);
