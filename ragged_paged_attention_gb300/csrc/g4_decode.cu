@@ -13,7 +13,7 @@
 //     its key from one 16-byte load a key, and sum Q of the group from registers.  Q is brought to 2^119..2^120
 //     by a power of two of its row (its other bf16 bits stay).  Every product is exact.
 //   * V: P s goes in as the B operand, one a group; what m adds is a sum over keys of p (m + 7.5 s) in float32,
-//     less 7.5 times the sum of the rounded P s, which a product with ones gives: the rounding of P s to bf16 (2^-9
+//     less 7.5 times the sum of the rounded P s, which a product with ones gives: the rounding of P s to bf16 (2^-8
 //     of itself) then counts for n - 7.5, a value's distance from the middle, not for n.
 // Otherwise as the kernel for wider caches: a producer warp resolves pages one stage ahead and copies each token's
 // rows of HG heads in one bulk copy; a consumer warp a KV head, keys on the M side of m16n8k16, up to 8 query

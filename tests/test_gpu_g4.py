@@ -207,9 +207,74 @@ def test_scales_of_the_values(up, d):
     b.q = (b.q.float() / up).to(BF16)
     got, bits = attend(b, sm_scale=d ** -0.5)
     assert bits == 0
-    # powers of two change no rounding; the pieces of a sequence join in another order, which float32 sums show
+    # Powers of two change no rounding of the keys. V at its own size and P with it are f16 in long queries (2^-11), past
+    # f16's range bf16: P, V and both outputs then have independent roundings of 2^-8 at most, 2^-8 / sqrt(3) in the
+    # root mean square
     a, c = one[:b.t].double(), got[:b.t].double() / 2.0 ** 30
+    assert (a - c).norm() <= 2 * 2.0 ** -8 / math.sqrt(3) * a.norm()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("up", [2.0 ** -5, 0.25, 4.0])
+def test_sizes_of_v_within_f16(up, d):
+    b = Batch(*LENS, 8, 2, d, 16, seed=d)
+    one = check(b)
+    n = d // group_of(d)
+    p = b.kv[..., d:].contiguous().view(BF16).unflatten(-1, (2, 2 * n))
+    p[..., 1, :] *= up
+    b.kv[..., d:] = p.flatten(-2).view(torch.uint8)
+    got = check(b)
+    # powers of two change no rounding; the pieces of a sequence join in another order, which float32 sums show
+    a, c = one[:b.t].double(), got[:b.t].double() / up
     assert (a - c).norm() <= 1e-3 * a.norm()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_a_key_of_nearly_all_the_weight(d):
+    # the first key takes all but some 2^-12 of each row and has no value: what is left is the others' average
+    b = Batch([300, 40], [900, 400], 4, 2, d, 16, seed=d)
+    n = d // group_of(d)
+    p = b.kv[..., d:].contiguous().view(BF16).unflatten(-1, (2, 2 * n))
+    for i in range(2):
+        p[int(b.table[i, 0]), 0, :, 0, 0::2] = 0.0         # a key of ones, no values
+        p[int(b.table[i, 0]), 0, :, 0, 1::2] = 1.0
+        p[int(b.table[i, 0]), 0, :, 1] = 0.0
+    b.kv[..., d:] = p.flatten(-2).view(torch.uint8)
+    scale = d ** -0.5
+    # the queries' sums put the first key's scores log(900 * 2^12) above zero
+    b.q = (b.q.float() + math.log(900 * 2.0 ** 12) / (scale * d)).to(BF16)
+    got, bits = attend(b, sm_scale=scale)
+    assert bits == 0
+    want = b.attention(scale)
+    # check's roundings (queries of a greater size); weights of 2^-22 of the greatest, held in f16 times 2^7 in steps of 2^-24,
+    # keep 2^-10 of themselves, beside which the 2^-8 leave that out
+    norm_q = float((b.q[:b.t].double().pow(2).sum(-1) / d).sqrt().mean())
+    tol = 6 * 2.0 ** -8 / math.sqrt(3) * math.sqrt(3 + norm_q ** 2)
+    err, size = (got[:b.t].double().cpu() - want).norm(dim=-1), want.norm(dim=-1)
+    assert (size > 0).all() and (err <= tol * size).all(), float((err / size).max())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("run", [64, 13])
+def test_sizes_of_v_from_key_to_key(run, d):
+    # V of runs of keys at sizes within f16's range, above and below it, and zeros; a row sees the nearest 20 keys, or all
+    b = Batch([300, 1, 90], [700, 500, 90], 4, 2, d, 16, seed=d)
+    n = d // group_of(d)
+    sizes = torch.tensor([1.0, 2.0 ** 20, 2.0 ** -14, 0.0, 0.125, 2.0 ** 40, 2.0 ** -30])
+    p = b.kv[..., d:].contiguous().view(BF16).unflatten(-1, (2, 2 * n))
+    for i, kv_len in enumerate([700, 500, 90]):
+        key = torch.arange(kv_len)
+        page = b.table[i, key // 16].long()
+        p[page, key % 16, :, 1, :] *= sizes[key // run % len(sizes)].to(BF16)[:, None, None]
+    b.kv[..., d:] = p.flatten(-2).view(torch.uint8)
+    for window in (20, None):
+        got, bits = attend(b, sm_scale=d ** -0.5, sliding_window=window)
+        assert bits == 0
+        want = b.attention(d ** -0.5, window)
+        # each row by itself, within 6 deviations of check's roundings
+        tol = 6 * 2.0 ** -8 / math.sqrt(3) * math.sqrt(3 + 1)
+        err, size = (got[:b.t].double().cpu() - want).norm(dim=-1), want.norm(dim=-1)
+        assert (err <= tol * size).all(), float((err / size.clamp_min(1e-300)).max())
 
 
 def test_long_context_offsets_past_32_bits():
