@@ -34,7 +34,7 @@
 namespace rpa {
 
 struct __align__(16) G4Item {
-    int seq, head, row, q_start, q_len, kv_len, block0, blocks;
+    int seq, head, row, q_start, q_len, kv_len, block0, blocks, place;
 };
 
 template <int D>
@@ -53,9 +53,9 @@ struct G4Pre {
     static constexpr int kOffRaw = kOffV + NV * kTile;
     static constexpr int kOffBar = kOffRaw + NR * kRaw;
     static constexpr int kBars = 2 * (NK + NV + NR) + 9 + (3 + 2 * PB) * TILES;
-    static constexpr int kOffItem = (kOffBar + kBars * 8 + 15) / 16 * 16;  // [2] G4Item, abort, TMEM base, exit, items to do again
-    static constexpr int kOffRedo = kOffItem + 2 * (int)sizeof(G4Item) + 16;  // [2] G4Item to do again, [2][2] int
-    static constexpr int kSmem = kOffRedo + 2 * (int)sizeof(G4Item) + 16;
+    static constexpr int kOffItem = (kOffBar + kBars * 8 + 15) / 16 * 16;  // [2] G4Item, abort, TMEM base, exit, first item to do again
+    static constexpr int kOffFits = kOffItem + 2 * (int)sizeof(G4Item) + 16;  // [2][2] int
+    static constexpr int kSmem = kOffFits + 16;
     static constexpr int kSoft = 4 * TILES;
     static constexpr int kThreads = (kSoft + 8) * 32;
     static constexpr int kColS = 0;
@@ -106,8 +106,8 @@ __device__ __forceinline__ uint32_t f16x2_fma(uint32_t a, uint32_t b, uint32_t c
 // (2^-11 of a value at most, not bf16's 2^-8) count for nothing beside the output's own. A number alone is the f16 subnormal
 // n 2^-24 (or n 2^-20), and values are held times 2^-10: a group fits with s < 4 (s 2^14 is a factor), |m| < 2^20, and s >= 2^-9
 // or |m| >= 2^-6 (below that a value has no more bits than bf16 gives it), or as zeros. V's converters look at the groups on
-// their way; an item in which one does not fit is done again with bf16 (2^-53 of V, 2^43 of P: the same 2^-10), as are
-// all that the CTA takes after it. (Looked at block by block before its V is turned: 4 x 4096 prompts 552 us, not 497.)
+// their way; an item in which one does not fit is done again with bf16 (2^-53 of V, 2^43 of P: the same 2^-10), which
+// makes such a cache's prompts twice as long. (Looked at block by block before its V is turned: 4 x 4096 prompts 552 us, not 497.)
 constexpr float kDownV = 0x1p-10f;
 // P and l are held times 2^7: at most 2^15 (the reference maximum may lag by 2^8), and f16 keeps 8 bits of weights down to
 // 2^-24 of a row's greatest (behind a first key of nearly all the weight and hardly any value, the others count).
@@ -155,9 +155,8 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     volatile int* flags = reinterpret_cast<volatile int*>(smem + T::kOffItem + 2 * sizeof(G4Item));
     volatile int& s_abort = flags[0];
-    G4Item* s_redo = reinterpret_cast<G4Item*>(smem + T::kOffRedo);
-    volatile int* out_of_f16 = reinterpret_cast<volatile int*>(s_redo + 2);  // of item n (n & 1), by V converter: does not fit
-    volatile int& n_redo = flags[3];
+    volatile int* item_fits = reinterpret_cast<volatile int*>(smem + T::kOffFits);  // V of item n (n & 1) in f16, by V converter
+    volatile int& s_again = flags[3];
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + T::kOffItem + 2 * sizeof(G4Item) + 4);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     WsHeader* hdr = a.hdr;
@@ -221,7 +220,8 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
     };
     if (tid == 0) {
         init_barriers();
-        s_abort = n_redo = 0;
+        s_abort = 0;
+        s_again = -1;
     }
     if (warp == kMma0) tmem_alloc(tmem_slot, T::kTmemCols);
     tc_fence_before();
@@ -487,15 +487,15 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
                 // ---------------- items and Q ----------------
                 const int n_items = hdr->num_items[1];
                 uint32_t fetched = 0;
-                // Item n, done in f16, goes to the list of those to do again where its V does not fit.
+                // Items with a V that f16 does not fit are done again in bf16 once there are no more: a chain through the list's
+                // entries (an item's type follows from its values alone, not from which CTA took it when).
                 auto ask = [&](uint32_t n) {
                     if (!kF16 || s_abort) return;
                     if (!mbar_wait(&turned[n & 1], (n >> 1) & 1, err)) {
                         s_abort = 1;
-                    } else if (out_of_f16[2 * (n & 1)] | out_of_f16[2 * (n & 1) + 1]) {
-                        out_of_f16[2 * (n & 1)] = out_of_f16[2 * (n & 1) + 1] = 0;
-                        s_redo[n_redo] = s_items[n & 1];
-                        n_redo = n_redo + 1;
+                    } else if (!item_fits[2 * (n & 1)] || !item_fits[2 * (n & 1) + 1]) {
+                        a.pre_items[s_items[n & 1].place].key_begin = s_again;
+                        s_again = s_items[n & 1].place;
                     }
                 };
                 auto fetch = [&]() {
@@ -505,15 +505,18 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
                     if (!mbar_wait(&item_empty[slot], ph ^ 1, err)) s_abort = 1;
                     // beside decode, no new item once most decode CTAs with a share are out of work: what is left goes to
                     // the launch after decode, on every SM
-                    const bool stop = s_abort || (!tail && a.overlap && hdr->dec_ctas > 0 &&
+                    const bool stop = s_abort || (kF16 && !tail && a.overlap && hdr->dec_ctas > 0 &&
                                                   *(volatile const int*)&hdr->next_item[0] >= max(1, hdr->dec_ctas * kPrefillStopPercent / 100));
                     if (fetched >= 2) ask(fetched - 2);
-                    const bool again = !kF16 && (int)fetched < n_redo;
-                    const int place = stop || again || (kF16 && n_redo > 0) ? n_items : atomicAdd(&hdr->next_item[1], 1);
-                    if (again) {
-                        n = s_redo[fetched];
-                    } else if (place < n_items) {
+                    int place = n_items;
+                    if (kF16 && !stop) place = atomicAdd(&hdr->next_item[1], 1);
+                    if (!kF16 && !s_abort && s_again >= 0) {
+                        place = s_again;
+                        s_again = a.pre_items[place].key_begin;
+                    }
+                    if (place < n_items) {
                         const WorkItem w = a.pre_items[place];
+                        n.place = place;
                         n.seq = w.seq;
                         n.head = w.head;
                         n.row = w.row_begin;
@@ -707,7 +710,7 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
                 if (kF16 && part) {
                     fits = __all_sync(0xffffffffu, fits);
                     if (lane == 0) {
-                        out_of_f16[2 * ((items - 1) & 1) + warp - kConv0 - 2] = !fits;
+                        item_fits[2 * ((items - 1) & 1) + warp - kConv0 - 2] = fits;
                         mbar_arrive(&turned[(items - 1) & 1]);
                     }
                 }
@@ -721,20 +724,18 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
     tc_fence_before();
     __syncthreads();  // (every role has ended, and with it every copy and product)
     tc_fence_after();
-    const bool redo = n_redo > 0 && !s_abort;
-    __syncthreads();
-    if (redo) {
+    if (s_again >= 0 && !s_abort) {
+        __syncthreads();
         if (tid == 0) {
             for (int i = 0; i < T::kBars; ++i) mbar_inval(&k_full[i]);
             init_barriers();
         }
         __syncthreads();
         work(std::false_type());
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
     }
-    // every role has left its loop
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
     if (warp == kMma0) tmem_dealloc(tmem, T::kTmemCols);
 }
 

@@ -390,3 +390,36 @@ def test_calls_on_two_streams():
     torch.cuda.synchronize()
     for o in outs:
         assert torch.equal(o[:b.t].view(torch.int16), want[:b.t].view(torch.int16))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_an_item_type_follows_from_its_own_values(d):
+    # V of some heads and sequences beyond f16's range, others within it: each sequence's outputs are the same alone and among the
+    # others, in every run, whichever order the SMs take the items in
+    q_lens, kv_lens = [700, 40, 600, 90, 500], [900, 900, 600, 300, 1200]
+    b = Batch(q_lens, kv_lens, 8, 4, d, 16, seed=d)
+    n = d // group_of(d)
+    p = b.kv[..., d:].contiguous().view(BF16).unflatten(-1, (2, 2 * n))
+    for i in range(5):
+        for h in range(4):
+            if (i + h) % 2:
+                at = b.place[i]
+                p[at // 16, at % 16, h, 1] *= 2.0 ** (10 if h % 2 else -20)
+    b.kv[..., d:] = p.flatten(-2).view(torch.uint8)
+    first, bits = attend(b, sm_scale=d ** -0.5)
+    assert bits == 0
+    want = b.attention(d ** -0.5)
+    tol = 6 * 2.0 ** -8 / math.sqrt(3) * math.sqrt(3 + 1)
+    err, size = (first[:b.t].double().cpu() - want).norm(dim=-1), want.norm(dim=-1)
+    assert (err <= tol * size).all(), float((err / size).max())
+    for _ in range(5):
+        got, bits = attend(b, sm_scale=d ** -0.5)
+        assert bits == 0 and torch.equal(got[:b.t].view(torch.int16), first[:b.t].view(torch.int16))
+    kv, lens, pages, _, num = b.gpu()
+    q = b.q.cuda()
+    num.fill_(1)
+    for i, m in enumerate(q_lens):
+        a = int(b.cu[i])
+        cu = torch.tensor([0, m], dtype=torch.int32, device="cuda")
+        got = api.rpa_g4_forward(q[a:a + m], kv, lens[i:i + 1], pages[i:i + 1].contiguous(), cu, num, sm_scale=d ** -0.5)
+        assert torch.equal(got.view(torch.int16), first[a:a + m].view(torch.int16))
