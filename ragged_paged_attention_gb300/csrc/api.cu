@@ -819,6 +819,9 @@ int rpa_g4_forward(const rpa_params* p, const void* q, const void* kv_pages, con
     // so few query rows that every sequence is decode-class: the prefill launches are left out
     if (a.batch_kind == RPA_BATCH_MIXED && (long long)p->max_num_tokens * (a.num_q_heads / a.num_kv_heads) <= 16)
         a.batch_kind = RPA_BATCH_DECODE_ONLY;
+    // (sharing the SMs between the classes, or starting one's launch before the other's end, does not pay: 64 decodes and 2 x 1024
+    // tokens of a 4096-key window 338 us so, 348 with both)
+    if (a.batch_kind == RPA_BATCH_MIXED && p->head_dim == 256) a.overlap = 0;
     a.min_chunk = kStepMinChunk + a.item_cost_keys;
     cudaError_t e = launch_g4_forward(a, sms, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "rpa_g4_forward launch");

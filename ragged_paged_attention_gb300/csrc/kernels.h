@@ -75,11 +75,16 @@ inline void rpa_rates(int head_dim, bool fp8, bool scale, bool pow2, float* pre,
     *dec = conv ? (fp8 && pow2 ? 38.f : 26.f) : 60.f;
 }
 
-// The same of the 4-bit cache's kernels, its bytes counted as one an element.
+// The same of the 4-bit cache's kernels (its bytes counted as one an element): prompts at 7200, 4200 and 4300 GFLOP/s an SM,
+// decodes at 43 to 47 GB/s an SM. Beside prompts, decodes are taken to reach no more than 3500 GB/s on any share of the SMs, so
+// that the two kernels share the SMs in most mixed batches: 128 decodes over up to 8192 keys beside 2 x 1024 tokens (8 KV
+// heads of 128) take 324 us so, 393 one after another (of 64: 261 and 304; beside 4 x 512 tokens 340 and 397; 32
+// decodes beside 4 x 1024 250 and 268; with 5500 in the place of 3500 some batches fall back to the latter). At head_dim
+// 256 they run one after another on plain launches (rpa_g4_forward).
 inline void g4_rates(int head_dim, float* pre, float* dec, float* hbm) {
-    *pre = head_dim >= 256 ? 3000.f : head_dim >= 128 ? 6500.f : 4500.f;
+    *pre = head_dim >= 256 ? 4300.f : head_dim >= 128 ? 7200.f : 4200.f;
     *dec = 45.f;
-    *hbm = 10000.f;
+    *hbm = 3500.f;
 }
 
 // A scale the f16 paths may take: a power of two with e4m3 * scale inside bf16's normal range
