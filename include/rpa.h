@@ -411,8 +411,9 @@ RPA_API int rpa_g4_read_kv_cache(const rpa_params* p, const void* kv_pages, cons
                                  void* v_out, void* workspace, size_t workspace_bytes, rpa_stream_t stream);
 
 /* rpa_forward over such a cache: the same arguments, masks and options (sliding_window, soft_cap, batch_kind).
- * `workspace`: rpa_g4_workspace_size bytes.  Sequences of more than 16 query rows a KV head see K and V rounded to
- * bf16. */
+ * `workspace`: rpa_g4_workspace_size bytes.  Sequences of more than 16 query rows a KV head see K rounded to bf16 and V
+ * to f16, or to bf16 where a group of V that a tile of queries sees has s >= 4, |m| >= 2^20, or both s < 2^-9 and |m| < 2^-6
+ * (the weights are rounded to the same type; prompts over such caches take up to twice as long). */
 RPA_API int rpa_g4_workspace_size(const rpa_params* p, size_t* bytes);
 RPA_API int rpa_g4_forward(const rpa_params* p, const void* q, const void* kv_pages, const int32_t* kv_lens,
                            const int32_t* page_indices, const int32_t* cu_q_lens, const int32_t* num_seqs, void* out,
@@ -431,7 +432,8 @@ RPA_API int rpa_g4_forward(const rpa_params* p, const void* q, const void* kv_pa
  * for every key of the batch's sequences (0 new weight where no query sees it); other entries are left as they are, as
  * are those of sequences without queries.  A slot that two sequences of a batch share gets either's.  kv_dtype is
  * RPA_DTYPE_BF16 or RPA_DTYPE_G4, head_dim 64, 128 or 256, k_scale and v_scale 0, mask_value NaN.  Queries: a decode
- * step's, to add up over steps, or a prompt's last ones.  `workspace`: rpa_key_weights_workspace_size bytes. */
+ * step's, to add up over steps, or a prompt's last ones.  `workspace`: rpa_key_weights_workspace_size bytes,
+ * up to half a GB of it for the scores of sequences of up to 16 query rows a KV head; those past it are computed twice. */
 RPA_API int rpa_key_weights_workspace_size(const rpa_params* p, size_t* bytes);
 RPA_API int rpa_key_weights(const rpa_params* p, const void* q, const void* kv_pages, const int32_t* kv_lens,
                             const int32_t* page_indices, const int32_t* cu_q_lens, const int32_t* num_seqs, const float* weights,

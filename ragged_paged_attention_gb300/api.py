@@ -1186,8 +1186,8 @@ def selftest_bounded_wait(workspace: torch.Tensor) -> None:
 def check_device_status(workspace: torch.Tensor | None = None) -> int:
     """Synchronise, read and clear the workspace error word; returns its bits (0 = fine).
 
-    Without a workspace: that of this thread's ``rpa_cross_forward`` and ``rpa_rope_forward_update`` calls on
-    the current stream that were given none.  (A captured call's own workspace is the graph's: give it one
+    Without a workspace: that of this thread's ``rpa_cross_forward``, ``rpa_rope_forward_update``, ``rpa_g4_forward``,
+    ``rpa_key_weights`` and ``rpa_evict_kv_cache`` calls on the current stream that were given none.  (A captured call's own workspace is the graph's: give it one
     to read its word.)"""
     lib = load_library()
     if workspace is None:

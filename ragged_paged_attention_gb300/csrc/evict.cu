@@ -8,13 +8,17 @@
 //
 // Selection: weights as integers of their order, the keep-th largest found 11 bits at a time from histograms in
 // shared memory, then one pass that counts and one that places, each thread on a run of consecutive slots.
+//
+// 48 sequences of 4000 to 12000 keys cut to 2048, 8 heads of 128 in bf16: selection 59 us (384 blocks, up to two an SM;
+// latencies of shared memory and barriers over five passes), moving 104 us (0.57 GB, rows of 512 bytes read and written
+// all over the pages: 5.4 TB/s), 155 us together.
 #include "common.cuh"
 #include "kernels.h"
 #include "profile.h"
 
 namespace rpa {
 
-constexpr int kEvictThreads = 512;
+constexpr int kEvictThreads = 1024;  // (48 sequences cut to 2048 keys: 156 us, with 512 threads 162; one 20 and 22)
 constexpr int kEvictBins = 2048;
 constexpr int kEvictAhead = 8;
 constexpr int kEvictHeld = 49152;      // most keys whose order a block holds in shared memory
@@ -182,7 +186,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
 }
 
 // A warp takes 32 slots of a head: their weights, a lane each, and the rows that come from elsewhere, 16 bytes a lane.
-constexpr int kMoveThreads = 256;
+constexpr int kMoveThreads = 128;  // (1 % less time than with 256)
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs a, int blocks_per_head) {
     __shared__ const uint4* from[kMoveThreads];
     __shared__ uint4* to[kMoveThreads];

@@ -262,15 +262,17 @@ struct MlaUpdateArgs {
 };
 
 // Key weights: a warp's piece of a row tile's keys is at least kKwMinPiece keys, and about kKwTarget of them are made;
-// the second kernel's items are kKwChunk keys.
+// the second kernel's items are kKwChunk keys. (96 decodes over 2000 to 8192 keys: 242 us, with 4096 of them 263, with 16384 239
+// but twice the results to join; at least 256 keys: the same. 6 decodes over up to 20000 4-bit keys: 50 us, 47 with 4096.)
 constexpr int kKwMinPiece = 128, kKwTarget = 8192, kKwChunk = 128;
 // A sequence of one row tile leaves its scores in the workspace, as far as kKwScores floats of it go (half a GB), and
-// the kernel that adds them up takes up to kKwLong keys an item.
+// the kernel that adds them up takes up to kKwLong keys an item (of 256, 512 or 1024 none is faster).
 constexpr long long kKwScores = 1ll << 27;
 constexpr int kKwLong = 512;
-// The tensor-core kernels' pieces: about kKwTcTarget of them in all, of blocks of 128 keys; at most kKwTcChunk blocks an item
-// of the second.
-constexpr int kKwTcTarget = 1200, kKwTcChunk = 8;
+// The tensor-core kernels' pieces: about kKwTcTarget of them in all (three an SM), of blocks of 128 keys; at most kKwTcChunk blocks
+// an item of the second. (8 windows over 8000 to 16000 keys: 106 us, with 1200 pieces 123, with 600 108, with 2400 181; with 4
+// blocks 142, with 16 2 % more than with 8.)
+constexpr int kKwTcTarget = 456, kKwTcChunk = 8;
 
 struct KwArgs {
     const __nv_bfloat16* q;

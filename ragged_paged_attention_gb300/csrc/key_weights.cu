@@ -10,6 +10,11 @@
 // waits for nobody else. A row's running maximum and sum stay in each lane on the keys it holds, and meet once an item.
 // Scores are exact products in float32: bf16 operands, or the 4-bit numbers as bf16 subnormals with their groups'
 // accumulators apart (g4_decode.cu). Maxima, sums and L are float32; exponentials are ex2.approx (2^-22), soft caps tanhf.
+//
+// 96 decodes over 2000 to 8192 keys, 32/8 heads of 128, bf16: 192 us for the statistics (1 GB of K in rows of 256 bytes, every
+// other 256 of a page: 5.3 TB/s) and 47 us for the sums (16 bytes of scores and 8 of weights a key; bound by the latency
+// of page table, scores and weights in a row). With the scores computed again instead of stored the call took 561 us,
+// not 241.
 #include "common.cuh"
 #include "g4.cuh"
 #include "kernels.h"
