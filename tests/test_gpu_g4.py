@@ -167,6 +167,13 @@ def test_ragged_lengths(hq, hkv, d, ps):
     check(Batch(*LENS, hq, hkv, d, ps, seed=hq * d + ps))
 
 
+@pytest.mark.parametrize("hq,hkv,ps", [(16, 8, 32), (8, 4, 16), (8, 4, 12), (24, 12, 1), (32, 4, 64), (6, 6, 16)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_numbers_of_kv_heads(hq, hkv, ps, d):
+    check(Batch(*LENS, hq, hkv, d, ps, seed=hq * d + ps))
+    check(Batch([1, 2, 1], [5000, 3, 900], hq, hkv, d, ps, seed=hkv), sliding_window=700)
+
+
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("q_lens,kv_lens", [([1] * 40, list(range(1, 3000, 75))), ([1], [20000]), ([1, 1], [1, 2]), ([1], [16]), ([4], [17]),
                                             ([129], [129]), ([64, 64], [127, 129]), ([1000], [1000]), ([0, 0], [5, 0]),
