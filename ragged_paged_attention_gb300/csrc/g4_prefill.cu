@@ -739,6 +739,28 @@ __global__ void __launch_bounds__(G4Pre<D>::kThreads, 1)
     if (warp == kMma0) tmem_dealloc(tmem, T::kTmemCols);
 }
 
+// Rows of `bytes` bytes (a multiple of 16, at most 1024), [tokens][heads] of them, dense, as a tensor [heads][tokens][row]
+// with a box of b_heads x b_tokens rows, each `pitch` bytes apart where it lands (zeros behind the row), without a swizzle.
+bool make_tmap_heads(CUtensorMap* tm, const void* base, uint64_t bytes, uint64_t heads, uint64_t tokens, uint32_t pitch, uint32_t b_tokens,
+                     uint32_t b_heads) {
+    static PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+    if (!enc) {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            return false;
+        enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }
+    const cuuint64_t dims[3] = {bytes / 4, tokens, heads};
+    const cuuint64_t strides[2] = {bytes * heads, bytes};
+    const cuuint32_t box[3] = {pitch / 4, b_tokens, b_heads};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, bool CAP>
 static cudaError_t launch_pre(const RpaArgs& a, int num_sms, cudaStream_t stream, int tail) {
     using T = G4Pre<D>;

@@ -1132,21 +1132,6 @@ bool make_tmap_bf16(CUtensorMap* tm, const void* base, uint64_t d0, uint64_t d1,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows of `bytes` bytes (a multiple of 16, at most 1024), [tokens][heads] of them, dense, as a tensor [heads][tokens][row]
-// with a box of b_heads x b_tokens rows, each `pitch` bytes apart where it lands (zeros behind the row), without a swizzle.
-bool make_tmap_heads(CUtensorMap* tm, const void* base, uint64_t bytes, uint64_t heads, uint64_t tokens, uint32_t pitch, uint32_t b_tokens,
-                     uint32_t b_heads) {
-    auto enc = tmap_encoder();
-    if (!enc) return false;
-    const cuuint64_t dims[3] = {bytes / 4, tokens, heads};
-    const cuuint64_t strides[2] = {bytes * heads, bytes};
-    const cuuint32_t box[3] = {pitch / 4, b_tokens, b_heads};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // 3-D one-byte tensor [d2][d1][d0] (d0 contiguous) with a box of {128, 1, b2}, 128-byte swizzle:
 // half of a raw K or V row per copy (the raw-staging path).
 static bool make_tmap_u8(CUtensorMap* tm, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b2) {
