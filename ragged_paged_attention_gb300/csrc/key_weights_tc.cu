@@ -50,7 +50,8 @@ __device__ __forceinline__ void kw_tc_blocks(const KwArgs& a, const KwTcItem& it
 
 template <int D, bool SUM>
 __global__ void __launch_bounds__(KwTc<D>::kThreads, 1)
-    kw_tc_kernel(const __grid_constant__ KwArgs a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv, int box_rows) {
+    kw_tc_kernel(const __grid_constant__ KwArgs a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv, int q_tma,
+                 int box_rows) {
     using T = KwTc<D>;
     constexpr int NQ = T::NQ, NK = T::NK;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -346,11 +347,28 @@ __global__ void __launch_bounds__(KwTc<D>::kThreads, 1)
                 const uint32_t qs = jq % NQ;
                 ok = __all_sync(0xffffffffu, mbar_wait(&q_empty[qs], ((jq / NQ) & 1) ^ 1, err));
                 if (!ok) break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&q_full[qs], T::kTile);
+                if (q_tma) {
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&q_full[qs], T::kTile);
 #pragma unroll
-                    for (int p = 0; p < T::DP; ++p)
-                        tma_load_3d(smem_u32(smem + qs * T::kTile + p * T::kPanel), &tm_q, 64 * p, it.head * G, it.q_start + tile * 128 / G, &q_full[qs]);
+                        for (int p = 0; p < T::DP; ++p)
+                            tma_load_3d(smem_u32(smem + qs * T::kTile + p * T::kPanel), &tm_q, 64 * p, it.head * G, it.q_start + tile * 128 / G,
+                                        &q_full[qs]);
+                    }
+                } else {
+                    // a group size that does not divide a tile: 16 bytes at a time, rows that are not there as zeros (8 windows with 48/8
+                    // heads: 321 us; on mma.sync 855)
+                    for (int i = lane; i < 128 * (D / 8); i += 32) {
+                        const int tr = i / (D / 8), c = i % (D / 8), R = tile * 128 + tr;
+                        const bool rv = R < it.q_len * G;
+                        cp_async16(smem_u32(smem + qs * T::kTile + (c >> 3) * T::kPanel + tr * 128 + (((c & 7) ^ (tr & 7)) << 4)),
+                                   a.q + ((size_t)(it.q_start + (rv ? R / G : 0)) * a.num_q_heads + it.head * G + (rv ? R % G : 0)) * D + c * 8, rv);
+                    }
+                    cp_async_commit();
+                    cp_async_wait<0>();
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&q_full[qs]);
                 }
                 ++jq;
                 auto page_of = [&](int b) -> int {
@@ -399,7 +417,7 @@ __global__ void __launch_bounds__(KwTc<D>::kThreads, 1)
 }
 
 template <int D, bool SUM>
-static cudaError_t launch_tc(const KwArgs& a, int num_sms, cudaStream_t stream, const CUtensorMap& tq, const CUtensorMap& tkv, int box_rows) {
+static cudaError_t launch_tc(const KwArgs& a, int num_sms, cudaStream_t stream, const CUtensorMap& tq, const CUtensorMap& tkv, int q_tma, int box_rows) {
     using T = KwTc<D>;
     auto kern = kw_tc_kernel<D, SUM>;
     static bool configured[64] = {};  // (by device: the attribute is the device's)
@@ -413,25 +431,26 @@ static cudaError_t launch_tc(const KwArgs& a, int num_sms, cudaStream_t stream, 
         configured[dev] = true;
     }
     ProfScope ps(SUM ? "rpa_kw_tc_sum" : "rpa_kw_tc_stats", stream);
-    return launch_pdl(kern, dim3(num_sms), dim3(T::kThreads), T::kSmem, stream, !prof_enabled(), a, tq, tkv, box_rows);
+    return launch_pdl(kern, dim3(num_sms), dim3(T::kThreads), T::kSmem, stream, !prof_enabled(), a, tq, tkv, q_tma, box_rows);
 }
 
 bool kw_tc_takes(const KwArgs& a, int head_dim, bool g4) {
-    const int G = a.num_q_heads / a.num_kv_heads, ps = a.page_size;
-    return !g4 && a.soft_cap == 0.f && a.sm_scale > 0.f && (head_dim == 64 || head_dim == 128 || head_dim == 256) && 128 % G == 0 &&
+    const int ps = a.page_size;
+    return !g4 && a.soft_cap == 0.f && a.sm_scale > 0.f && (head_dim == 64 || head_dim == 128 || head_dim == 256) &&
            (ps & (ps - 1)) == 0 && ps >= 8 && (long long)a.total_num_pages * ps <= INT32_MAX;
 }
 
 cudaError_t launch_kw_tc(const KwArgs& a, int head_dim, bool sum, int num_sms, cudaStream_t stream) {
     CUtensorMap tq, tkv;
-    const int G = a.num_q_heads / a.num_kv_heads, ps = a.page_size, box_rows = ps < 128 ? ps : 128;
+    memset(&tq, 0, sizeof tq);
+    const int G = a.num_q_heads / a.num_kv_heads, ps = a.page_size, box_rows = ps < 128 ? ps : 128, q_tma = 128 % G == 0;
     if (!make_tmap_bf16(&tkv, a.kv_pages, head_dim, 2 * a.num_kv_heads, (uint64_t)a.total_num_pages * ps, 1, box_rows) ||
-        !make_tmap_bf16(&tq, a.q, head_dim, a.num_q_heads, a.max_num_tokens, G, 128 / G))
+        (q_tma && !make_tmap_bf16(&tq, a.q, head_dim, a.num_q_heads, a.max_num_tokens, G, 128 / G)))
         return cudaErrorInvalidValue;
     switch (head_dim) {
-        case 64: return sum ? launch_tc<64, true>(a, num_sms, stream, tq, tkv, box_rows) : launch_tc<64, false>(a, num_sms, stream, tq, tkv, box_rows);
-        case 128: return sum ? launch_tc<128, true>(a, num_sms, stream, tq, tkv, box_rows) : launch_tc<128, false>(a, num_sms, stream, tq, tkv, box_rows);
-        case 256: return sum ? launch_tc<256, true>(a, num_sms, stream, tq, tkv, box_rows) : launch_tc<256, false>(a, num_sms, stream, tq, tkv, box_rows);
+        case 64: return sum ? launch_tc<64, true>(a, num_sms, stream, tq, tkv, q_tma, box_rows) : launch_tc<64, false>(a, num_sms, stream, tq, tkv, q_tma, box_rows);
+        case 128: return sum ? launch_tc<128, true>(a, num_sms, stream, tq, tkv, q_tma, box_rows) : launch_tc<128, false>(a, num_sms, stream, tq, tkv, q_tma, box_rows);
+        case 256: return sum ? launch_tc<256, true>(a, num_sms, stream, tq, tkv, q_tma, box_rows) : launch_tc<256, false>(a, num_sms, stream, tq, tkv, q_tma, box_rows);
         default: return cudaErrorInvalidValue;
     }
 }

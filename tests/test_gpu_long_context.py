@@ -77,6 +77,12 @@ def test_weights_of_batch_shapes(q_lens, kv_lens, g4):
     check_weights(Batch(q_lens, kv_lens, 8, 2, 128, 16, g4=g4, seed=len(q_lens)))
 
 
+@pytest.mark.parametrize("hq,hkv", [(12, 2), (40, 8), (48, 1), (71, 1), (130, 1), (160, 1)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_weights_of_group_sizes(hq, hkv, d):
+    check_weights(Batch([1, 3, 0, 2, 40, 1, 30], [1, 700, 64, 2, 40, 600, 330], hq, hkv, d, 16, seed=hq), sliding_window=200 if hq == 40 else None)
+
+
 @pytest.mark.parametrize("g4", [False, True])
 def test_weights_of_many_sequences(g4):
     g = torch.Generator().manual_seed(5)
