@@ -9,9 +9,12 @@
 // A block of 128 x 128 scores is 512 cycles of the tensor pipe and of the exponentials (D = 128) and 32 KB of K, which
 // HBM brings in some 700: both kernels are bound by reading K where a sequence has one tile, by the exponentials where
 // it has many. 8 windows of 32 queries over 8000-16000 keys, 32/8 heads of 128: STATS 45 us, SUM 53 (185 MB of K each: 4.1
-// and 3.5 TB/s with one tile in flight an SM); 16 rows at a time on mma.sync 252 and 326 us. Scores are exact products summed in float32; maxima, sums and L are float32.
+// and 3.5 TB/s with one tile in flight an SM); 16 rows at a time on mma.sync 252 and 326 us. With a soft cap
+// (tanhf) 102 and 137 us, 401 and 464 there. Scores are exact products summed in float32; maxima, sums and L are float32.
 #include <cuda.h>
 #include <cudaTypedefs.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -48,7 +51,7 @@ __device__ __forceinline__ void kw_tc_blocks(const KwArgs& a, const KwTcItem& it
     hi = max(lo, min(it.block1, (end + 127) >> 7));
 }
 
-template <int D, bool SUM>
+template <int D, bool SUM, bool CAP>
 __global__ void __launch_bounds__(KwTc<D>::kThreads, 1)
     kw_tc_kernel(const __grid_constant__ KwArgs a, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv, int q_tma,
                  int box_rows) {
@@ -112,7 +115,8 @@ __global__ void __launch_bounds__(KwTc<D>::kThreads, 1)
         // ---------------- scores: this group's buffer ----------------
         const int group = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t col_s = tmem + ((uint32_t)(quarter * 32) << 16) + group * 128;
-        const float cs = a.sm_scale * kLog2e;  // (> 0: the host's condition)
+        const float cs = CAP ? kLog2e : a.sm_scale * kLog2e;  // (> 0: the host's condition)
+        [[maybe_unused]] const float cap = a.soft_cap, to_cap = a.sm_scale / a.soft_cap;
         float* Ls = reinterpret_cast<float*>(smem + T::kOffL) + warp * 128;  // (a warp's own copy: no warp waits for another)
         uint32_t mine = 0;  // blocks of this group so far
         bool ok = true;
@@ -129,6 +133,10 @@ __global__ void __launch_bounds__(KwTc<D>::kThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_free[group]);
+            if constexpr (CAP) {
+#pragma unroll
+                for (int i = 0; i < 128; ++i) x[i] = cap * tanhf(x[i] * to_cap);
+            }
             return true;
         };
         while (ok && next_item(it, false)) {
@@ -416,10 +424,10 @@ __global__ void __launch_bounds__(KwTc<D>::kThreads, 1)
     if (warp == kMma) tmem_dealloc(tmem, 256);
 }
 
-template <int D, bool SUM>
+template <int D, bool SUM, bool CAP>
 static cudaError_t launch_tc(const KwArgs& a, int num_sms, cudaStream_t stream, const CUtensorMap& tq, const CUtensorMap& tkv, int q_tma, int box_rows) {
     using T = KwTc<D>;
-    auto kern = kw_tc_kernel<D, SUM>;
+    auto kern = kw_tc_kernel<D, SUM, CAP>;
     static bool configured[64] = {};  // (by device: the attribute is the device's)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -436,7 +444,7 @@ static cudaError_t launch_tc(const KwArgs& a, int num_sms, cudaStream_t stream, 
 
 bool kw_tc_takes(const KwArgs& a, int head_dim, bool g4) {
     const int ps = a.page_size;
-    return !g4 && a.soft_cap == 0.f && a.sm_scale > 0.f && (head_dim == 64 || head_dim == 128 || head_dim == 256) &&
+    return !g4 && (a.soft_cap != 0.f || a.sm_scale > 0.f) && (head_dim == 64 || head_dim == 128 || head_dim == 256) &&
            (ps & (ps - 1)) == 0 && ps >= 8 && (long long)a.total_num_pages * ps <= INT32_MAX;
 }
 
@@ -447,10 +455,18 @@ cudaError_t launch_kw_tc(const KwArgs& a, int head_dim, bool sum, int num_sms, c
     if (!make_tmap_bf16(&tkv, a.kv_pages, head_dim, 2 * a.num_kv_heads, (uint64_t)a.total_num_pages * ps, 1, box_rows) ||
         (q_tma && !make_tmap_bf16(&tq, a.q, head_dim, a.num_q_heads, a.max_num_tokens, G, 128 / G)))
         return cudaErrorInvalidValue;
+    auto launch = [&](auto dim) {
+        constexpr int D = decltype(dim)::value;
+        if (a.soft_cap != 0.f)
+            return sum ? launch_tc<D, true, true>(a, num_sms, stream, tq, tkv, q_tma, box_rows)
+                       : launch_tc<D, false, true>(a, num_sms, stream, tq, tkv, q_tma, box_rows);
+        return sum ? launch_tc<D, true, false>(a, num_sms, stream, tq, tkv, q_tma, box_rows)
+                   : launch_tc<D, false, false>(a, num_sms, stream, tq, tkv, q_tma, box_rows);
+    };
     switch (head_dim) {
-        case 64: return sum ? launch_tc<64, true>(a, num_sms, stream, tq, tkv, q_tma, box_rows) : launch_tc<64, false>(a, num_sms, stream, tq, tkv, q_tma, box_rows);
-        case 128: return sum ? launch_tc<128, true>(a, num_sms, stream, tq, tkv, q_tma, box_rows) : launch_tc<128, false>(a, num_sms, stream, tq, tkv, q_tma, box_rows);
-        case 256: return sum ? launch_tc<256, true>(a, num_sms, stream, tq, tkv, q_tma, box_rows) : launch_tc<256, false>(a, num_sms, stream, tq, tkv, q_tma, box_rows);
+        case 64: return launch(std::integral_constant<int, 64>());
+        case 128: return launch(std::integral_constant<int, 128>());
+        case 256: return launch(std::integral_constant<int, 256>());
         default: return cudaErrorInvalidValue;
     }
 }

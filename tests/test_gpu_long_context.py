@@ -84,6 +84,13 @@ def test_weights_of_group_sizes(hq, hkv, d):
 
 
 @pytest.mark.parametrize("g4", [False, True])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("scale,cap", [(-0.2, 20.0), (0.0, 5.0), (0.3, 1.5), (-0.1, None), (0.0, None)])
+def test_weights_with_any_scale_and_cap(scale, cap, d, g4):
+    check_weights(Batch([1, 40, 2, 150], [900, 300, 70, 1200], 8, 2, d, 16, g4=g4, seed=d), sm_scale=scale, soft_cap=cap)
+
+
+@pytest.mark.parametrize("g4", [False, True])
 def test_weights_of_many_sequences(g4):
     g = torch.Generator().manual_seed(5)
     q_lens = torch.randint(0, 3, (2500,), generator=g)
