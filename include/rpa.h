@@ -451,8 +451,9 @@ typedef struct {
     int32_t pages_per_seq;
     int32_t max_keys;            /* > 0, >= sinks + recent: places of slots_out a head */
     int32_t sinks;               /* >= 0: a sequence's first keys, which always stay */
-    int32_t recent;              /* >= 0: and its last ones */
+    int32_t recent;              /* >= 0: and its last ones: those in the last slots, or with positions those that came last */
     int32_t reserved;            /* 0 */
+    int32_t* positions;          /* when each key came (below), or NULL; a struct_size that ends before it counts as NULL */
 } rpa_evict_params;
 
 /* Leaves each sequence and KV head its budgets[i] keys of the largest weights, in the first slots of its pages.
@@ -469,7 +470,15 @@ typedef struct {
  * go, in theirs.  (A key's own position is in its rotation: attention over what is left is by rpa_forward without a
  * window, new tokens with `positions` of their own.)  Slots behind the new length keep what they hold.  No page may belong to two
  * sequences of the batch.  A sequence whose metadata is bad is left alone.  `workspace`: rpa_evict_workspace_size
- * bytes. */
+ * bytes.
+ *
+ * rpa_evict_params.positions: int32, as weights, written in place.  After one call the order of the slots is no longer the
+ * order in which the keys came, so a cache that is cut again and again gives positions: without them `recent` means the last
+ * slots, which hold the newest keys only until a call has moved some.  An entry below 0 (memset it all to -1 at first, and the
+ * entries of a page that another sequence gets) is a new key's: new keys get the numbers behind the greatest entry of
+ * their head, in the order of their slots, and keep them from then on; `recent` keys are those whose numbers are among the
+ * head's last `recent`.  The entries of slots that are left behind the new length become -1 again, so that tokens written there
+ * are new.  Entries of the caller's own (at most 2^30, different within a sequence's head) do as well. */
 RPA_API int rpa_evict_workspace_size(const rpa_evict_params* p, size_t* bytes);
 RPA_API int rpa_evict_kv_cache(const rpa_evict_params* p, void* kv_pages, const int32_t* kv_lens, const int32_t* page_indices,
                                const int32_t* num_seqs, const float* weights, const int32_t* budgets, int32_t* kv_lens_out,

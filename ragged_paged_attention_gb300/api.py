@@ -91,7 +91,7 @@ class rpa_evict_params(ctypes.Structure):
     _fields_ = [("struct_size", ctypes.c_uint32), ("version", ctypes.c_uint32), ("num_kv_heads", ctypes.c_int32),
                 ("row_bytes", ctypes.c_int32), ("total_num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("max_num_seqs", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32), ("max_keys", ctypes.c_int32),
-                ("sinks", ctypes.c_int32), ("recent", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+                ("sinks", ctypes.c_int32), ("recent", ctypes.c_int32), ("reserved", ctypes.c_int32), ("positions", ctypes.c_void_p)]
 
 
 ROPE_HALF, ROPE_INTERLEAVED, ROPE_MAX_DIM = 0, 1, 256
@@ -823,9 +823,9 @@ def _is_g4(kv_pages) -> bool:
     return isinstance(kv_pages, torch.Tensor) and kv_pages.dtype is torch.uint8
 
 
-def _page_weights(dev, t, name, kv_pages, hkv):
-    """Checks float32 weights [pages, Hkv, page_size] of a cache."""
-    _on(dev, t, name, torch.float32)
+def _page_weights(dev, t, name, kv_pages, hkv, dtype=torch.float32):
+    """Checks weights (or positions) [pages, Hkv, page_size] of a cache."""
+    _on(dev, t, name, dtype)
     want = (kv_pages.shape[0], hkv, kv_pages.shape[1])
     if tuple(t.shape) != want:
         raise ValueError(f"{name} must be {want}, got {tuple(t.shape)}")
@@ -908,10 +908,12 @@ def rpa_evict_workspace_size(params: rpa_evict_params) -> int:
 
 
 def rpa_evict_kv_cache(kv_pages, kv_lens, page_indices, num_seqs, weights, budgets, max_keys, *, sinks=0, recent=0,
-                       kv_lens_out=None, slots_out=None, weights_out=None, workspace=None):
+                       kv_lens_out=None, slots_out=None, weights_out=None, positions=None, workspace=None):
     """Leaves each sequence and KV head its ``budgets[i]`` (at most ``max_keys``) keys of the largest ``weights``
     (``rpa_key_weights``'s), its first ``sinks`` and last ``recent`` before all others, in the first slots of its pages;
-    writes ``kv_pages`` in place. Returns ``(kv_lens_out, slots_out)``: the new lengths (a new tensor where none is given;
+    writes ``kv_pages`` in place. ``positions`` (int32 [pages, Hkv, page_size], -1 throughout at first, written in place)
+    holds when each key came: with it ``recent`` means the keys that came last, call after call; without it the last
+    slots, which hold those only until a call has moved keys. Returns ``(kv_lens_out, slots_out)``: the new lengths (a new tensor where none is given;
     ``kv_lens`` itself works) and, int32 [max_num_seqs, Hkv, max_keys], the slot that each kept key had. ``weights_out``
     (``weights`` itself works) gets the kept keys' weights in their new slots."""
     lib = _lib or load_library()
@@ -920,7 +922,7 @@ def rpa_evict_kv_cache(kv_pages, kv_lens, page_indices, num_seqs, weights, budge
         with torch.cuda.device(dev):
             return rpa_evict_kv_cache(kv_pages, kv_lens, page_indices, num_seqs, weights, budgets, max_keys, sinks=sinks,
                                       recent=recent, kv_lens_out=kv_lens_out, slots_out=slots_out, weights_out=weights_out,
-                                      workspace=workspace)
+                                      positions=positions, workspace=workspace)
     if kv_pages.dim() != 4 or not kv_pages.is_contiguous():
         raise ValueError("kv_pages must be contiguous, [pages, page_size, heads, row]")
     _on(dev, page_indices, "page_indices", _I32)
@@ -934,6 +936,9 @@ def rpa_evict_kv_cache(kv_pages, kv_lens, page_indices, num_seqs, weights, budge
     _page_weights(dev, weights, "weights", kv_pages, hkv)
     if weights_out is not None:
         _page_weights(dev, weights_out, "weights_out", kv_pages, hkv)
+    if positions is not None:
+        _page_weights(dev, positions, "positions", kv_pages, hkv, _I32)
+        prm.positions = positions.data_ptr()
     if kv_lens_out is None:
         kv_lens_out = kv_lens.clone()
     _on(dev, kv_lens_out, "kv_lens_out", _I32, seqs)

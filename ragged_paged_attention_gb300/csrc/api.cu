@@ -951,7 +951,7 @@ int rpa_key_weights(const rpa_params* p, const void* q, const void* kv_pages, co
 
 static int check_evict_params(const rpa_evict_params* p) {
     if (!p) return fail(RPA_ERR_NULL, "params is NULL");
-    if (p->struct_size < sizeof(rpa_evict_params)) return fail(RPA_ERR_VALUE, "rpa_evict_params.struct_size too small");
+    if (p->struct_size < offsetof(rpa_evict_params, positions)) return fail(RPA_ERR_VALUE, "rpa_evict_params.struct_size too small");
     if (p->version != RPA_ABI_VERSION) return fail(RPA_ERR_VALUE, "rpa_evict_params.version %u != %d", p->version, RPA_ABI_VERSION);
     if (p->num_kv_heads <= 0 || p->row_bytes <= 0 || p->total_num_pages <= 0 || p->page_size <= 0 || p->max_num_seqs <= 0 ||
         p->pages_per_seq <= 0 || p->max_keys <= 0)
@@ -965,14 +965,18 @@ static int check_evict_params(const rpa_evict_params* p) {
     return RPA_OK;
 }
 
+// (Behind the fields that a caller built against the first form of the struct has.)
+static int32_t* evict_positions(const rpa_evict_params* p) { return p->struct_size >= sizeof(rpa_evict_params) ? p->positions : nullptr; }
+
 struct EvictLayout {
-    size_t kept, holes, total;
+    size_t kept, bases, holes, total;
 };
 
 static EvictLayout evict_layout(const rpa_evict_params* p) {
     EvictLayout L;
     L.kept = kWsHeaderBytes;
-    L.holes = align_up(L.kept + sizeof(int) * (size_t)p->max_num_seqs);
+    L.bases = align_up(L.kept + sizeof(int) * (size_t)p->max_num_seqs);
+    L.holes = align_up(L.bases + sizeof(long long) * (size_t)p->max_num_seqs * p->num_kv_heads);
     L.total = align_up(L.holes + sizeof(int) * (size_t)p->max_num_seqs * p->num_kv_heads * p->max_keys);
     return L;
 }
@@ -995,6 +999,11 @@ int rpa_evict_kv_cache(const rpa_evict_params* p, void* kv_pages, const int32_t*
     if (!aligned16(kv_pages)) return fail(RPA_ERR_VALUE, "kv_pages must be 16-byte aligned");
     if (slots_out == kv_lens || slots_out == page_indices || slots_out == budgets || slots_out == kv_lens_out || kv_lens_out == budgets)
         return fail(RPA_ERR_VALUE, "slots_out and kv_lens_out must not alias page_indices or budgets, nor slots_out kv_lens");
+    int32_t* const positions = evict_positions(p);
+    if (positions)
+        for (const void* x : {(const void*)kv_pages, (const void*)kv_lens, (const void*)page_indices, (const void*)num_seqs, (const void*)weights,
+                              (const void*)budgets, (const void*)kv_lens_out, (const void*)slots_out, (const void*)weights_out})
+            if (x == positions) return fail(RPA_ERR_VALUE, "positions must not alias another tensor");
     const EvictLayout L = evict_layout(p);
     rc = check_workspace(workspace, workspace_bytes, L.total);
     if (rc) return rc;
@@ -1020,7 +1029,9 @@ int rpa_evict_kv_cache(const rpa_evict_params* p, void* kv_pages, const int32_t*
     a.sinks = p->sinks;
     a.recent = p->recent;
     a.err = &reinterpret_cast<WsHeader*>(ws)->error_bits;
+    a.positions = positions;
     a.kept = reinterpret_cast<int*>(ws + L.kept);
+    a.bases = reinterpret_cast<long long*>(ws + L.bases);
     a.holes = reinterpret_cast<int*>(ws + L.holes);
     cudaError_t e = launch_evict(a, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "rpa_evict_kv_cache launch");

@@ -12,6 +12,10 @@
 // 48 sequences of 4000 to 12000 keys cut to 2048, 8 heads of 128 in bf16: selection 59 us (384 blocks, up to two an SM;
 // latencies of shared memory and barriers over five passes), moving 104 us (0.57 GB, rows of 512 bytes read and written
 // all over the pages: 5.4 TB/s), 155 us together.
+//
+// With positions (kernels of their own, so that calls without are as they were) a key's age is its number, not its slot: the
+// numbers of new keys go on behind the greatest in a head, each kept key takes its number along, and the `recent`
+// greatest come before all other keys.
 #include "common.cuh"
 #include "kernels.h"
 #include "profile.h"
@@ -65,16 +69,30 @@ __device__ __forceinline__ int evict_keep(const EvictArgs& a, int s, int& n) {
     return min(n, max(budget, a.sinks + a.recent));
 }
 
+// The number of slot i's key: its own, or, where it has none yet, the one that its place among the new keys gives it.
+__device__ __forceinline__ long long evict_number(const EvictArgs& a, size_t at, int i, long long base) {
+    const int p = a.positions[at];
+    return p < 0 ? base + i : p;
+}
+
+template <bool AGED>
 __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __grid_constant__ EvictArgs a) {
     extern __shared__ uint32_t held[];  // the keys' order, where they fit
     __shared__ int hist[kEvictBins];
     __shared__ long long scan[40];
     __shared__ int s_bad, s_digit, s_above;
+    [[maybe_unused]] __shared__ int s_greatest, s_first_new, s_last_new;
     const int s = blockIdx.x / a.num_kv_heads, h = blockIdx.x % a.num_kv_heads, tid = threadIdx.x;
     pdl_launch_dependents();  // (the moving kernel waits for this grid's end)
     int n = 0, keep = evict_keep(a, s, n);
     // every page of the sequence is one of the cache's, or the sequence is left alone
-    if (tid == 0) s_bad = 0;
+    if (tid == 0) {
+        s_bad = 0;
+        if constexpr (AGED) {
+            s_greatest = s_last_new = -1;
+            s_first_new = INT32_MAX;
+        }
+    }
     __syncthreads();
     if (keep >= 0) {
         const int pages = cdiv(n, a.page_size);
@@ -89,6 +107,34 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
         keep = -1;
     }
     if (h == 0 && tid == 0) a.kept[s] = keep;
+    auto index = [&](int i) { return evict_weight(a, evict_slot(a, s, i), h); };
+    [[maybe_unused]] long long base = 0, newest = 0;  // slot i's number where it is new, and the greatest of all
+    if constexpr (AGED) {
+        if (keep < 0) return;
+        int greatest = -1, first_new = INT32_MAX, last_new = -1;
+        for (int i = tid; i < n; i += kEvictThreads) {
+            const int p = a.positions[index(i)];
+            greatest = max(greatest, p);
+            if (p < 0) {
+                first_new = min(first_new, i);
+                last_new = i;
+            }
+        }
+        greatest = __reduce_max_sync(0xffffffffu, greatest);
+        first_new = __reduce_min_sync(0xffffffffu, first_new);
+        last_new = __reduce_max_sync(0xffffffffu, last_new);
+        if ((tid & 31) == 0) {
+            atomicMax(&s_greatest, greatest);
+            atomicMin(&s_first_new, first_new);
+            atomicMax(&s_last_new, last_new);
+        }
+        __syncthreads();
+        base = (long long)s_greatest + 1 - s_first_new;
+        newest = s_last_new >= 0 ? base + s_last_new : s_greatest;
+        if (tid == 0) a.bases[s * a.num_kv_heads + h] = base;
+        if (keep == 0)
+            for (int i = tid; i < n; i += kEvictThreads) a.positions[index(i)] = -1;
+    }
     if (keep <= 0) return;
     int* out = a.slots_out + ((size_t)s * a.num_kv_heads + h) * a.max_keys;
     if (keep == n) {
@@ -96,8 +142,13 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
         return;
     }
     auto order_of = [&](int i) -> uint32_t {
-        if (i < a.sinks || i >= n - a.recent) return 0xffffffffu;
-        return evict_order(a.weights[evict_weight(a, evict_slot(a, s, i), h)]);
+        if (i < a.sinks) return 0xffffffffu;
+        if constexpr (AGED) {
+            const size_t at = index(i);
+            return evict_number(a, at, i, base) > newest - a.recent ? 0xffffffffu : evict_order(a.weights[at]);
+        }
+        if (i >= n - a.recent) return 0xffffffffu;
+        return evict_order(a.weights[index(i)]);
     };
     const bool fits = n <= a.held;
     if (fits) {
@@ -181,12 +232,16 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
         const uint32_t v = order(i);
         const bool stays = v > top || (v == top && e < ties);
         e += v == top;
-        if (stays) out[hole_at[mover++]] = i;
+        if (stays)
+            out[hole_at[mover++]] = i;
+        else if constexpr (AGED)
+            a.positions[index(i)] = -1;  // (the slots of movers: by the thread that moves them)
     }
 }
 
 // A warp takes 32 slots of a head: their weights, a lane each, and the rows that come from elsewhere, 16 bytes a lane.
 constexpr int kMoveThreads = 128;  // (1 % less time than with 256)
+template <bool AGED>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs a, int blocks_per_head) {
     __shared__ const uint4* from[kMoveThreads];
     __shared__ uint4* to[kMoveThreads];
@@ -201,11 +256,19 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     const int src = i < keep ? a.slots_out[((size_t)s * a.num_kv_heads + h) * a.max_keys + i] : i;
     const bool moves = src != i;
     EvictSlot at = {0, 0}, at_src = {0, 0};
-    if (i < keep && (moves || a.weights_out)) {
+    if (i < keep && (moves || AGED || a.weights_out)) {
         at = evict_slot(a, s, i);
         at_src = moves ? evict_slot(a, s, src) : at;
     }
     if (i < keep && a.weights_out) a.weights_out[evict_weight(a, at, h)] = a.weights[evict_weight(a, at_src, h)];
+    if constexpr (AGED) {
+        if (i < keep) {
+            const size_t was = evict_weight(a, at_src, h);
+            const long long number = evict_number(a, was, src, a.bases[head]);
+            if (moves) a.positions[was] = -1;
+            a.positions[evict_weight(a, at, h)] = (int)min(number, (long long)INT32_MAX);
+        }
+    }
     const uint32_t mask = __ballot_sync(0xffffffffu, moves);
     if (moves) {
         const int k = w0 + __popc(mask & ((1u << lane) - 1));
@@ -231,14 +294,15 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     }
 }
 
-cudaError_t launch_evict(EvictArgs& a, cudaStream_t stream) {
+template <bool AGED>
+static cudaError_t launch_kernels(EvictArgs& a, cudaStream_t stream) {
     static bool configured[64] = {};  // (by device: the attribute is the device's)
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!configured[dev]) {
-        e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvictHeld * 4);
+        e = cudaFuncSetAttribute(evict_select_kernel<AGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvictHeld * 4);
         if (e != cudaSuccess) return e;
         configured[dev] = true;
     }
@@ -247,14 +311,18 @@ cudaError_t launch_evict(EvictArgs& a, cudaStream_t stream) {
     a.held = most <= kEvictHeld ? (int)most : 0;
     {
         ProfScope ps("rpa_evict_select", stream);
-        evict_select_kernel<<<a.max_num_seqs * a.num_kv_heads, kEvictThreads, a.held * 4, stream>>>(a);
+        evict_select_kernel<AGED><<<a.max_num_seqs * a.num_kv_heads, kEvictThreads, a.held * 4, stream>>>(a);
         e = cudaGetLastError();
     }
     if (e != cudaSuccess) return e;
     ProfScope ps("rpa_evict_move", stream);
     const int blocks = max(1, cdiv(a.max_keys, kMoveThreads));
-    return launch_pdl(evict_move_kernel, dim3((unsigned)a.max_num_seqs * a.num_kv_heads * blocks), dim3(kMoveThreads), 0, stream,
+    return launch_pdl(evict_move_kernel<AGED>, dim3((unsigned)a.max_num_seqs * a.num_kv_heads * blocks), dim3(kMoveThreads), 0, stream,
                       !prof_enabled(), a, blocks);
+}
+
+cudaError_t launch_evict(EvictArgs& a, cudaStream_t stream) {
+    return a.positions ? launch_kernels<true>(a, stream) : launch_kernels<false>(a, stream);
 }
 
 }  // namespace rpa

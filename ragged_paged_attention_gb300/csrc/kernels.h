@@ -320,6 +320,7 @@ struct EvictArgs {
     int32_t* kv_lens_out;           // may be kv_lens, or null
     int32_t* slots_out;             // [max_num_seqs, num_kv_heads, max_keys]
     float* weights_out;             // may be weights, or null
+    int32_t* positions;             // as weights, in place: the keys' numbers, below 0 for new ones; or null
     int num_kv_heads, row_bytes;    // row_bytes: a key's K and V of one head
     int total_num_pages, page_size, max_num_seqs, pages_per_seq, max_keys, sinks, recent;
     int held, page_shift;           // set by the launch: keys whose order a block holds in shared memory; log2 of a
@@ -327,6 +328,7 @@ struct EvictArgs {
     // workspace
     uint32_t* err;
     int* kept;                      // [max_num_seqs] keys that stay, -1: left alone
+    long long* bases;               // [max_num_seqs, num_kv_heads] with positions: a new key's number less its slot
     int* holes;                     // [max_num_seqs, num_kv_heads, max_keys]
 };
 
