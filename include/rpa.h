@@ -477,8 +477,9 @@ typedef struct {
  * slots, which hold the newest keys only until a call has moved some.  An entry below 0 (memset it all to -1 at first, and the
  * entries of a page that another sequence gets) is a new key's: new keys get the numbers behind the greatest entry of
  * their head, in the order of their slots, and keep them from then on; `recent` keys are those whose numbers are among the
- * head's last `recent`.  The entries of slots that are left behind the new length become -1 again, so that tokens written there
- * are new.  Entries of the caller's own (at most 2^30, different within a sequence's head) do as well. */
+ * head's last `recent`.  The entries of the slots from the new length to the old one become -1 again and their weights_out 0, so
+ * that tokens written there are new and start without weight (without positions those weights stay as they are, and
+ * rpa_key_weights would add to them).  Entries of the caller's own (at most 2^30, different within a sequence's head) do as well. */
 RPA_API int rpa_evict_workspace_size(const rpa_evict_params* p, size_t* bytes);
 RPA_API int rpa_evict_kv_cache(const rpa_evict_params* p, void* kv_pages, const int32_t* kv_lens, const int32_t* page_indices,
                                const int32_t* num_seqs, const float* weights, const int32_t* budgets, int32_t* kv_lens_out,

