@@ -430,7 +430,9 @@ RPA_API int rpa_g4_forward(const rpa_params* p, const void* q, const void* kv_pa
  *   weights, weights_out  float32 [total_num_pages, num_kv_heads, page_size]; weights_out may be weights; weights may
  *                         be NULL with keep 0, and is not read then
  * for every key of the batch's sequences (0 new weight where no query sees it); other entries are left as they are, as
- * are those of sequences without queries.  A slot that two sequences of a batch share gets either's.  kv_dtype is
+ * are those of sequences without queries.  Sequences of a batch may share pages only where weights_out is not weights (or keep
+ * is 0): a shared slot then gets one sequence's result.  In place one would read what another has written, and add to
+ * that, in some runs and not in others; nothing records it.  kv_dtype is
  * RPA_DTYPE_BF16 or RPA_DTYPE_G4, head_dim 64, 128 or 256, k_scale and v_scale 0, mask_value NaN.  Queries: a decode
  * step's, to add up over steps, or a prompt's last ones.  `workspace`: rpa_key_weights_workspace_size bytes,
  * up to half a GB of it for the scores of sequences of up to 16 query rows a KV head; those past it are computed twice. */
@@ -469,7 +471,7 @@ typedef struct {
  * Kept keys in the first slots stay where they are; the others move, in their order, to the slots of the keys that
  * go, in theirs.  (A key's own position is in its rotation: attention over what is left is by rpa_forward without a
  * window, new tokens with `positions` of their own.)  Slots behind the new length keep what they hold.  No page may belong to two
- * sequences of the batch.  A sequence whose metadata is bad is left alone.  `workspace`: rpa_evict_workspace_size
+ * sequences, be the other in the batch or not (its keys would move under it).  A sequence whose metadata is bad is left alone.  `workspace`: rpa_evict_workspace_size
  * bytes.
  *
  * rpa_evict_params.positions: int32, as weights, written in place.  After one call the order of the slots is no longer the

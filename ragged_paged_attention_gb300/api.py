@@ -843,7 +843,8 @@ def rpa_key_weights(q, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, wei
     """The attention that each cached key gets from the batch's queries, added up: ``weights_out`` = ``keep * weights`` + the sum of
     the softmax probabilities of the sequence's queries and the group's heads, float32 [pages, Hkv, page_size], at the
     slots of the batch's keys. Returns ``weights_out`` (``weights`` itself where none is given). The cache is bf16 or 4-bit
-    (``rpa_g4_update_kv_cache``'s)."""
+    (``rpa_g4_update_kv_cache``'s). Sequences that share pages need a ``weights_out`` of its own (a shared slot gets one
+    sequence's result there): in place one would add to what another has just written."""
     lib = _lib or load_library()
     dev = _cuda_index(q, "q")
     if dev != _current():
@@ -916,7 +917,8 @@ def rpa_evict_kv_cache(kv_pages, kv_lens, page_indices, num_seqs, weights, budge
     behind the new length get -1 and a ``weights_out`` of 0, for new tokens; without it ``recent`` means the last slots,
     which hold those only until a call has moved keys, and the weights left behind stay as they are. Returns ``(kv_lens_out, slots_out)``: the new lengths (a new tensor where none is given;
     ``kv_lens`` itself works) and, int32 [max_num_seqs, Hkv, max_keys], the slot that each kept key had. ``weights_out``
-    (``weights`` itself works) gets the kept keys' weights in their new slots."""
+    (``weights`` itself works) gets the kept keys' weights in their new slots. No page may belong to two sequences, inside the
+    batch or outside it: the other one's keys would move too."""
     lib = _lib or load_library()
     dev = _cuda_index(kv_pages, "kv_pages")
     if dev != _current():
