@@ -960,7 +960,7 @@ static int check_evict_params(const rpa_evict_params* p) {
     if (p->sinks < 0 || p->recent < 0 || (long long)p->sinks + p->recent > p->max_keys)
         return fail(RPA_ERR_VALUE, "sinks and recent must be positive and together at most max_keys");
     if ((long long)p->max_num_seqs * p->pages_per_seq > INT32_MAX || (long long)p->pages_per_seq * p->page_size > INT32_MAX ||
-        (long long)p->max_num_seqs * p->num_kv_heads * ((p->max_keys + 255) / 256) > INT32_MAX)
+        (long long)p->max_num_seqs * p->num_kv_heads * (((long long)p->max_keys + kEvictMoveThreads - 1) / kEvictMoveThreads) > INT32_MAX)
         return fail(RPA_ERR_SHAPE, "page table or slots_out too large");
     return RPA_OK;
 }

@@ -247,18 +247,17 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
 }
 
 // A warp takes 32 slots of a head: their weights, a lane each, and the rows that come from elsewhere, 16 bytes a lane.
-constexpr int kMoveThreads = 128;  // (1 % less time than with 256)
 template <bool AGED>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs a, int blocks_per_head) {
-    __shared__ const uint4* from[kMoveThreads];
-    __shared__ uint4* to[kMoveThreads];
+__global__ void __launch_bounds__(kEvictMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs a, int blocks_per_head) {
+    __shared__ const uint4* from[kEvictMoveThreads];
+    __shared__ uint4* to[kEvictMoveThreads];
     const int head = blockIdx.x / blocks_per_head, s = head / a.num_kv_heads, h = head % a.num_kv_heads;
     const int block = blockIdx.x % blocks_per_head, lane = threadIdx.x & 31, w0 = threadIdx.x & ~31;
     pdl_wait();
     const int keep = a.kept[s];
     if (keep < 0) return;
     if (a.kv_lens_out && h == 0 && block == 0 && threadIdx.x == 0) a.kv_lens_out[s] = keep;
-    const int i = block * kMoveThreads + threadIdx.x;
+    const int i = block * kEvictMoveThreads + threadIdx.x;
     if (i - lane >= keep) return;
     const int src = i < keep ? a.slots_out[((size_t)s * a.num_kv_heads + h) * a.max_keys + i] : i;
     const bool moves = src != i;
@@ -323,8 +322,8 @@ static cudaError_t launch_kernels(EvictArgs& a, cudaStream_t stream) {
     }
     if (e != cudaSuccess) return e;
     ProfScope ps("rpa_evict_move", stream);
-    const int blocks = max(1, cdiv(a.max_keys, kMoveThreads));
-    return launch_pdl(evict_move_kernel<AGED>, dim3((unsigned)a.max_num_seqs * a.num_kv_heads * blocks), dim3(kMoveThreads), 0, stream,
+    const int blocks = (a.max_keys - 1) / kEvictMoveThreads + 1;
+    return launch_pdl(evict_move_kernel<AGED>, dim3((unsigned)a.max_num_seqs * a.num_kv_heads * blocks), dim3(kEvictMoveThreads), 0, stream,
                       !prof_enabled(), a, blocks);
 }
 

@@ -44,3 +44,11 @@ def test_positions_alias_nothing(lib):
         assert lib.rpa_evict_kv_cache(ctypes.byref(p), *ptrs(9), ctypes.c_void_p(1 << 20), n.value, None) == -4
     p = params(positions=4096 * 10)  # (then the workspace is looked at)
     assert lib.rpa_evict_kv_cache(ctypes.byref(p), *ptrs(9), ctypes.c_void_p(1 << 20), n.value - 1, None) == -8
+
+
+@pytest.mark.parametrize("sizes,code", [(dict(max_num_seqs=32768, num_kv_heads=256, max_keys=38400), -2), (dict(max_num_seqs=32768, num_kv_heads=256, max_keys=32640), 0),
+                                        (dict(max_keys=2 ** 31 - 1), 0), (dict(max_num_seqs=128, max_keys=2 ** 31 - 1), -2)], ids=str)
+def test_more_blocks_than_a_grid_has_are_refused(lib, sizes, code):
+    # a block moves 128 keys of a head: a grid has at most 2^31 - 1 of them
+    p, n = params(**sizes), ctypes.c_size_t(0)
+    assert lib.rpa_evict_workspace_size(ctypes.byref(p), ctypes.byref(n)) == code
