@@ -5,7 +5,7 @@ import torch
 
 from long_context import BF16, Batch, row_bytes
 from ragged_paged_attention_gb300 import api
-from test_gpu_long_context import cache_rows, random_weights
+from test_gpu_long_context import cache_rows, check_evict, random_weights
 
 pytestmark = pytest.mark.gpu
 
@@ -93,6 +93,16 @@ def entries(b, kind, seed=0):
 def test_recent_keys_by_when_they_came(hkv, d, ps, g4, dtype, kind, in_place):
     b = Batch([0] * len(LENS), LENS, hkv, hkv, d, ps, g4=g4, dtype=dtype, seed=d)
     check(b, random_weights(b, d), BUDGETS, 1600, entries(b, kind, ps), sinks=2, recent=7, in_place=in_place)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("hkv,d,ps", [(4, 64, 16), (3, 96, 12), (2, 128, 16), (1, 192, 8), (2, 256, 1)])
+def test_int4_caches(hkv, d, ps, in_place):
+    # (a row is d / 2 bytes of K and as many of V)
+    b = Batch([0] * len(LENS), LENS, hkv, hkv, d // 2, ps, g4=False, dtype=torch.int8, seed=d)
+    b.kv = b.kv.view(torch.uint8)
+    check_evict(b, random_weights(b, d), BUDGETS, 1600, sinks=2, recent=7, in_place=in_place)
+    check(b, random_weights(b, d), BUDGETS, 1600, entries(b, "grown", d), sinks=2, recent=7, in_place=in_place)
 
 
 @pytest.mark.parametrize("sinks,recent", [(0, 0), (4, 0), (0, 64), (300, 300), (1, 1599)])
