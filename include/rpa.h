@@ -413,7 +413,8 @@ RPA_API int rpa_g4_read_kv_cache(const rpa_params* p, const void* kv_pages, cons
 /* rpa_forward over such a cache: the same arguments, masks and options (sliding_window, soft_cap, batch_kind).
  * `workspace`: rpa_g4_workspace_size bytes.  Sequences of more than 16 query rows a KV head see K rounded to bf16 and V
  * to f16, or to bf16 where a group of V that a tile of queries sees has s >= 4, |m| >= 2^20, or both s < 2^-9 and |m| < 2^-6
- * (the weights are rounded to the same type; prompts over such caches take up to twice as long). */
+ * (the weights are rounded to the same type; prompts over such caches take up to twice as long).  V in f16 is within 2^-11 of
+ * itself from 2^-4 on and within 2^-14 in all below; in bf16 within 2^-8 of itself. */
 RPA_API int rpa_g4_workspace_size(const rpa_params* p, size_t* bytes);
 RPA_API int rpa_g4_forward(const rpa_params* p, const void* q, const void* kv_pages, const int32_t* kv_lens,
                            const int32_t* page_indices, const int32_t* cu_q_lens, const int32_t* num_seqs, void* out,

@@ -102,10 +102,12 @@ __device__ __forceinline__ uint32_t f16x2_fma(uint32_t a, uint32_t b, uint32_t c
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
 }
-// V's panels and the P that meets them are f16 where an item's groups of V allow it: then their roundings
-// (2^-11 of a value at most, not bf16's 2^-8) count for nothing beside the output's own. A number alone is the f16 subnormal
-// n 2^-24 (or n 2^-20), and values are held times 2^-10: a group fits with s < 4 (s 2^14 is a factor), |m| < 2^20, and s >= 2^-9
-// or |m| >= 2^-6 (below that a value has no more bits than bf16 gives it), or as zeros. V's converters look at the groups on
+// V's panels and the P that meets them are f16 where an item's groups of V allow it. A number alone is the f16 subnormal
+// n 2^-24 (or n 2^-20), and values are held times 2^-10: within 2^-11 of themselves from 2^-4 on (bf16: 2^-8), and below that,
+// as f16 subnormals, within 2^-15 (twice that where |m| < 2^-7, since m is rounded first). A group fits with s < 4 (s 2^14 is a
+// factor), |m| < 2^20, and s >= 2^-9 or |m| >= 2^-6, or as zeros. At the least s a step of f16 is s / 32, beside the s that the
+// cache rounds to, and outputs are as near as with bf16: 2.85e-3 of themselves with s from 2^-9 to 1.5 2^-9 about zero, 2.8e-3
+// in bf16 just below, 2.2e-3 with s from 2^-8 on (1.6e-3 are the outputs' own rounding). V's converters look at the groups on
 // their way; an item in which one does not fit is done again with bf16 (2^-53 of V, 2^43 of P: the same 2^-10), which
 // makes such a cache's prompts twice as long. (Looked at block by block before its V is turned: 4 x 4096 prompts 552 us, not 497.)
 constexpr float kDownV = 0x1p-10f;
