@@ -413,7 +413,7 @@ RPA_API int rpa_g4_read_kv_cache(const rpa_params* p, const void* kv_pages, cons
 /* rpa_forward over such a cache: the same arguments, masks and options (sliding_window, soft_cap, batch_kind).
  * `workspace`: rpa_g4_workspace_size bytes.  Sequences of more than 16 query rows a KV head see K rounded to bf16 and V
  * to f16, or to bf16 where a group of V that a tile of queries sees has s >= 4, |m| >= 2^20, or both s < 2^-9 and |m| < 2^-6
- * (the weights are rounded to the same type; prompts over such caches take up to twice as long).  V in f16 is within 2^-11 of
+ * (the weights are rounded to the same type; prompts over such caches take up to twice as long).  V in f16 is within 2^-10 of
  * itself from 2^-4 on and within 2^-14 in all below; in bf16 within 2^-8 of itself. */
 RPA_API int rpa_g4_workspace_size(const rpa_params* p, size_t* bytes);
 RPA_API int rpa_g4_forward(const rpa_params* p, const void* q, const void* kv_pages, const int32_t* kv_lens,
@@ -434,8 +434,8 @@ RPA_API int rpa_g4_forward(const rpa_params* p, const void* q, const void* kv_pa
  * are those of sequences without queries.  Sequences of a batch may share pages only where weights_out is not weights (or keep
  * is 0): a shared slot then gets one sequence's result.  In place one would read what another has written, and add to
  * that, in some runs and not in others; nothing records it.  kv_dtype is
- * RPA_DTYPE_BF16 or RPA_DTYPE_G4, head_dim 64, 128 or 256, k_scale and v_scale 0, mask_value NaN.  Queries: a decode
- * step's, to add up over steps, or a prompt's last ones.  `workspace`: rpa_key_weights_workspace_size bytes,
+ * RPA_DTYPE_BF16 or RPA_DTYPE_G4, head_dim 64, 128 or 256, k_scale and v_scale 0, mask_value NaN; batch_kind is not
+ * looked at.  Queries: a decode step's, to add up over steps, or a prompt's last ones.  `workspace`: rpa_key_weights_workspace_size bytes,
  * up to half a GB of it for the scores of sequences of up to 16 query rows a KV head; those past it are computed twice. */
 RPA_API int rpa_key_weights_workspace_size(const rpa_params* p, size_t* bytes);
 RPA_API int rpa_key_weights(const rpa_params* p, const void* q, const void* kv_pages, const int32_t* kv_lens,
@@ -472,7 +472,7 @@ typedef struct {
  * Kept keys in the first slots stay where they are; the others move, in their order, to the slots of the keys that
  * go, in theirs.  (A key's own position is in its rotation: attention over what is left is by rpa_forward without a
  * window, new tokens with `positions` of their own.)  Slots behind the new length keep what they hold.  No page may belong to two
- * sequences, be the other in the batch or not (its keys would move under it).  A sequence whose metadata is bad is left alone.  `workspace`: rpa_evict_workspace_size
+ * sequences, be the other in the batch or not (its keys would move under it), nor twice to one.  A sequence whose metadata is bad is left alone.  `workspace`: rpa_evict_workspace_size
  * bytes.
  *
  * rpa_evict_params.positions: int32, as weights, written in place.  After one call the order of the slots is no longer the

@@ -9,8 +9,8 @@
 // Selection: weights as integers of their order, the keep-th largest found 11 bits at a time from histograms in
 // shared memory, then one pass that counts and one that places, each thread on a run of consecutive slots.
 //
-// 48 sequences of 4000 to 12000 keys cut to 2048, 8 heads of 128 in bf16: selection 59 us (384 blocks, up to two an SM;
-// latencies of shared memory and barriers over five passes), moving 104 us (0.57 GB, rows of 512 bytes read and written
+// 48 sequences of 4000 to 12000 keys cut to 2048, 8 heads of 128 in bf16: selection 59 us (384 blocks, one an SM: 53
+// registers by 1024 threads; latencies of shared memory and barriers over five passes), moving 104 us (0.57 GB, rows of 512 bytes read and written
 // all over the pages: 5.4 TB/s), 155 us together.
 //
 // With positions (kernels of their own, so that calls without are as they were) a key's age is its number, not its slot: the
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __gri
             if (pass == 0 || v >> width == top) atomicAdd(&hist[v >> shift & ((1u << bits) - 1)], 1);
         }
         __syncthreads();
-        // bins from the greatest down, four a thread: the one where the count passes keep
+        // bins from the greatest down, two a thread: the one where the count passes keep
         constexpr int kPer = kEvictBins / kEvictThreads;
         int c[kPer], sum = 0;
 #pragma unroll

@@ -75,7 +75,7 @@ __device__ __forceinline__ uint32_t g4_params(uint32_t extremes) {
 // with s's float32 reciprocal would fall on either side.  The reciprocal as a sum of two floats (Brisebarre and
 // Muller, "Correctly rounded multiplication by arbitrary precision constants", 2008) gives a quotient within 2^-46 of
 // itself before its one rounding, so one that is a float comes out exactly: 16 instructions a pair of values became 10 (4 x
-// 4096 tokens of 32 + 8 + 8 heads of 128: 97 us, with divisions 137).  Adding 2^23 then rounds to nearest even, and leaves the
+// 4096 tokens of 32 + 8 + 8 heads of 128: 97 us, with divisions 137; 87 now in a graph).  Adding 2^23 then rounds to nearest even, and leaves the
 // number in the low bits.
 __device__ __forceinline__ uint32_t g4_numbers(const uint4& x, uint32_t sm) {
     const float s = bf16_lo(sm), m = bf16_hi(sm);

@@ -553,7 +553,8 @@ static cudaError_t dispatch(const RpaArgs& a, int num_sms, cudaStream_t stream, 
         case 64: return launch_dec<64, 4>(a, num_sms, stream, per_sm_out);
         case 128: return launch_dec<128, 4>(a, num_sms, stream, per_sm_out);
         // Two heads a CTA leave four warps an SM that compute (64 decodes that see 1024 to 4096 keys of 8 heads, with a
-        // soft cap: 180 us; four heads a CTA 128), but half of four would idle where a cache has two heads.
+        // soft cap: 180 us; four heads a CTA 128, although 118 bytes of their 168 registers a thread spill), but half of four would
+        // idle where a cache has two heads.
         case 256: return a.decode_heads == 4 ? launch_dec<256, 4>(a, num_sms, stream, per_sm_out) : launch_dec<256, 2>(a, num_sms, stream, per_sm_out);
         default: return cudaErrorInvalidValue;
     }

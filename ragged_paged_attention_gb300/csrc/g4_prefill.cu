@@ -15,8 +15,8 @@
 // Barriers, all waits bounded: raw_full/empty, k/v_full, k/v_empty (panels), q_full, q_empty, item_full/empty; per tile
 // s_full (QK done), s_free (scores loaded), and P buffer p_full (P written, O rescaled) and pv_done; per tile o_empty.
 //
-// What bounds it: the prompts' products alone would take 285 us at cuBLAS's rate where 4 x 4096 tokens over 8192 keys (32 heads of
-// 128, 8 KV heads) take 497: a block's softmax (64 exponentials a row, on one of four quarters of the SM) and the conversions
+// What bounds it: the prompts' products alone would take 285 us at cuBLAS's rate where 4 x 4096 tokens over their own 4096 keys (32
+// heads of 128, 8 KV heads) take 519 in a graph: a block's softmax (64 exponentials a row, on one of four quarters of the SM) and the conversions
 // (26 cycles of such a quarter for 8 numbers of 32 rows of K, 18 of V) each take about as long as the
 // products, share the issue slots, and read or write shared memory beside the tensor pipe. Without the conversions: 478 us.
 // 128-key blocks had 387 without them, but no room for raw rows by tensor copies. With a soft cap and a window of 4096, 2 x
@@ -104,12 +104,12 @@ __device__ __forceinline__ uint32_t f16x2_fma(uint32_t a, uint32_t b, uint32_t c
 }
 // V's panels and the P that meets them are f16 where an item's groups of V allow it. A number alone is the f16 subnormal
 // n 2^-24 (or n 2^-20), and values are held times 2^-10: within 2^-11 of themselves from 2^-4 on (bf16: 2^-8), and below that,
-// as f16 subnormals, within 2^-15 (twice that where |m| < 2^-7, since m is rounded first). A group fits with s < 4 (s 2^14 is a
+// as f16 subnormals, within 2^-15 (twice either where |m| < 2^-7, since m is rounded first). A group fits with s < 4 (s 2^14 is a
 // factor), |m| < 2^20, and s >= 2^-9 or |m| >= 2^-6, or as zeros. At the least s a step of f16 is s / 32, beside the s that the
 // cache rounds to, and outputs are as near as with bf16: 2.85e-3 of themselves with s from 2^-9 to 1.5 2^-9 about zero, 2.8e-3
 // in bf16 just below, 2.2e-3 with s from 2^-8 on (1.6e-3 are the outputs' own rounding). V's converters look at the groups on
 // their way; an item in which one does not fit is done again with bf16 (2^-53 of V, 2^43 of P: the same 2^-10), which
-// makes such a cache's prompts twice as long. (Looked at block by block before its V is turned: 4 x 4096 prompts 552 us, not 497.)
+// makes such a cache's prompts twice as long (4 x 4096 tokens 1016 us, not 519; one key of small V that all see is enough). (Looked at block by block before its V is turned: 4 x 4096 prompts 552 us, not 497.)
 constexpr float kDownV = 0x1p-10f;
 // P and l are held times 2^7: at most 2^15 (the reference maximum may lag by 2^8), and f16 keeps 8 bits of weights down to
 // 2^-24 of a row's greatest (behind a first key of nearly all the weight and hardly any value, the others count).

@@ -10,7 +10,8 @@
 // HBM brings in some 700: both kernels are bound by reading K where a sequence has one tile, by the exponentials where
 // it has many. 8 windows of 32 queries over 8000-16000 keys, 32/8 heads of 128: STATS 45 us, SUM 53 (185 MB of K each: 4.1
 // and 3.5 TB/s with one tile in flight an SM); 16 rows at a time on mma.sync 252 and 326 us. With a soft cap
-// (tanhf) 102 and 137 us, 401 and 464 there. Scores are exact products summed in float32; maxima, sums and L are float32.
+// (tanhf) 102 and 137 us, 401 and 464 there. A block's 128 scores a thread fill the registers: of 168, SUM spills 16 bytes, with
+// the cap's 128 unrolled tanhf 168 (STATS 56). Scores are exact products summed in float32; maxima, sums and L are float32.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
