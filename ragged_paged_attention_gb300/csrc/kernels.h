@@ -142,7 +142,6 @@ struct RpaArgs {
     int overlap;                // run prefill beside decode (off while kernels are timed one by one)
     float pre_flops_per_ns_sm;  // prefill kernel rate per SM (this head size and cache type)
     float dec_bytes_per_ns_sm;  // decode kernel rate per SM while SMs, not HBM, limit it
-    float dec_hbm_bytes_per_ns; // and with HBM saturated
     int item_cost_keys;         // per-group cost on the decode line (a multiple of 16 keys)
     int min_chunk;              // smallest static decode share (a multiple of 16 above item_cost_keys)
     // workspace
@@ -154,6 +153,7 @@ struct RpaArgs {
     float* partial_ml;
     float* partial_o;
     int max_dec_items, max_pre_items;
+    float dec_hbm_bytes_per_ns; // decode kernel's rate with HBM saturated (the 4-bit cache's plan reads it, kDecHbmBytesPerNs elsewhere)
 };
 
 struct RpaUpdateArgs {

@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSm) rpa_rope_updat
     // not write, and it ends after this grid has
     pdl_launch_dependents();
     __shared__ int cu[kRopeCu];
-    auto resolve = [&](int t0, int nt) { rope_slots(a, t0, nt, cu, sh.pos, sh.slot); };
+    auto resolve = [&](int t0, int nt) { rope_slots<kRopeThreads>(a, t0, nt, cu, sh.pos, sh.slot); };
     unsigned share = blockIdx.x;
     if (share < a.q_share.blocks) {
         rope_block<true, INTER>(
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kG4ReadThreads) rpa_g4_read_kernel(const __gri
     __shared__ int cu[kRopeCu], pos[kRopeTokens];
     __shared__ uint8_t* slot[kRopeTokens];
     const int t0 = blockIdx.x * tokens, nt = min(tokens, a.max_num_tokens - t0);
-    rope_slots(a, t0, nt, cu, pos, slot);
+    rope_slots<kG4ReadThreads>(a, t0, nt, cu, pos, slot);
     __syncthreads();
     const int d = a.head_dim, lg = d == 64 ? 5 : 6, per_head = d / 16, per_part = a.num_kv_heads * per_head;
     for (int i = threadIdx.x; i < nt * 2 * per_part; i += kG4ReadThreads) {

@@ -182,11 +182,12 @@ __device__ __forceinline__ bool rope_slot(const RopeUpdateArgs& a, int t, int& p
 // cu: kRopeCu ints of shared memory.  Behind it a barrier.
 constexpr int kRopeCu = 1024;
 constexpr int kRopeTokens = 32;     // most tokens of a block
+template <int kThreads>
 __device__ __forceinline__ void rope_slots(const RopeUpdateArgs& a, int t0, int nt, int* cu, int* pos_of, uint8_t** slot_of) {
     if (a.max_num_seqs < kRopeCu) {
         // all of cu_q_lens in one round trip, then a token a thread: two more for all of them (a warp a
         // token took four or five, again for every eight tokens: 4 x 4096 tokens 74.0 us, now 70.5)
-        for (int i = threadIdx.x; i <= a.max_num_seqs; i += blockDim.x) cu[i] = a.cu_q_lens[i];
+        for (int i = threadIdx.x; i <= a.max_num_seqs; i += kThreads) cu[i] = a.cu_q_lens[i];
         const int num = a.num_seqs[0];
         const bool some = num > 0 && num <= a.max_num_seqs;
         if (!some && num != 0 && t0 == 0 && threadIdx.x == 0) set_error(a.err, RPA_DEV_ERR_NUM_SEQS);
@@ -206,7 +207,7 @@ __device__ __forceinline__ void rope_slots(const RopeUpdateArgs& a, int t0, int 
         }
         return;
     }
-    for (int k = threadIdx.x >> 5; k < nt; k += blockDim.x >> 5) {  // a warp a token
+    for (int k = threadIdx.x >> 5; k < nt; k += kThreads / 32) {  // a warp a token
         int pos = 0;
         uint8_t* slot = nullptr;
         if (!rope_slot(a, t0 + k, pos, slot)) slot = nullptr;

@@ -28,7 +28,9 @@ namespace rpa {
 // finishes last). Equal shares remove the tail a queue of long items leaves (a few CTAs
 // finishing while the rest of the GPU idles); the pool evens out CTAs that stream faster
 // than others.
-__device__ __forceinline__ void plan_body(const RpaArgs& a) {
+// rows: of a prefill item; hbm: the decode kernel's rate with HBM saturated. (Read from the arguments in every plan, the one beside the update
+// spilled 28 bytes, as it does with both as template parameters, and the mixed step of rpa_rope_forward_update took 1.4 us of 221 more.)
+__device__ __forceinline__ void plan_body(const RpaArgs& a, int rows = kPrefillRows, float hbm = kDecHbmBytesPerNs) {
     __shared__ long long scan_ll[40];
     __shared__ long long red[32], red_g[32];
     __shared__ float red_f[32];
@@ -135,7 +137,7 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
         if (tid + 1 < S) {
             nn = tid + 1;
             const float tp = pre_flops / (a.pre_flops_per_ns_sm * (float)nn);
-            const float td = dec_bytes / fminf(a.dec_hbm_bytes_per_ns, a.dec_bytes_per_ns_sm * (float)(S - nn));
+            const float td = dec_bytes / fminf(hbm, a.dec_bytes_per_ns_sm * (float)(S - nn));
             tt = fmaxf(tp, td);
         }
         for (int o = 16; o > 0; o >>= 1) {
@@ -177,7 +179,7 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
             n_pre = 0;
         } else if (a.overlap && dec_bytes > 0.f && S > 1) {
             const float serial = pre_flops / (a.pre_flops_per_ns_sm * (float)S) +
-                                 dec_bytes / fminf(a.dec_hbm_bytes_per_ns, a.dec_bytes_per_ns_sm * (float)S);
+                                 dec_bytes / fminf(hbm, a.dec_bytes_per_ns_sm * (float)S);
             if (bt < 0.9f * serial) n_pre = bn;
         }
         hdr->prefill_ctas = n_pre;
@@ -249,7 +251,7 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
                 nrh = cdiv(ql * G, kDecodeRows);
                 wk = (round_bk(kl - klo) + a.item_cost_keys) * n_groups * nrh;
             } else {
-                np = cdiv(ql * G, a.prefill_rows) * a.num_kv_heads;
+                np = cdiv(ql * G, rows) * a.num_kv_heads;
             }
         }
         long long tot_w;
@@ -338,7 +340,7 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
             WorkItem w;
             w.seq = s0 + k;
             w.head = h;
-            w.row_begin = r * a.prefill_rows;
+            w.row_begin = r * rows;
             w.key_begin = 0;
             w.key_end = e_kl[k];
             w.first_item = it;
@@ -365,6 +367,8 @@ __device__ __forceinline__ void plan_body(const RpaArgs& a) {
 }
 
 __global__ void __launch_bounds__(1024) rpa_plan_kernel(RpaArgs a) { plan_body(a); }
+// for the 4-bit cache's kernels
+__global__ void __launch_bounds__(1024) rpa_g4_plan_kernel(RpaArgs a) { plan_body(a, a.prefill_rows, a.dec_hbm_bytes_per_ns); }
 
 // Zero rows of cross attention's sequences without keys (which the plans leave out), by the blocks
 // beside the plan's. They wait for the stream's earlier work first: it may still use `out`, or be
@@ -725,7 +729,7 @@ cudaError_t launch_g4_forward(const RpaArgs& a, int num_sms, cudaStream_t stream
     cudaError_t e;
     {
         ProfScope ps("rpa_plan", stream);
-        e = launch_pdl(rpa_plan_kernel, dim3(1), dim3(1024), 0, stream, a.overlap != 0, a);
+        e = launch_pdl(rpa_g4_plan_kernel, dim3(1), dim3(1024), 0, stream, a.overlap != 0, a);
     }
     if (e != cudaSuccess) return e;
     if (a.batch_kind == RPA_BATCH_DECODE_ONLY) {
