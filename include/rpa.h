@@ -478,7 +478,7 @@ typedef struct {
  * rpa_evict_params.positions: int32, as weights, written in place.  After one call the order of the slots is no longer the
  * order in which the keys came, so a cache that is cut again and again gives positions: without them `recent` means the last
  * slots, which hold the newest keys only until a call has moved some.  An entry below 0 (memset it all to -1 at first, and the
- * entries of a page that another sequence gets) is a new key's: new keys get the numbers behind the greatest entry of
+ * entries of a page that another sequence gets, whose weights are 0 then, too) is a new key's: new keys get the numbers behind the greatest entry of
  * their head, in the order of their slots, and keep them from then on; `recent` keys are those whose numbers are among the
  * head's last `recent`.  The entries of the slots from the new length to the old one become -1 again and their weights_out 0, so
  * that tokens written there are new and start without weight (without positions those weights stay as they are, and
